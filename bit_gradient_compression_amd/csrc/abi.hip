@@ -6,10 +6,12 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <vector>
 
 #include "loco.h"
 #include "loco_internal.hpp"
+#include "loco_layer_internal.hpp"
 
 #define LOCO_API extern "C" __attribute__((visibility("default")))
 
@@ -61,7 +63,7 @@ constexpr int64_t kMaxElems = (int64_t)1 << 52;
 
 using namespace loco;
 
-LOCO_API int loco_version(void) { return 10100; }
+LOCO_API int loco_version(void) { return 10200; }
 
 LOCO_API const char* loco_status_string(int status) {
     switch (status) {
@@ -366,5 +368,307 @@ LOCO_API int loco_sparse_aggregate(const loco_sparse_payload_t* peers, int npeer
     p.out_scale = out_scale;
     p.out = out;
     if (launch_sa(p, chunk, bits, out_dtype == LOCO_BF16, (hipStream_t)stream) != hipSuccess) return LOCO_ERR_HIP;
+    return LOCO_OK;
+}
+
+// ---- layer operators --------------------------------------------------------------------
+
+namespace loco {
+
+namespace {
+
+bool act_ok(int a) { return a >= LOCO_ACT_NONE && a <= LOCO_ACT_SILU; }
+int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// One buffer of a call.  `needed`: a null pointer is an error (of an empty buffer it is not).
+struct Buf {
+    const void* p;
+    int64_t bytes;
+    bool written, needed;
+};
+
+int check_bufs(std::initializer_list<Buf> bufs) {
+    for (const Buf& b : bufs)
+        if (b.needed && b.bytes > 0 && !b.p) return LOCO_ERR_INVALID;
+    for (const Buf& b : bufs)
+        if (b.p && b.bytes > 0 && !aligned16(b.p)) return LOCO_ERR_ALIGN;
+    // no buffer that is written may overlap another buffer of the call
+    for (const Buf& a : bufs)
+        for (const Buf& b : bufs) {
+            if (&a == &b || !a.written || !a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) continue;
+            if (overlap(range_of(a.p, a.bytes), range_of(b.p, b.bytes))) return LOCO_ERR_INVALID;
+        }
+    return LOCO_OK;
+}
+
+// Rows and columns whose product, in bytes, fits far inside 64 bits.
+bool sizes_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && cols >= 0 && rows <= ((int64_t)1 << 40) && cols <= ((int64_t)1 << 40) &&
+           (cols == 0 || rows <= ((int64_t)1 << 52) / cols);
+}
+
+int check_ckpt(const loco_checkpoint_t& c) {
+    if (c.block < 1) return LOCO_ERR_INVALID;
+    return c.block == 32 || c.block == 64 ? LOCO_OK : LOCO_ERR_UNSUPPORTED;
+}
+CkptDev ckpt_dev(const loco_checkpoint_t* c, int64_t cols) {
+    if (!c) return {nullptr, nullptr, 0, 0};
+    return {c->codes, c->exps, c->block == 64, nblocks(cols, c->block)};
+}
+Buf codes_buf(const loco_checkpoint_t* c, int64_t rows, int64_t cols, bool written) {
+    return {c ? c->codes : nullptr, c ? rows * cols : 0, written, true};
+}
+Buf exps_buf(const loco_checkpoint_t* c, int64_t rows, int64_t cols, bool written) {
+    return {c ? c->exps : nullptr, c ? rows * nblocks(cols, c->block) : 0, written, true};
+}
+
+int hip_status(hipError_t e) { return e == hipSuccess ? LOCO_OK : LOCO_ERR_HIP; }
+
+// Features of a product: counts that the tile kernels' 32-bit offsets hold.
+int check_product(int64_t rows, int64_t out_features, int64_t in_features) {
+    if (out_features < 0 || in_features < 0) return LOCO_ERR_INVALID;
+    if (!sizes_ok(rows, out_features) || !sizes_ok(rows, in_features)) return LOCO_ERR_INVALID;
+    constexpr int64_t kMost = (int64_t)1 << 36;  // elements of one matrix: a grid holds the tiles of as many
+    const int64_t widest = std::max(out_features, in_features);
+    if (widest > kMmMaxFeatures || rows > ((int64_t)1 << 28) || rows * widest > kMost ||
+        out_features * in_features > kMost)
+        return LOCO_ERR_UNSUPPORTED;
+    return LOCO_OK;
+}
+
+int64_t mm_part_bytes(int64_t m, int64_t n, int64_t k) {
+    const int s = mm_splits(m, n, k);
+    return s > 1 ? round16((int64_t)s * m * n * 4) : 0;
+}
+
+}  // namespace
+}  // namespace loco
+
+LOCO_API int loco_layer_norm(const void* x, loco_dtype_t dtype, const void* weight, const void* bias,
+                             loco_dtype_t param_dtype, int64_t rows, int64_t cols, float eps, void* y, float* mean,
+                             float* rstd, const loco_checkpoint_t* ckpt, void* stream) {
+    if (!sizes_ok(rows, cols) || cols < 1) return LOCO_ERR_INVALID;
+    if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return LOCO_ERR_INVALID;
+    if (!isfinite(eps) || eps < 0.0f) return LOCO_ERR_INVALID;
+    if (ckpt) {
+        const int st = check_ckpt(*ckpt);
+        if (st != LOCO_OK) return st;
+    }
+    if (cols > kLnMaxCols) return LOCO_ERR_UNSUPPORTED;
+    if (rows == 0) return LOCO_OK;
+    const int64_t s = dtype_size(dtype), ps = dtype_size(param_dtype);
+    const int st = check_bufs({{x, rows * cols * s, false, true},
+                               {weight, cols * ps, false, false},
+                               {bias, cols * ps, false, false},
+                               {y, rows * cols * s, true, true},
+                               {mean, rows * 4, true, true},
+                               {rstd, rows * 4, true, true},
+                               codes_buf(ckpt, rows, cols, true),
+                               exps_buf(ckpt, rows, cols, true)});
+    if (st != LOCO_OK) return st;
+    LnParams p = {x, weight, bias, y, mean, rstd, ckpt_dev(ckpt, cols), rows, (int)cols, eps,
+                  dtype == LOCO_F32, param_dtype == LOCO_F32};
+    return hip_status(launch_ln(p, (hipStream_t)stream));
+}
+
+LOCO_API int64_t loco_layer_norm_backward_workspace(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 1 || cols > kLnMaxCols) return 0;
+    return ln_bwd_groups(rows, cols) * 2 * cols * 4;
+}
+
+LOCO_API int loco_layer_norm_backward(const void* dy, const void* x, loco_dtype_t dtype, const void* weight,
+                                      loco_dtype_t param_dtype, const float* mean, const float* rstd,
+                                      const void* residual, int64_t rows, int64_t cols, void* dx, void* dweight,
+                                      void* dbias, loco_dtype_t grad_dtype, void* workspace, int64_t workspace_bytes,
+                                      void* stream) {
+    if (!sizes_ok(rows, cols) || cols < 1) return LOCO_ERR_INVALID;
+    if (!dtype_ok(dtype) || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return LOCO_ERR_INVALID;
+    if (cols > kLnMaxCols) return LOCO_ERR_UNSUPPORTED;
+    const bool sums = dweight || dbias;
+    const int64_t need = sums ? loco_layer_norm_backward_workspace(rows, cols) : 0;
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    if (rows == 0 && !sums) return LOCO_OK;
+    const int64_t s = dtype_size(dtype), gs = dtype_size(grad_dtype);
+    const int st = check_bufs({{dy, rows * cols * s, false, true},
+                               {x, rows * cols * s, false, true},
+                               {weight, cols * dtype_size(param_dtype), false, false},
+                               {mean, rows * 4, false, true},
+                               {rstd, rows * 4, false, true},
+                               {residual, rows * cols * s, false, false},
+                               {dx, rows * cols * s, true, true},
+                               {dweight, cols * gs, true, false},
+                               {dbias, cols * gs, true, false},
+                               {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    LnBwdParams p = {dy, x, weight, mean, rstd, residual, dx, dweight, dbias, sums ? (float*)workspace : nullptr,
+                     rows, (int)cols, dtype == LOCO_F32, param_dtype == LOCO_F32, grad_dtype == LOCO_F32};
+    return hip_status(launch_ln_bwd(p, (hipStream_t)stream));
+}
+
+LOCO_API int loco_checkpoint_write(const void* x, loco_dtype_t dtype, int64_t rows, int64_t cols,
+                                   const loco_checkpoint_t* ckpt, void* stream) {
+    if (!ckpt || !sizes_ok(rows, cols) || !dtype_ok(dtype)) return LOCO_ERR_INVALID;
+    int st = check_ckpt(*ckpt);
+    if (st != LOCO_OK) return st;
+    if (rows == 0 || cols == 0) return LOCO_OK;
+    st = check_bufs({{x, rows * cols * dtype_size(dtype), false, true},
+                     codes_buf(ckpt, rows, cols, true),
+                     exps_buf(ckpt, rows, cols, true)});
+    if (st != LOCO_OK) return st;
+    return hip_status(launch_ckpt_write(x, dtype == LOCO_F32, rows, cols, ckpt_dev(ckpt, cols), (hipStream_t)stream));
+}
+
+LOCO_API int loco_checkpoint_read(const loco_checkpoint_t* ckpt, int64_t rows, int64_t cols, loco_act_t act, void* out,
+                                  loco_dtype_t out_dtype, void* stream) {
+    if (!ckpt || !sizes_ok(rows, cols) || !dtype_ok(out_dtype) || !act_ok(act)) return LOCO_ERR_INVALID;
+    int st = check_ckpt(*ckpt);
+    if (st != LOCO_OK) return st;
+    if (rows == 0 || cols == 0) return LOCO_OK;
+    st = check_bufs({{out, rows * cols * dtype_size(out_dtype), true, true},
+                     codes_buf(ckpt, rows, cols, false),
+                     exps_buf(ckpt, rows, cols, false)});
+    if (st != LOCO_OK) return st;
+    return hip_status(
+        launch_ckpt_read(ckpt_dev(ckpt, cols), rows, cols, act, out, out_dtype == LOCO_F32, (hipStream_t)stream));
+}
+
+LOCO_API int64_t loco_linear_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
+    if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
+    return mm_part_bytes(rows, out_features, in_features);
+}
+
+LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16_t* bias, const uint16_t* residual,
+                         int64_t rows, int64_t out_features, int64_t in_features, loco_act_t act, void* out,
+                         loco_dtype_t out_dtype, const loco_checkpoint_t* ckpt, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+    if (!act_ok(act) || !dtype_ok(out_dtype)) return LOCO_ERR_INVALID;
+    int st = ckpt ? check_ckpt(*ckpt) : LOCO_OK;
+    if (st != LOCO_OK) return st;
+    st = check_product(rows, out_features, in_features);
+    if (st != LOCO_OK) return st;
+    if (rows == 0 || out_features == 0) return LOCO_OK;
+    const int64_t n = out_features, k = in_features, need = loco_linear_workspace(rows, n, k);
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    st = check_bufs({{x, rows * k * 2, false, true},
+                     {weight, n * k * 2, false, true},
+                     {bias, n * 2, false, false},
+                     {residual, rows * n * 2, false, false},
+                     {out, rows * n * dtype_size(out_dtype), true, true},
+                     codes_buf(ckpt, rows, n, true),
+                     exps_buf(ckpt, rows, n, true),
+                     {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    MmParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = x;
+    p.b = weight;
+    p.m = rows;
+    p.n = n;
+    p.k = k;
+    p.a_kmajor = p.b_kmajor = 1;
+    p.ep.bias = bias;
+    p.ep.ckpt = ckpt_dev(ckpt, n);
+    p.ep.act = act;
+    p.ep.residual = residual;
+    p.ep.out = out;
+    p.ep.out_f32 = out_dtype == LOCO_F32;
+    p.part = (float*)workspace;
+    p.splits = mm_splits(rows, n, k);
+    return hip_status(launch_mm(p, (hipStream_t)stream));
+}
+
+LOCO_API int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
+    if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
+    return mm_part_bytes(rows, in_features, out_features);
+}
+
+LOCO_API int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, const uint16_t* residual, int64_t rows,
+                                    int64_t out_features, int64_t in_features, loco_act_t act,
+                                    const loco_checkpoint_t* ckpt, void* dx, loco_dtype_t out_dtype, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+    if (!act_ok(act) || !dtype_ok(out_dtype) || (!ckpt && act != LOCO_ACT_NONE)) return LOCO_ERR_INVALID;
+    int st = ckpt ? check_ckpt(*ckpt) : LOCO_OK;
+    if (st != LOCO_OK) return st;
+    st = check_product(rows, out_features, in_features);
+    if (st != LOCO_OK) return st;
+    if (rows == 0 || in_features == 0) return LOCO_OK;
+    const int64_t n = in_features, k = out_features, need = loco_linear_input_grad_workspace(rows, k, n);
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    st = check_bufs({{dy, rows * k * 2, false, true},
+                     {weight, n * k * 2, false, true},
+                     {residual, rows * n * 2, false, false},
+                     {dx, rows * n * dtype_size(out_dtype), true, true},
+                     codes_buf(ckpt, rows, n, false),
+                     exps_buf(ckpt, rows, n, false),
+                     {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    MmParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = dy;
+    p.b = weight;
+    p.m = rows;
+    p.n = n;
+    p.k = k;
+    p.a_kmajor = 1;
+    if (act != LOCO_ACT_NONE) p.ep.slope = ckpt_dev(ckpt, n);
+    p.ep.act = act;
+    p.ep.residual = residual;
+    p.ep.out = dx;
+    p.ep.out_f32 = out_dtype == LOCO_F32;
+    p.part = (float*)workspace;
+    p.splits = mm_splits(rows, n, k);
+    return hip_status(launch_mm(p, (hipStream_t)stream));
+}
+
+LOCO_API int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features,
+                                                   loco_act_t act) {
+    if (check_product(rows, out_features, in_features) != LOCO_OK || !act_ok(act)) return 0;
+    return mm_part_bytes(out_features, in_features, rows) +
+           round16(col_sum_groups(rows, std::max<int64_t>(out_features, 1)) * out_features * 4);
+}
+
+LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t* ckpt, int64_t rows,
+                                     int64_t out_features, int64_t in_features, loco_act_t act, int accumulate,
+                                     void* dweight, void* dbias, loco_dtype_t grad_dtype, void* workspace,
+                                     int64_t workspace_bytes, void* stream) {
+    if (!ckpt || !act_ok(act) || !dtype_ok(grad_dtype)) return LOCO_ERR_INVALID;
+    int st = check_ckpt(*ckpt);
+    if (st != LOCO_OK) return st;
+    st = check_product(rows, out_features, in_features);
+    if (st != LOCO_OK) return st;
+    if (out_features == 0) return LOCO_OK;
+    const int64_t n = out_features, k = in_features, gs = dtype_size(grad_dtype);
+    const int64_t need = loco_linear_weight_grad_workspace(rows, n, k, act);
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    st = check_bufs({{dy, rows * n * 2, false, true},
+                     codes_buf(ckpt, rows, k, false),
+                     exps_buf(ckpt, rows, k, false),
+                     {dweight, n * k * gs, true, true},
+                     {dbias, n * gs, true, false},
+                     {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    const hipStream_t hs = (hipStream_t)stream;
+    const int64_t part = mm_part_bytes(n, k, rows);
+    if (k > 0) {
+        MmParams p;
+        memset(&p, 0, sizeof(p));
+        p.a = dy;
+        p.b_codes = 1;
+        p.bq = ckpt_dev(ckpt, k);
+        p.bq_act = act;
+        p.m = n;
+        p.n = k;
+        p.k = rows;
+        p.ep.out = dweight;
+        p.ep.out_f32 = grad_dtype == LOCO_F32;
+        p.ep.accumulate = accumulate != 0;
+        p.part = (float*)workspace;
+        p.splits = mm_splits(n, k, rows);
+        const hipError_t e = launch_mm(p, hs);
+        if (e != hipSuccess) return LOCO_ERR_HIP;
+    }
+    if (dbias)
+        return hip_status(launch_col_sum(dy, rows, n, (float*)((char*)workspace + part), dbias, grad_dtype == LOCO_F32,
+                                         accumulate != 0, hs));
     return LOCO_OK;
 }

@@ -9,6 +9,7 @@ a call returns an error status, the call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -24,10 +25,17 @@ LOCO_ERR_ALIGN = -2
 LOCO_ERR_UNSUPPORTED = -3
 LOCO_ERR_HIP = -4
 LOCO_MAX_PEERS = 128
+LOCO_ACT_NONE = 0
+LOCO_ACT_RELU = 1
+LOCO_ACT_GELU = 2
+LOCO_ACT_SILU = 3
 
 SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequant_reduce",
            "loco_dequant_reduce_adam", "loco_topk_quantize", "loco_sparse_aggregate", "loco_status_string",
-           "loco_version"]
+           "loco_version", "loco_layer_norm", "loco_layer_norm_backward", "loco_layer_norm_backward_workspace",
+           "loco_checkpoint_write", "loco_checkpoint_read", "loco_linear", "loco_linear_workspace",
+           "loco_linear_input_grad", "loco_linear_input_grad_workspace", "loco_linear_weight_grad",
+           "loco_linear_weight_grad_workspace"]
 
 
 class LocoError(RuntimeError):
@@ -58,6 +66,10 @@ class AdamParams(ctypes.Structure):
 
 class SparsePayload(ctypes.Structure):
     _fields_ = [("idx", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
+
+
+class Checkpoint(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("block", ctypes.c_int)]
 
 
 _lib = None
@@ -100,6 +112,23 @@ def load(path: str | None = None):
                                           ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int,
                                           ctypes.c_void_p]
     lib.loco_sparse_aggregate.restype = ctypes.c_int
+    ptr, i32, i64, f32, ckpt = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
+                                ctypes.POINTER(Checkpoint))
+    for fn, res, args in (
+            ("loco_layer_norm", i32, [ptr, i32, ptr, ptr, i32, i64, i64, f32, ptr, ptr, ptr, ckpt, ptr]),
+            ("loco_layer_norm_backward", i32, [ptr, ptr, i32, ptr, i32, ptr, ptr, ptr, i64, i64, ptr, ptr, ptr, i32,
+                                               ptr, i64, ptr]),
+            ("loco_layer_norm_backward_workspace", i64, [i64, i64]),
+            ("loco_checkpoint_write", i32, [ptr, i32, i64, i64, ckpt, ptr]),
+            ("loco_checkpoint_read", i32, [ckpt, i64, i64, i32, ptr, i32, ptr]),
+            ("loco_linear", i32, [ptr, ptr, ptr, ptr, i64, i64, i64, i32, ptr, i32, ckpt, ptr, i64, ptr]),
+            ("loco_linear_workspace", i64, [i64, i64, i64]),
+            ("loco_linear_input_grad", i32, [ptr, ptr, ptr, i64, i64, i64, i32, ckpt, ptr, i32, ptr, i64, ptr]),
+            ("loco_linear_input_grad_workspace", i64, [i64, i64, i64]),
+            ("loco_linear_weight_grad", i32, [ptr, ckpt, i64, i64, i64, i32, i32, ptr, ptr, i32, ptr, i64, ptr]),
+            ("loco_linear_weight_grad_workspace", i64, [i64, i64, i64, i32])):
+        getattr(lib, fn).argtypes = args
+        getattr(lib, fn).restype = res
     lib.loco_status_string.argtypes = [ctypes.c_int]
     lib.loco_status_string.restype = ctypes.c_char_p
     lib.loco_version.argtypes = []
@@ -324,6 +353,195 @@ def loco_sparse_aggregate(peers, n: int, *, chunk: int, k: int, out, out_scale: 
     _check("loco_sparse_aggregate", st)
 
 
+# -- layer operators ---------------------------------------------------------------------
+#
+# A matrix is a contiguous tensor whose last dimension is its columns; the leading ones
+# together are its rows (tokens).  A checkpoint is a pair (codes int8, exps uint8), with
+# the block (32 or 64) given beside it.
+
+def _rows_cols(t, what):
+    if t.dim() < 1:
+        raise ValueError(f"{what} must have at least one dimension")
+    cols = t.shape[-1]
+    return (t.numel() // cols if cols else math.prod(t.shape[:-1])), cols
+
+
+def _sized(t, numel: int, what: str, dtypes=None) -> None:
+    """t (None passes: the C call decides) must hold exactly numel elements of one of dtypes."""
+    if t is None:
+        return
+    if t.numel() != numel:
+        raise ValueError(f"{what} has {t.numel()} elements; the call needs {numel}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_BF = (torch.bfloat16,)
+_F32 = (torch.float32,)
+
+
+def _checkpoint(checkpoint, block, rows, cols, dev):
+    """The C struct of (codes, exps), or None."""
+    if checkpoint is None:
+        return None
+    codes, exps = checkpoint
+    _sized(codes, rows * cols, "checkpoint codes", (torch.int8,))
+    if block in (32, 64):
+        _sized(exps, rows * num_blocks(cols, block), "checkpoint exps", (torch.uint8,))
+    return ctypes.byref(Checkpoint(_ptr(codes, dev), _ptr(exps, dev), block))
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def loco_layer_norm(x, weight, bias, *, out, mean, rstd, eps: float = 1e-5, checkpoint=None, block: int = 64,
+                    stream=None) -> None:
+    """out = (x - mean) * rstd * weight + bias over x's last dimension; mean and rstd
+    (float32, one per row) are written for the backward pass, and `checkpoint`, if given,
+    with the 8-bit checkpoint of the output.  weight and bias may be None."""
+    dev = _device()
+    rows, cols = _rows_cols(x, "x")
+    _sized(x, rows * cols, "x", _FLOATS)
+    _sized(out, rows * cols, "out", (x.dtype,))
+    param = weight if weight is not None else bias
+    _sized(param, cols, "weight" if weight is not None else "bias", _FLOATS)
+    _sized(bias, cols, "bias", None if param is None else (param.dtype,))
+    _sized(mean, rows, "mean", _F32)
+    _sized(rstd, rows, "rstd", _F32)
+    ck = _checkpoint(checkpoint, block, rows, cols, dev)
+    st = load().loco_layer_norm(_ptr(x, dev), _dtype_code(x), _ptr(weight, dev), _ptr(bias, dev), _dtype_code(param),
+                                rows, cols, eps, _ptr(out, dev), _ptr(mean, dev), _ptr(rstd, dev),
+                                ck, _stream(stream, dev))
+    _check("loco_layer_norm", st)
+
+
+def loco_layer_norm_backward(dy, x, weight, mean, rstd, *, dx, dweight=None, dbias=None, residual=None,
+                             workspace=None, stream=None) -> None:
+    """dx of loco_layer_norm (plus residual, if given), and dweight and dbias summed over the
+    rows, each optional.  workspace: a tensor of layer_norm_backward_workspace(rows, cols)
+    bytes, not needed without dweight and dbias."""
+    dev = _device()
+    rows, cols = _rows_cols(x, "x")
+    _sized(x, rows * cols, "x", _FLOATS)
+    for t, what in ((dy, "dy"), (dx, "dx"), (residual, "residual")):
+        _sized(t, rows * cols, what, (x.dtype,))
+    _sized(weight, cols, "weight", _FLOATS)
+    _sized(mean, rows, "mean", _F32)
+    _sized(rstd, rows, "rstd", _F32)
+    grad = dweight if dweight is not None else dbias
+    _sized(grad, cols, "dweight" if dweight is not None else "dbias", _FLOATS)
+    _sized(dbias, cols, "dbias", None if grad is None else (grad.dtype,))
+    st = load().loco_layer_norm_backward(_ptr(dy, dev), _ptr(x, dev), _dtype_code(x), _ptr(weight, dev),
+                                         _dtype_code(weight), _ptr(mean, dev), _ptr(rstd, dev), _ptr(residual, dev),
+                                         rows, cols, _ptr(dx, dev), _ptr(dweight, dev), _ptr(dbias, dev),
+                                         _dtype_code(grad), _ptr(workspace, dev), _nbytes(workspace),
+                                         _stream(stream, dev))
+    _check("loco_layer_norm_backward", st)
+
+
+def loco_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    return load().loco_layer_norm_backward_workspace(rows, cols)
+
+
+def loco_checkpoint_write(x, *, codes, exps, block: int = 64, stream=None) -> None:
+    """The 8-bit checkpoint of x: codes int8 of x's shape, exps uint8, one per block of a row."""
+    dev = _device()
+    rows, cols = _rows_cols(x, "x")
+    _sized(x, rows * cols, "x", _FLOATS)
+    ck = _checkpoint((codes, exps), block, rows, cols, dev)
+    st = load().loco_checkpoint_write(_ptr(x, dev), _dtype_code(x), rows, cols,
+                                      ck, _stream(stream, dev))
+    _check("loco_checkpoint_write", st)
+
+
+def loco_checkpoint_read(codes, exps, *, out, block: int = 64, act: int = LOCO_ACT_NONE, stream=None) -> None:
+    """out = act(the values of the checkpoint); the matrix's shape is out's."""
+    dev = _device()
+    rows, cols = _rows_cols(out, "out")
+    _sized(out, rows * cols, "out", _FLOATS)
+    ck = _checkpoint((codes, exps), block, rows, cols, dev)
+    st = load().loco_checkpoint_read(ck, rows, cols, act,
+                                     _ptr(out, dev), _dtype_code(out), _stream(stream, dev))
+    _check("loco_checkpoint_read", st)
+
+
+def loco_linear(x, weight, *, out, bias=None, act: int = LOCO_ACT_NONE, residual=None, checkpoint=None,
+                block: int = 64, workspace=None, stream=None) -> None:
+    """out = act(x weight^T + bias) + residual, with weight [out_features, in_features];
+    `checkpoint`, if given, is written with the 8-bit checkpoint of the activation's input.
+    bfloat16, out bfloat16 or float32."""
+    dev = _device()
+    rows, k = _rows_cols(x, "x")
+    n, wk = _rows_cols(weight, "weight")
+    if wk != k:
+        raise ValueError(f"x has {k} columns, weight {wk}")
+    _sized(x, rows * k, "x", _BF)
+    _sized(weight, n * k, "weight", _BF)
+    _sized(bias, n, "bias", _BF)
+    _sized(residual, rows * n, "residual", _BF)
+    _sized(out, rows * n, "out", _FLOATS)
+    ck = _checkpoint(checkpoint, block, rows, n, dev)
+    st = load().loco_linear(_ptr(x, dev), _ptr(weight, dev), _ptr(bias, dev), _ptr(residual, dev), rows, n, k, act,
+                            _ptr(out, dev), _dtype_code(out), ck,
+                            _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    _check("loco_linear", st)
+
+
+def loco_linear_workspace(rows: int, out_features: int, in_features: int) -> int:
+    return load().loco_linear_workspace(rows, out_features, in_features)
+
+
+def loco_linear_input_grad(dy, weight, *, out, act: int = LOCO_ACT_NONE, checkpoint=None, block: int = 64,
+                           residual=None, workspace=None, stream=None) -> None:
+    """out = (dy weight) * act'(z) + residual, with z read from the 8-bit checkpoint of the
+    activation's input (needed unless act is LOCO_ACT_NONE)."""
+    dev = _device()
+    rows, n = _rows_cols(dy, "dy")
+    wn, k = _rows_cols(weight, "weight")
+    if wn != n:
+        raise ValueError(f"dy has {n} columns, weight {wn} rows")
+    _sized(dy, rows * n, "dy", _BF)
+    _sized(weight, n * k, "weight", _BF)
+    _sized(residual, rows * k, "residual", _BF)
+    _sized(out, rows * k, "out", _FLOATS)
+    ck = _checkpoint(checkpoint, block, rows, k, dev)
+    st = load().loco_linear_input_grad(_ptr(dy, dev), _ptr(weight, dev), _ptr(residual, dev), rows, n, k, act,
+                                       ck, _ptr(out, dev), _dtype_code(out),
+                                       _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    _check("loco_linear_input_grad", st)
+
+
+def loco_linear_input_grad_workspace(rows: int, out_features: int, in_features: int) -> int:
+    return load().loco_linear_input_grad_workspace(rows, out_features, in_features)
+
+
+def loco_linear_weight_grad(dy, checkpoint, *, out, block: int = 64, act: int = LOCO_ACT_NONE, dbias=None,
+                            accumulate: bool = False, workspace=None, stream=None) -> None:
+    """out [out_features, in_features] = dy^T act(the checkpoint's values), dbias = dy summed
+    over the rows; with accumulate, added to what they hold.  out and dbias are bfloat16
+    or float32, alike."""
+    dev = _device()
+    rows, n = _rows_cols(dy, "dy")
+    wn, k = _rows_cols(out, "out")
+    if wn != n:
+        raise ValueError(f"dy has {n} columns, out {wn} rows")
+    _sized(dy, rows * n, "dy", _BF)
+    _sized(out, n * k, "out", _FLOATS)
+    _sized(dbias, n, "dbias", (out.dtype,))
+    ck = _checkpoint(checkpoint, block, rows, k, dev)
+    st = load().loco_linear_weight_grad(_ptr(dy, dev), ck, rows, n, k, act,
+                                        1 if accumulate else 0, _ptr(out, dev), _ptr(dbias, dev), _dtype_code(out),
+                                        _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    _check("loco_linear_weight_grad", st)
+
+
+def loco_linear_weight_grad_workspace(rows: int, out_features: int, in_features: int,
+                                      act: int = LOCO_ACT_NONE) -> int:
+    return load().loco_linear_weight_grad_workspace(rows, out_features, in_features, act)
+
+
 # short names
 compensate_quantize = loco_compensate_quantize
 compensate_quantize_ex = loco_compensate_quantize_ex
@@ -331,3 +549,14 @@ dequant_reduce = loco_dequant_reduce
 dequant_reduce_adam = loco_dequant_reduce_adam
 topk_quantize = loco_topk_quantize
 sparse_aggregate = loco_sparse_aggregate
+layer_norm = loco_layer_norm
+layer_norm_backward = loco_layer_norm_backward
+layer_norm_backward_workspace = loco_layer_norm_backward_workspace
+checkpoint_write = loco_checkpoint_write
+checkpoint_read = loco_checkpoint_read
+linear = loco_linear
+linear_workspace = loco_linear_workspace
+linear_input_grad = loco_linear_input_grad
+linear_input_grad_workspace = loco_linear_input_grad_workspace
+linear_weight_grad = loco_linear_weight_grad
+linear_weight_grad_workspace = loco_linear_weight_grad_workspace

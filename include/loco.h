@@ -276,6 +276,136 @@ int loco_sparse_aggregate(const loco_sparse_payload_t* peers, int npeers, int64_
                           int chunk, int k, int bits, float out_scale, void* out,
                           loco_dtype_t out_dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Layer operators: the products, norms and activation checkpoints of the layer whose
+ * backward pass writes the gradient that loco_compensate_quantize takes.
+ *
+ * Matrices are row-major and contiguous; rows are tokens.  A call that needs scratch
+ * memory takes `workspace`, device memory of at least the bytes that the matching
+ * loco_*_workspace function returns for the same sizes (0: none, and workspace may be
+ * NULL); its contents before and after are unspecified.  Sums, statistics and
+ * accumulators are fp32 (the matrix cores' products of bf16 are exact in it); fused
+ * multiply-adds are used, and sums run in an order of the library's own that depends on
+ * the sizes only, so the same call gives the same bits.  Infinities and NaNs in the
+ * inputs follow IEEE arithmetic into the outputs they reach.
+ * ------------------------------------------------------------------------------ */
+
+/* Activations a(z). */
+typedef enum {
+    LOCO_ACT_NONE = 0, /* z */
+    LOCO_ACT_RELU = 1, /* max(z, 0) */
+    LOCO_ACT_GELU = 2, /* z * sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)), the tanh form */
+    LOCO_ACT_SILU = 3  /* z * sigmoid(z) */
+} loco_act_t;
+
+/*
+ * An 8-bit activation checkpoint of a matrix [rows, cols].  Blocks of `block` elements
+ * run along each row and restart with it (the last of a row may be short).
+ *   codes  device i8[rows * cols]
+ *   exps   device u8[rows * ceil(cols / block)]: the block's step is 2^(exps - 127)
+ *   block  32 or 64
+ * A value is codes * step.  Written, the step is the least power of two >= 2^-126 with
+ * max|x| < 127.5 * step and the code is rint(x / step), ties to even: one rounding, of at
+ * most half a step.  A code times a power of two has at most 7 significant bits, so
+ * every value is a bf16 number and the matrix cores read it exactly.  A block that holds
+ * an infinity or a NaN is written with exps 255 and codes 0; exps 255 reads as NaN where the
+ * code is 0 and as an infinity elsewhere, exps 0 as 0.
+ */
+typedef struct {
+    int8_t* codes;
+    uint8_t* exps;
+    int block;
+} loco_checkpoint_t;
+
+/*
+ * loco_layer_norm - y = (x - mean) * rstd * weight + bias per row, with
+ * mean = sum(x)/cols and rstd = 1/sqrt(sum((x - mean)^2)/cols + eps).
+ *   x, y          device [rows, cols] of `dtype` (LOCO_F32 or LOCO_BF16)
+ *   weight, bias  device [cols] of `param_dtype`; NULL: ones, zeros
+ *   eps           finite, >= 0
+ *   mean, rstd    device f32[rows] (written), for the backward pass
+ *   ckpt          NULL, or the 8-bit checkpoint of y to write (of the fp32 y, before its
+ *                 rounding to dtype)
+ *   cols          1 .. 16384 (LOCO_ERR_UNSUPPORTED beyond); rows 0 is a no-op
+ */
+int loco_layer_norm(const void* x, loco_dtype_t dtype, const void* weight, const void* bias,
+                    loco_dtype_t param_dtype, int64_t rows, int64_t cols, float eps, void* y,
+                    float* mean, float* rstd, const loco_checkpoint_t* ckpt, void* stream);
+
+/*
+ * loco_layer_norm_backward - with xh = (x - mean) * rstd and g = dy * weight:
+ *   dx      = rstd * (g - sum(g)/cols - xh * sum(g * xh)/cols) [+ residual]
+ *   dweight = sum over the rows of dy * xh,  dbias = sum over the rows of dy
+ *   dy, x, residual, dx  device [rows, cols] of `dtype`; residual may be NULL
+ *   weight               device [cols] of `param_dtype`; NULL: ones
+ *   mean, rstd           device f32[rows], as loco_layer_norm wrote them
+ *   dweight, dbias       device [cols] of `grad_dtype` (written), each may be NULL;
+ *                        with rows 0 they are written as zeros
+ *   workspace            loco_layer_norm_backward_workspace(rows, cols) bytes; may be NULL
+ *                        if dweight and dbias are
+ */
+int loco_layer_norm_backward(const void* dy, const void* x, loco_dtype_t dtype, const void* weight,
+                             loco_dtype_t param_dtype, const float* mean, const float* rstd,
+                             const void* residual, int64_t rows, int64_t cols, void* dx,
+                             void* dweight, void* dbias, loco_dtype_t grad_dtype,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+int64_t loco_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * loco_checkpoint_write - the 8-bit checkpoint of x [rows, cols] of `dtype`.
+ * loco_checkpoint_read  - out = act(value), [rows, cols] of `out_dtype`.
+ */
+int loco_checkpoint_write(const void* x, loco_dtype_t dtype, int64_t rows, int64_t cols,
+                          const loco_checkpoint_t* ckpt, void* stream);
+int loco_checkpoint_read(const loco_checkpoint_t* ckpt, int64_t rows, int64_t cols, loco_act_t act,
+                         void* out, loco_dtype_t out_dtype, void* stream);
+
+/*
+ * loco_linear - z = x weight^T + bias; out = act(z) + residual.
+ *   x         device bf16[rows, in];  weight  device bf16[out_features, in]
+ *   bias      device bf16[out_features], or NULL;  residual  device bf16[rows, out_features],
+ *             or NULL
+ *   ckpt      NULL, or the 8-bit checkpoint of z to write (of the fp32 z)
+ *   out       device [rows, out_features] of `out_dtype`
+ *   rows >= 0; in and out_features 0 .. 2^20 (LOCO_ERR_UNSUPPORTED beyond)
+ */
+int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16_t* bias, const uint16_t* residual,
+                int64_t rows, int64_t out_features, int64_t in_features, loco_act_t act, void* out,
+                loco_dtype_t out_dtype, const loco_checkpoint_t* ckpt, void* workspace,
+                int64_t workspace_bytes, void* stream);
+int64_t loco_linear_workspace(int64_t rows, int64_t out_features, int64_t in_features);
+
+/*
+ * loco_linear_input_grad - dx = (dy weight) * act'(z) + residual, where z is read from the
+ * 8-bit checkpoint of the activation's input [rows, in].
+ *   dy        device bf16[rows, out_features];  weight  device bf16[out_features, in]
+ *   ckpt      the checkpoint; NULL: act must be LOCO_ACT_NONE
+ *   residual  device bf16[rows, in], or NULL
+ *   dx        device [rows, in] of `out_dtype`
+ */
+int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, const uint16_t* residual,
+                           int64_t rows, int64_t out_features, int64_t in_features, loco_act_t act,
+                           const loco_checkpoint_t* ckpt, void* dx, loco_dtype_t out_dtype,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features);
+
+/*
+ * loco_linear_weight_grad - dweight = dy^T a, dbias = sum over the rows of dy, with
+ * a = act(value of the 8-bit checkpoint [rows, in]).  LOCO_ACT_NONE takes the checkpoint's
+ * values as they are; an activation's value is rounded to bf16 for the product.
+ *   dy          device bf16[rows, out_features]
+ *   dweight     device [out_features, in] of `grad_dtype`
+ *   dbias       device [out_features] of `grad_dtype`, or NULL
+ *   accumulate  nonzero: added to what dweight and dbias hold (in fp32, rounded once)
+ * With rows 0 the gradients are zero.
+ */
+int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t* ckpt, int64_t rows,
+                            int64_t out_features, int64_t in_features, loco_act_t act, int accumulate,
+                            void* dweight, void* dbias, loco_dtype_t grad_dtype, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features,
+                                          loco_act_t act);
+
 /* A static, human-readable name for a status code. */
 const char* loco_status_string(int status);
 
