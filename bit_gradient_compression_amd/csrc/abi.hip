@@ -624,7 +624,8 @@ LOCO_API int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_fea
                                                    loco_act_t act) {
     if (check_product(rows, out_features, in_features) != LOCO_OK || !act_ok(act)) return 0;
     return mm_part_bytes(out_features, in_features, rows) +
-           round16(col_sum_groups(rows, std::max<int64_t>(out_features, 1)) * out_features * 4);
+           round16(col_sum_groups(rows, std::max<int64_t>(out_features, 1)) * out_features * 4) +
+           (mm_decodes(out_features, in_features) ? round16(rows * in_features * 2) : 0);
 }
 
 LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t* ckpt, int64_t rows,
@@ -648,14 +649,22 @@ LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t
                      {workspace, need, true, true}});
     if (st != LOCO_OK) return st;
     const hipStream_t hs = (hipStream_t)stream;
-    const int64_t part = mm_part_bytes(n, k, rows);
+    // workspace: the product's partial sums, the bias gradient's, the decoded checkpoint
+    const int64_t part = mm_part_bytes(n, k, rows), sums = round16(col_sum_groups(rows, n) * n * 4);
     if (k > 0) {
         MmParams p;
         memset(&p, 0, sizeof(p));
         p.a = dy;
-        p.b_codes = 1;
-        p.bq = ckpt_dev(ckpt, k);
-        p.bq_act = act;
+        if (mm_decodes(n, k)) {
+            uint16_t* b = (uint16_t*)((char*)workspace + part + sums);
+            if (rows > 0 && launch_ckpt_read(ckpt_dev(ckpt, k), rows, k, act, b, false, hs) != hipSuccess)
+                return LOCO_ERR_HIP;
+            p.b = b;
+        } else {
+            p.b_codes = 1;
+            p.bq = ckpt_dev(ckpt, k);
+            p.bq_act = act;
+        }
         p.m = n;
         p.n = k;
         p.k = rows;

@@ -91,6 +91,8 @@ struct MmParams {
 hipError_t launch_mm(const MmParams& p, hipStream_t stream);
 // Splits of the contraction that a product of this shape is worked in.
 int mm_splits(int64_t m, int64_t n, int64_t k);
+// Whether C [m, n] with a checkpointed B is worked from B decoded to bf16 beforehand.
+bool mm_decodes(int64_t m, int64_t n);
 
 // out[n] = sum over the rows of x [rows, n]; part [col_sum_groups][n].
 int64_t col_sum_groups(int64_t rows, int64_t n);
