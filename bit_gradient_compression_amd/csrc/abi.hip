@@ -436,11 +436,6 @@ int check_product(int64_t rows, int64_t out_features, int64_t in_features) {
     return LOCO_OK;
 }
 
-int64_t mm_part_bytes(int64_t m, int64_t n, int64_t k) {
-    const int s = mm_splits(m, n, k);
-    return s > 1 ? round16((int64_t)s * m * n * 4) : 0;
-}
-
 }  // namespace
 }  // namespace loco
 
@@ -534,7 +529,7 @@ LOCO_API int loco_checkpoint_read(const loco_checkpoint_t* ckpt, int64_t rows, i
 
 LOCO_API int64_t loco_linear_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
     if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
-    return mm_part_bytes(rows, out_features, in_features);
+    return mm_part_bytes(true, true, rows, out_features, in_features);
 }
 
 LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16_t* bias, const uint16_t* residual,
@@ -573,13 +568,12 @@ LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16
     p.ep.out = out;
     p.ep.out_f32 = out_dtype == LOCO_F32;
     p.part = (float*)workspace;
-    p.splits = mm_splits(rows, n, k);
     return hip_status(launch_mm(p, (hipStream_t)stream));
 }
 
 LOCO_API int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
     if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
-    return mm_part_bytes(rows, in_features, out_features);
+    return mm_part_bytes(true, false, rows, in_features, out_features);
 }
 
 LOCO_API int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, const uint16_t* residual, int64_t rows,
@@ -616,14 +610,13 @@ LOCO_API int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, 
     p.ep.out = dx;
     p.ep.out_f32 = out_dtype == LOCO_F32;
     p.part = (float*)workspace;
-    p.splits = mm_splits(rows, n, k);
     return hip_status(launch_mm(p, (hipStream_t)stream));
 }
 
 LOCO_API int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features,
                                                    loco_act_t act) {
     if (check_product(rows, out_features, in_features) != LOCO_OK || !act_ok(act)) return 0;
-    return mm_part_bytes(out_features, in_features, rows) +
+    return round16(mm_part_bytes(false, false, out_features, in_features, rows)) +
            round16(col_sum_groups(rows, std::max<int64_t>(out_features, 1)) * out_features * 4) +
            (mm_decodes(out_features, in_features) ? round16(rows * in_features * 2) : 0);
 }
@@ -650,7 +643,7 @@ LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t
     if (st != LOCO_OK) return st;
     const hipStream_t hs = (hipStream_t)stream;
     // workspace: the product's partial sums, the bias gradient's, the decoded checkpoint
-    const int64_t part = mm_part_bytes(n, k, rows), sums = round16(col_sum_groups(rows, n) * n * 4);
+    const int64_t part = round16(mm_part_bytes(false, false, n, k, rows)), sums = round16(col_sum_groups(rows, n) * n * 4);
     if (k > 0) {
         MmParams p;
         memset(&p, 0, sizeof(p));
@@ -672,7 +665,6 @@ LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t
         p.ep.out_f32 = grad_dtype == LOCO_F32;
         p.ep.accumulate = accumulate != 0;
         p.part = (float*)workspace;
-        p.splits = mm_splits(n, k, rows);
         const hipError_t e = launch_mm(p, hs);
         if (e != hipSuccess) return LOCO_ERR_HIP;
     }

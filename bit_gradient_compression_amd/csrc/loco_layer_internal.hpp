@@ -85,12 +85,11 @@ struct MmParams {
     int64_t m, n, k;
     int a_kmajor, b_kmajor;
     MmEpilogue ep;
-    float* part;  // [splits][m][n] partial sums, where splits > 1
-    int splits;
+    float* part;  // mm_part_bytes bytes
 };
 hipError_t launch_mm(const MmParams& p, hipStream_t stream);
-// Splits of the contraction that a product of this shape is worked in.
-int mm_splits(int64_t m, int64_t n, int64_t k);
+// Partial sums of a product whose contraction is worked in splits; 0: it is not split.
+int64_t mm_part_bytes(bool a_kmajor, bool b_kmajor, int64_t m, int64_t n, int64_t k);
 // Whether C [m, n] with a checkpointed B is worked from B decoded to bf16 beforehand.
 bool mm_decodes(int64_t m, int64_t n);
 

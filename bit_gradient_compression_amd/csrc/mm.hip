@@ -26,6 +26,18 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kStep = 64;  // k per step
 
+// N pieces of work f(0) ... f(N - 1) spread evenly over SLOTS places in the code; the pieces of
+// place x.
+template <int SLOTS, int N, typename F>
+__device__ __forceinline__ void spread(int x, F f) {
+    constexpr int every = SLOTS / N > 1 ? SLOTS / N : 1, at_once = (N + SLOTS - 1) / SLOTS;
+    if (x % every == 0) {
+#pragma unroll
+        for (int c = 0; c < at_once; ++c)
+            if (x / every * at_once + c < N) f(x / every * at_once + c);
+    }
+}
+
 // ---- LDS tiles ------------------------------------------------------------------------
 //
 // A tile of W rows or columns and STEP k is a sequence of 16-byte chunks, written in order
@@ -33,26 +45,54 @@ constexpr int kStep = 64;  // k per step
 // holds W/8 chunks.  The chunk at position c of row r is the operand's chunk c ^ swz(r).  LDS
 // has 64 banks of 4 bytes, 16 chunks across.  k-major: sixteen lanes read one k of sixteen
 // rows, 16 / (STEP/8) rows of which lie in different banks anyway; the swizzle tells the
-// others apart.  free-major: a read takes 64 bytes from each of four rows, which the swizzle
-// spreads over all banks.
+// others apart.  free-major: a read takes stretches of four rows, eight rows
+// apart for other lanes, which the swizzle spreads over all banks.
 template <bool KMAJOR, int W, int STEP>
 struct Tile {
     static constexpr int kChunks = W * STEP / 8;
     static constexpr int kPerRow = KMAJOR ? STEP / 8 : W / 8;
     static __device__ __forceinline__ int swz(int row) {
-        return KMAJOR ? row / (16 / kPerRow) & (kPerRow - 1) : (row & 3) * 4;
+        if constexpr (KMAJOR) return row / (16 / kPerRow) & (kPerRow - 1);
+        // free-major: two chunks from each of four rows, and the same eight rows on
+        else if constexpr (kPerRow >= 16) return (row & 3) * 4 ^ (row >> 2 & 2);
+        else if constexpr (kPerRow == 8) return (row & 2) ^ (row >> 1 & 4);
+        else return row >> 2 & 2;
     }
+    static_assert(KMAJOR || kPerRow == 4 || kPerRow % 8 == 0, "rows that the swizzle stays inside of");
     static __device__ __forceinline__ int row_of(int q) { return q / kPerRow; }
     static __device__ __forceinline__ int chunk_of(int q) { return (q % kPerRow) ^ swz(row_of(q)); }
 };
 
-// Fragment of a 32 x 16 (free x k) operand block: lane l holds free index l % 32 and the
-// eight k from 8 * (l / 32).
-template <bool KMAJOR, int W, int STEP>
+// The matrix instruction: MS x MS results from MS x KS and KS x MS operands.  Lane l holds
+// free index l % MS of an operand and the eight k from 8 * (l / MS).
+template <int MS>
+struct Mfma;
+template <>
+struct Mfma<32> {
+    static constexpr int KS = 16;
+    typedef f32x16 acc_t;
+    static __device__ __forceinline__ acc_t mul(bf16x8 a, bf16x8 b, acc_t c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    // row of register r; the column is lane % 32
+    static __device__ __forceinline__ int row(int r, int lane) { return 8 * (r / 4) + 4 * (lane >> 5) + r % 4; }
+};
+template <>
+struct Mfma<16> {
+    static constexpr int KS = 32;
+    typedef f32x4 acc_t;
+    static __device__ __forceinline__ acc_t mul(bf16x8 a, bf16x8 b, acc_t c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ int row(int r, int lane) { return 4 * (lane >> 4) + r; }
+};
+
+// An operand's fragment at (free0, k0) of a tile.
+template <bool KMAJOR, int W, int STEP, int MS>
 __device__ __forceinline__ bf16x8 read_frag(const u32x4* tile, int free0, int k0, int lane) {
     using T = Tile<KMAJOR, W, STEP>;
     if constexpr (KMAJOR) {
-        const int r = free0 + (lane & 31), c = k0 / 8 + (lane >> 5);
+        const int r = free0 + (lane & (MS - 1)), c = k0 / 8 + lane / MS;
         return __builtin_bit_cast(bf16x8, tile[r * T::kPerRow + (c ^ T::swz(r))]);
     } else {
         // Each group of 16 lanes takes 4 rows (k) of 16 columns: lane i of the group reads
@@ -63,8 +103,8 @@ __device__ __forceinline__ bf16x8 read_frag(const u32x4* tile, int free0, int k0
         } f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int k = k0 + (lane >> 5) * 8 + h * 4 + ((lane & 15) >> 2);
-            const int col = free0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+            const int k = k0 + lane / MS * 8 + h * 4 + ((lane & 15) >> 2);
+            const int col = free0 + (lane & (MS - 1) & 16) + (lane & 3) * 4;
             const int q = k * T::kPerRow + ((col >> 3) ^ T::swz(k));
             const char* p = (const char*)(tile + q) + (col & 4) * 2;
             f.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
@@ -222,43 +262,147 @@ __device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& tm
     tn = id % width / rows;
 }
 
-// A wave's accumulators to rows: register r of a 32 x 32 block is row 8 (r / 4) + 4 (lane / 32) +
-// r % 4, column lane % 32.  32 rows of 64 columns at a time turn through the wave's own
-// stretch of LDS, after which eight lanes hold one row's 64 columns: stores, the residual's
-// loads and a checkpoint's blocks all take whole chunks.
+// ---- from accumulators to rows -----------------------------------------------------------
+//
+// 32 rows of 64 columns (a part) at a time turn through the wave's own stretch of LDS, after
+// which eight lanes hold one row's 64 columns, in four passes of eight rows: stores, the
+// residual's loads and a checkpoint's blocks all take whole chunks.
 constexpr int kRowPad = 68;  // floats from row to row: the eight rows of one read start in different banks
-template <int MI, int NI>
-__device__ __forceinline__ void store_acc(const MmArgs& g, const f32x16 (&acc)[MI][NI], float* mine, int64_t m0,
-                                          int64_t n0, int lane) {
-    // One copy of the epilogue's code: the loop over the 32 x 64 parts is a real one, and each
-    // part's registers are picked by a uniform branch.
+constexpr int kPasses = 2;  // of eight rows, worked together
+
+// What the epilogue reads of a part, loaded ahead of its use.
+struct PartLoads {
+    u32x4 residual[kPasses];
+    u32x2 codes[kPasses];
+    uint32_t exps[kPasses];
+    __device__ __forceinline__ void load(const MmEpilogue& e, int64_t n, int64_t row, int64_t col) {
+        if (e.residual) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) residual[p] = load16(e.residual + (row + p * 8) * n + col);
+        }
+        if (e.slope.codes) {
+            const int shift = e.slope.block64 ? 6 : 5;
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+                __builtin_memcpy(&codes[p], e.slope.codes + (row + p * 8) * n + col, 8);
+                exps[p] = e.slope.exps[(row + p * 8) * e.slope.nblocks + (col >> shift)];
+            }
+        }
+    }
+};
+
+// The epilogue of rows that lie inside the matrix: epilogue() for whole chunks of several rows,
+// without its tests of each chunk's end and with nothing that waits between the passes.
+__device__ __forceinline__ void epilogue_part(const MmEpilogue& e, const PartLoads& in, int64_t n, int64_t row,
+                                              int64_t col, float (&v)[kPasses][8]) {
+    float t[8];
+    if (e.bias) {
+        unpack_bf16x8(load16(e.bias + col), t);
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[p][i] += t[i];
+    }
+    if (e.ckpt.codes) {
+        const int shift = e.ckpt.block64 ? 6 : 5;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const uint32_t x = ckpt_exp(block_top(v[p], e.ckpt.block64));
+            store_codes(e.ckpt.codes + (row + p * 8) * n + col, 8, ckpt_codes(v[p], x));
+            if ((col & ((1 << shift) - 1)) == 0)
+                e.ckpt.exps[(row + p * 8) * e.ckpt.nblocks + (col >> shift)] = (uint8_t)x;
+        }
+    }
+    if (e.slope.codes) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            decode_codes(in.codes[p], in.exps[p], t);
+            slope_chunk_any(e.act, t, v[p]);
+        }
+    } else if (e.act) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) act_chunk_any(e.act, v[p]);
+    }
+    if (e.residual) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            unpack_bf16x8(in.residual[p], t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[p][i] += t[i];
+        }
+    }
+    if (e.accumulate) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            load_chunk_any(e.out, e.out_f32, (row + p * 8) * n + col, 8, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[p][i] += t[i];
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) store_chunk_any(e.out, e.out_f32, (row + p * 8) * n + col, 8, v[p]);
+}
+
+template <int MS, int MI, int NI>
+__device__ __forceinline__ void store_acc(const MmArgs& g, const typename Mfma<MS>::acc_t (&acc)[MI][NI], float* mine,
+                                          int64_t m0, int64_t n0, int lane) {
+    constexpr int PI = 32 / MS, PJ = 64 / MS;  // blocks of a part
+    constexpr int ACROSS = NI / PJ, PARTS = MI / PI * ACROSS;
+    const int rl = lane >> 3, cl = (lane & 7) * 8;
+    // row and column of a part; uniform, and so is whether it lies inside
+    auto row_of = [&](int part) __attribute__((always_inline)) { return m0 + part / ACROSS * 32; };
+    auto col_of = [&](int part) __attribute__((always_inline)) { return n0 + part % ACROSS * 64; };
+    auto inside = [&](int part) __attribute__((always_inline)) { return row_of(part) + 32 <= g.m && col_of(part) + 64 <= g.n; };
+    // One copy of the epilogue's code: the loop over the parts is a real one, and each part's
+    // registers are picked by a uniform branch.
 #pragma unroll 1
-    for (int part = 0; part < MI * NI / 2; ++part) {
+    for (int part = 0; part < PARTS; ++part) {
+        const int64_t row0 = row_of(part) + rl, col = col_of(part) + cl;
+        PartLoads in;
+        const bool whole = inside(part), ep = whole && !g.part;
+        if (ep) in.load(g.ep, g.n, row0, col);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int x = 0; x < PARTS; ++x)
+            if (part == x) {
 #pragma unroll
-            for (int h = 0; h < NI / 2; ++h)
-                if (part == i * (NI / 2) + h) {
+                for (int i = 0; i < PI; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int j = 0; j < PJ; ++j)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            mine[(8 * (r / 4) + 4 * (lane >> 5) + r % 4) * kRowPad + j * 32 + (lane & 31)] =
-                                acc[i][2 * h + j][r];
+                        for (int r = 0; r < MS * MS / 64; ++r)
+                            mine[(i * MS + Mfma<MS>::row(r, lane)) * kRowPad + j * MS + (lane & (MS - 1))] =
+                                acc[x / ACROSS * PI + i][x % ACROSS * PJ + j][r];
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (whole) {
+#pragma unroll
+            for (int q = 0; q < 4 / kPasses; ++q) {
+                float v[kPasses][8];
+                const int64_t row = row0 + q * kPasses * 8;
+#pragma unroll
+                for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) v[p][x] = mine[((q * kPasses + p) * 8 + rl) * kRowPad + cl + x];
+                if (g.part) {
+                    float* out = g.part + ((int64_t)blockIdx.y * g.m + row) * g.n + col;
+#pragma unroll
+                    for (int p = 0; p < kPasses; ++p) store_chunk(out + p * 8 * g.n, 8, v[p]);
+                } else {
+                    epilogue_part(g.ep, in, g.n, row, col, v);
+                    if (q + 1 < 4 / kPasses) in.load(g.ep, g.n, row + kPasses * 8, col);
                 }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const int64_t row0 = m0 + part / (NI / 2) * 32, col0 = n0 + part % (NI / 2) * 64;
+            }
+            continue;
+        }
 #pragma unroll 1
-        for (int pass = 0; pass < 4; ++pass) {
-            const int r = pass * 8 + (lane >> 3), c = (lane & 7) * 8;
-            const int64_t row = row0 + r, col = col0 + c;
+        for (int p = 0; p < 4; ++p) {
+            const int64_t row = row0 + p * 8, left = g.n - col;
             float v[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = mine[r * kRowPad + c + x];
-            const int64_t left = g.n - col;
+            for (int x = 0; x < 8; ++x) v[x] = mine[(p * 8 + rl) * kRowPad + cl + x];
             const int valid = row >= g.m || left <= 0 ? 0 : left < 8 ? (int)left : 8;
             if (g.part) store_chunk(g.part + ((int64_t)blockIdx.y * g.m + row) * g.n + col, valid, v);
             else epilogue(g.ep, row, g.n, col, valid, v);
@@ -309,9 +453,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
         for (int s = 0; s < kStep / 16; ++s) {
             bf16x8 fa[MI], fb[NI];
 #pragma unroll
-            for (int i = 0; i < MI; ++i) fa[i] = read_frag<AK, BM, kStep>(ta, wm * TM + i * 32, s * 16, lane);
+            for (int i = 0; i < MI; ++i) fa[i] = read_frag<AK, BM, kStep, 32>(ta, wm * TM + i * 32, s * 16, lane);
 #pragma unroll
-            for (int j = 0; j < NI; ++j) fb[j] = read_frag<BK, BN, kStep>(tb, wn * TN + j * 32, s * 16, lane);
+            for (int j = 0; j < NI; ++j) fb[j] = read_frag<BK, BN, kStep, 32>(tb, wn * TN + j * 32, s * 16, lane);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -326,7 +470,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
         __syncthreads();
     }
 
-    store_acc<MI, NI>(g, acc, (float*)lds + wave * 32 * kRowPad, m0 + wm * TM, n0 + wn * TN, lane);
+    store_acc<32, MI, NI>(g, acc, (float*)lds + wave * 32 * kRowPad, m0 + wm * TM, n0 + wn * TN, lane);
 }
 
 // ---- the tile kernel, staged past the registers --------------------------------------------
@@ -354,16 +498,16 @@ struct Dma {
     __device__ __forceinline__ void init(const Operand& o, int64_t free0, int64_t k0) {
         static_assert(THREADS % T::kPerRow == 0 && (THREADS / T::kPerRow) % 16 == 0 || !KMAJOR,
                       "a thread's loads share their chunk's place in the row");
-        static_assert(THREADS / T::kPerRow % 4 == 0 || KMAJOR, "a thread's loads share their swizzle");
         const int t = threadIdx.x;
         s.base = (const char*)(o.p + (KMAJOR ? free0 * o.ld + k0 : k0 * o.ld + free0));
         s.left = ((KMAJOR ? o.free : o.k) * o.ld) * 2 - (s.base - (const char*)o.p);
         s.step = (KMAJOR ? STEP : STEP * o.ld) * 2;
         k_chunk = T::chunk_of(t);
-        const uint32_t per = (uint32_t)(THREADS / T::kPerRow * o.ld * 2);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            off[j] = (uint32_t)(T::row_of(t) * o.ld * 2) + T::chunk_of(t) * 16 + j * per;
+        for (int j = 0; j < kPer; ++j) {
+            const int q = t + j * THREADS;
+            off[j] = (uint32_t)(T::row_of(q) * o.ld * 2) + T::chunk_of(q) * 16;
+        }
     }
     // One of the next step's loads; `k_left` is the k that are left from the step on.  The
     // instruction takes its LDS address from m0 and each lane's 16 bytes follow the last one's.
@@ -380,7 +524,7 @@ struct Dma {
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                      :
                      : "s"(to), "v"(o), "s"(r)
-                     : "memory", "m0");
+                     : "memory");
     }
     __device__ __forceinline__ void advance() {
         s.base += s.step;
@@ -402,16 +546,18 @@ __device__ __forceinline__ void step_barrier() {
 // their way.  Within a step the fragments of the next 16 k are read while the matrix cores
 // work on the present ones.  The barrier between steps comes before the last 16 k of a step,
 // whose fragments are in registers by then: behind it the next step's first fragments are
-// read, the loads into the step just read out start, and the matrix cores are busy meanwhile.
+// read, the loads into the step just read out start, and the matrix cores are busy meanwhile
+// (the barrier sits where a quarter of those products is left).
 // Loads past the last step are started all the same (and write zeros, or k that are not
 // multiplied), so that the count of pending loads is the same in every step.
-template <int BM, int BN, int WM, int WN, int STEP, int STAGES, bool AK, bool BK>
+template <int BM, int BN, int WM, int WN, int STEP, int STAGES, int MS, bool AK, bool BK>
 __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) void mm_dma_kernel(const MmArgs g) {
     constexpr int THREADS = WM * WN * 64;
-    constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
+    constexpr int TM = BM / WM, TN = BN / WN, MI = TM / MS, NI = TN / MS;
+    using M = Mfma<MS>;
     using DA = Dma<AK, BM, STEP, THREADS>;
     using DB = Dma<BK, BN, STEP, THREADS>;
-    constexpr int ACH = DA::T::kChunks, BCH = DB::T::kChunks, SUB = STEP / 16;
+    constexpr int ACH = DA::T::kChunks, BCH = DB::T::kChunks, SUB = STEP / M::KS;
     static_assert(STAGES * (ACH + BCH) * 16 >= WM * WN * 32 * kRowPad * 4, "the epilogue's rows fit the tiles' LDS");
     __shared__ u32x4 lds[STAGES * (ACH + BCH)];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -423,11 +569,11 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
     const int k_all = (int)(min(g.k, k_lo + g.k_split) - k_lo);
     const int steps = (k_all + STEP - 1) / STEP;
 
-    f32x16 acc[MI][NI];
+    typename M::acc_t acc[MI][NI];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = f32x16{};
+        for (int j = 0; j < NI; ++j) acc[i][j] = typename M::acc_t{};
 
     DA da;
     DB db;
@@ -436,9 +582,9 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
     db.init(g.b, n0, k_lo);
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
     int k_left = k_all;
-    constexpr int LOADS = DA::kPer + DB::kPer;
+    constexpr int LOADS = DA::kPer + DB::kPer, EARLY = LOADS / 2;
     // load j of the step that comes next in the order of loading
-    auto issue = [&](int stage, int j) {
+    auto issue = [&](int stage, int j) __attribute__((always_inline)) {
         const uint32_t t = lds_at + stage * (ACH + BCH) * 16;
         if (j < DA::kPer) da.issue(t, j, k_left);
         else db.issue(t + ACH * 16, j - DA::kPer, k_left);
@@ -449,17 +595,18 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
         }
     };
     // fragment f of 16 k of a step, in the order in which the products take them
-    auto read = [&](int stage, int s, int f) {
+    auto read = [&](int stage, int s, int f) __attribute__((always_inline)) {
         const u32x4* t = lds + stage * (ACH + BCH);
         const int slot = s & 1;
         if (f >= 1 && f <= NI)
-            fb[slot][f - 1] = read_frag<BK, BN, STEP>(t + ACH, wn * TN + (f - 1) * 32, s * 16, lane);
+            fb[slot][f - 1] = read_frag<BK, BN, STEP, MS>(t + ACH, wn * TN + (f - 1) * MS, s * M::KS, lane);
         else {
             const int i = f == 0 ? 0 : f - NI;
-            fa[slot][i] = read_frag<AK, BM, STEP>(t, wm * TM + i * 32, s * 16, lane);
+            fa[slot][i] = read_frag<AK, BM, STEP, MS>(t, wm * TM + i * MS, s * M::KS, lane);
         }
     };
     constexpr int PENDING = (STAGES - 2) * LOADS;
+    constexpr int MF = MI * NI, BARX = MF * 3 / 4;
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i)
 #pragma unroll
@@ -468,33 +615,35 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
 #pragma unroll
     for (int f = 0; f < MI + NI; ++f) read(0, 0, f);
 #pragma unroll
-    for (int j = 0; j < LOADS / 2; ++j) issue(STAGES - 1, j);
+    for (int j = 0; j < EARLY; ++j) issue(STAGES - 1, j);
     for (int it = 0; it < steps; it += STAGES) {
 #pragma unroll
         for (int stage = 0; stage < STAGES; ++stage) {
             if (it + stage >= steps) break;
-            constexpr int MF = MI * NI;
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
                 const bool last = s + 1 == SUB;
-                if (last) step_barrier<PENDING>();
-                // Between two products: the reads of the next 16 k, and behind the barrier and in
-                // the next step's first 16 k half of a step's loads each.  The matrix cores are busy
-                // for 32 cycles with each product, which hides what issues in between.
+                // Between two products: the reads of the next fragments, and behind the barrier and
+                // in the next step's first products half of a step's loads each.
 #pragma unroll
                 for (int x = 0; x < MF; ++x) {
-                    acc[x / NI][x % NI] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        fa[s & 1][x / NI], fb[s & 1][x % NI], acc[x / NI][x % NI], 0, 0, 0);
+                    if (last && x == BARX) step_barrier<PENDING>();
+                    acc[x / NI][x % NI] = M::mul(fa[s & 1][x / NI], fb[s & 1][x % NI], acc[x / NI][x % NI]);
                     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int f = x * (MI + NI) / MF; f < (x + 1) * (MI + NI) / MF; ++f) {
-                        if (last) read(stage + 1 == STAGES ? 0 : stage + 1, 0, f);
-                        else read(stage, s + 1, f);
-                    }
-                    if (last || s == 0) {
-#pragma unroll
-                        for (int j = x * (LOADS / 2) / MF; j < (x + 1) * (LOADS / 2) / MF; ++j)
-                            issue(last ? stage : stage == 0 ? STAGES - 1 : stage - 1, last ? j : LOADS / 2 + j);
+                    if (last) {
+                        if (x >= BARX) {
+                            spread<MF - BARX, MI + NI>(x - BARX, [&](int f) __attribute__((always_inline)) {
+                                read(stage + 1 == STAGES ? 0 : stage + 1, 0, f);
+                            });
+                            spread<MF - BARX, EARLY>(
+                                x - BARX, [&](int j) __attribute__((always_inline)) { issue(stage, j); });
+                        }
+                    } else {
+                        spread<MF, MI + NI>(x, [&](int f) __attribute__((always_inline)) { read(stage, s + 1, f); });
+                        if (s == 0)
+                            spread<MF, LOADS - EARLY>(x, [&](int j) __attribute__((always_inline)) {
+                                issue(stage == 0 ? STAGES - 1 : stage - 1, EARLY + j);
+                            });
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -502,7 +651,7 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
         }
     }
     step_barrier<0>();  // the epilogue takes over the LDS that the last loads were written to
-    store_acc<MI, NI>(g, acc, (float*)lds + wave * 32 * kRowPad, m0 + wm * TM, n0 + wn * TN, lane);
+    store_acc<MS, MI, NI>(g, acc, (float*)lds + wave * 32 * kRowPad, m0 + wm * TM, n0 + wn * TN, lane);
 }
 
 // The splits' partial sums, joined in order, and the epilogue: rows are padded to 64 columns
@@ -511,47 +660,108 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const MmArgs g, int splits
     const int64_t t = t0 + (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row = t / per_row, col = (t - row * per_row) * 8, left = g.n - col;
     const int valid = row >= g.m || left <= 0 ? 0 : left < 8 ? (int)left : 8;
-    float v[8], u[8];
+    const float* part = g.part + row * g.n + col;
+    float v[8], u[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    for (int s = 0; s < splits; ++s) {
-        load_chunk(g.part + ((int64_t)s * g.m + row) * g.n + col, valid, u);
+    // eight splits' loads at a time, added in order
+    for (int s0 = 0; s0 < splits; s0 += 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += u[i];
+        for (int s = 0; s < 8; ++s) load_chunk(part + min(s0 + s, splits - 1) * (g.m * g.n), valid, u[s]);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = s0 + s < splits ? v[i] + u[s][i] : v[i];
     }
     epilogue(g.ep, row, g.n, col, valid, v);
 }
 
-#ifndef MM_CFG
-#define MM_BM 256
-#define MM_BN 256
-#define MM_CFG 256, 256, 2, 4, 64, 2
-#define MM_THREADS 512
-#endif
-const void* pick_dma(bool ak, bool bk) {
-    if (ak && bk) return (const void*)&mm_dma_kernel<MM_CFG, true, true>;
-    if (ak) return (const void*)&mm_dma_kernel<MM_CFG, true, false>;
-    return (const void*)&mm_dma_kernel<MM_CFG, false, false>;
+constexpr int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+// The layouts that occur: both operands k-major, the second free-major, both free-major.
+enum : int { kKK = 0, kKF = 1, kFF = 2 };
+int layout_of(bool ak, bool bk) { return ak ? (bk ? kKK : kKF) : kFF; }
+
+// The tile shapes.  `slots` workgroups are at work at once; `step_us` is the time of one step of
+// 64 k with one workgroup on a compute unit and with all slots taken, `tile_us` that of a
+// tile's start and epilogue.
+struct Shape {
+    int bm, bn, threads, slots;
+    double step_us[2], tile_us;
+    const void* kernel[3];
+};
+template <int BM, int BN, int WM, int WN, int STAGES>
+Shape shape(int slots, double alone_us, double full_us, double tile_us) {
+    return {BM, BN, WM * WN * 64, slots, {alone_us, full_us}, tile_us,
+            {(const void*)&mm_dma_kernel<BM, BN, WM, WN, kStep, STAGES, 16, true, true>,
+             (const void*)&mm_dma_kernel<BM, BN, WM, WN, kStep, STAGES, 16, true, false>,
+             (const void*)&mm_dma_kernel<BM, BN, WM, WN, kStep, STAGES, 16, false, false>}};
 }
-const void* pick_mm(bool ak, bool bk, bool codes) {
+constexpr int kShapes = 5;
+const Shape& shape_at(int i) {
+    static const Shape shapes[kShapes] = {
+        shape<256, 256, 2, 4, 2>(256, 1.38, 1.38, 10.0),
+        shape<128, 128, 2, 2, 2>(512, 0.78, 1.02, 5.0),
+        shape<64, 128, 1, 2, 3>(512, 0.55, 0.65, 4.0),
+        shape<128, 64, 2, 1, 3>(512, 0.55, 0.65, 4.0),
+        shape<32, 256, 1, 4, 4>(256, 0.5, 0.5, 5.0),
+    };
+    return shapes[i];
+}
+
+// Operands whose rows are whole 16-byte chunks go past the registers.
+bool chunked(int layout, int64_t m, int64_t n, int64_t k) {
+    return (layout == kFF ? m : k) % 8 == 0 && (layout == kKK ? k : n) % 8 == 0;
+}
+
+struct Plan {
+    int shape;  // -1: the tile staged through registers
+    int splits;
+};
+
+// The shape and the splits of the contraction that finish first: rounds of workgroups, each the
+// steps of its split, and for splits the time to write the partial sums and to join them.
+// Splits are what fills the chip where there are few tiles and many k.
+Plan plan(int layout, int64_t m, int64_t n, int64_t k) {
+    Plan best = {-1, 1};
+    double best_us = 0.0;
+    const bool fast = chunked(layout, m, n, k);
+    const int64_t steps = tiles_of(k, kStep);
+    for (int i = 0; i < (fast ? kShapes : 1); ++i) {
+        const Shape* s = fast ? &shape_at(i) : nullptr;
+        const int bm = fast ? s->bm : 128, bn = fast ? s->bn : 128, slots = fast ? s->slots : 512;
+        const double tile_us = fast ? s->tile_us : 8.0;
+        const int64_t tiles = tiles_of(m, bm) * tiles_of(n, bn);
+        for (int64_t splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : splits * 5 / 4) {
+            const int64_t per = tiles_of(steps, splits);
+            if (splits > 1 && (per < 4 || tiles_of(steps, per) < splits)) continue;
+            const int64_t rounds = tiles_of(tiles * splits, slots);
+            const double step_us = fast ? s->step_us[tiles * splits > 256] : 1.3;
+            double us = rounds * (per * step_us + tile_us);
+            if (splits > 1) us += 4.0 + splits * (double)(m * n) * 8.0 / 6e6;
+            if (best_us == 0.0 || us < best_us) {
+                best = {fast ? i : -1, (int)splits};
+                best_us = us;
+            }
+        }
+    }
+    return best;
+}
+
+const void* pick_mm(int layout, bool codes) {
     if (codes) return (const void*)&mm_kernel<128, 128, 2, 2, false, false, true>;
-    if (bk) return (const void*)&mm_kernel<128, 128, 2, 2, true, true, false>;
+    if (layout == kKK) return (const void*)&mm_kernel<128, 128, 2, 2, true, true, false>;
     return (const void*)&mm_kernel<128, 128, 2, 2, true, false, false>;
 }
 
-constexpr int kTile = 128;
-int64_t tiles_of(int64_t n, int64_t tile = kTile) { return (n + tile - 1) / tile; }
-
 }  // namespace
 
-// Few tiles leave compute units idle: the contraction is split until the workgroups fill
-// the chip, with at least 512 k per split.
-int mm_splits(int64_t m, int64_t n, int64_t k) {
-    const int64_t tiles = tiles_of(m) * tiles_of(n);
-    if (tiles <= 0) return 1;
-    const int64_t most = k / 512, wanted = 256 / tiles;
-    const int64_t s = wanted < most ? wanted : most;
-    return s < 2 ? 1 : s > 64 ? 64 : (int)s;
+bool mm_decodes(int64_t m, int64_t n) { return chunked(kFF, m, n, 0); }
+
+int64_t mm_part_bytes(bool a_kmajor, bool b_kmajor, int64_t m, int64_t n, int64_t k) {
+    if (m <= 0 || n <= 0) return 0;
+    const int splits = plan(layout_of(a_kmajor, b_kmajor), m, n, k).splits;
+    return splits > 1 ? splits * m * n * 4 : 0;
 }
 
 hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
@@ -561,32 +771,31 @@ hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
     g.m = p.m;
     g.n = p.n;
     g.k = p.k;
-    const bool dma = !p.b_codes && (p.a_kmajor ? p.k : p.m) % 8 == 0 && (p.b_kmajor ? p.k : p.n) % 8 == 0;
-    g.tiles_m = (int)tiles_of(p.m, dma ? MM_BM : kTile);
-    g.tiles_n = (int)tiles_of(p.n, dma ? MM_BN : kTile);
-    const int64_t steps = (p.k + kStep - 1) / kStep;
-    g.k_split = (steps + p.splits - 1) / p.splits * kStep;
-    g.part = p.splits > 1 ? p.part : nullptr;
+    const int layout = layout_of(p.a_kmajor, p.b_kmajor);
+    const Plan pl = plan(layout, p.m, p.n, p.k);
+    const Shape* s = pl.shape >= 0 && !p.b_codes ? &shape_at(pl.shape) : nullptr;
+    g.tiles_m = (int)tiles_of(p.m, s ? s->bm : 128);
+    g.tiles_n = (int)tiles_of(p.n, s ? s->bn : 128);
+    g.k_split = tiles_of(tiles_of(p.k, kStep), pl.splits) * kStep;
+    g.part = pl.splits > 1 ? p.part : nullptr;
     g.ep = p.ep;
-    const void* k = dma ? pick_dma(p.a_kmajor, p.b_kmajor) : pick_mm(p.a_kmajor, p.b_kmajor, p.b_codes != 0);
     void* args[] = {(void*)&g};
-    const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
-    hipError_t err = hipLaunchKernel(k, dim3((unsigned)tiles, (unsigned)p.splits), dim3(dma ? MM_THREADS : 256), args, 0, stream);
-    if (err != hipSuccess || p.splits == 1) return err;
-    int64_t per_row = (p.n + 63) / 64 * 8, t0 = 0;
-    int splits = p.splits;
+    hipError_t err = hipLaunchKernel(s ? s->kernel[layout] : pick_mm(layout, p.b_codes != 0),
+                                     dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)pl.splits),
+                                     dim3(s ? s->threads : 256), args, 0, stream);
+    if (err != hipSuccess || pl.splits == 1) return err;
+    int64_t per_row = tiles_of(p.n, 64) * 8, t0 = 0;
+    int splits = pl.splits;
     const int64_t chunks = p.m * per_row;
     void* jargs[] = {(void*)&g, (void*)&splits, (void*)&per_row, (void*)&t0};
     for (; t0 < chunks; t0 += kMaxGrid * 256) {
         const int64_t left = chunks - t0;
-        const int64_t blocks = left < kMaxGrid * 256 ? (left + 255) / 256 : kMaxGrid;
+        const int64_t blocks = left < kMaxGrid * 256 ? tiles_of(left, 256) : kMaxGrid;
         err = hipLaunchKernel((const void*)&mm_join_kernel, dim3((unsigned)blocks), dim3(256), jargs, 0, stream);
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
 }
-
-bool mm_decodes(int64_t m, int64_t n) { return m % 8 == 0 && n % 8 == 0; }
 
 // ---- column sums ------------------------------------------------------------------------
 
