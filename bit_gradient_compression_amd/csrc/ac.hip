@@ -12,65 +12,97 @@ namespace loco {
 namespace {
 
 constexpr int kAcThreads = 256;
+constexpr int kAcChunks = 2;  // per thread, all loaded before the first is worked
+constexpr int64_t kAcTile = kAcThreads * kAcChunks;
 
 // Chunk t of the tensor: rows are padded to whole blocks, so that a block never spans two
-// rows and its lanes stay together.
+// rows and its lanes stay together.  Rows that are whole blocks lie end to end and need no
+// division (FLAT: one row).
 struct ChunkAt {
-    int64_t row;
-    int64_t col;
+    int64_t row, col;
     int valid;
 };
+template <bool FLAT>
 __device__ __forceinline__ ChunkAt chunk_at(int64_t t, int64_t rows, int64_t cols, int64_t per_row) {
     ChunkAt a;
-    a.row = t / per_row;
+    if constexpr (FLAT) a.row = 0;
+    else if (rows * per_row < (int64_t)1 << 31) a.row = (uint32_t)t / (uint32_t)per_row;
+    else a.row = t / per_row;
     a.col = (t - a.row * per_row) * 8;
     const int64_t left = cols - a.col;
     a.valid = a.row >= rows || left <= 0 ? 0 : left < 8 ? (int)left : 8;
     return a;
 }
 
-template <typename T>
+template <typename T, bool FLAT>
 __global__ __launch_bounds__(kAcThreads) void ckpt_write_kernel(const T* x, CkptDev ck, int64_t rows, int64_t cols,
                                                                 int64_t per_row, int64_t t0) {
-    const int64_t t = t0 + (int64_t)blockIdx.x * kAcThreads + threadIdx.x;
-    const ChunkAt a = chunk_at(t, rows, cols, per_row);
-    float v[8];
-    load_chunk(x + a.row * cols + a.col, a.valid, v);
-    const uint32_t e = ckpt_exp(block_top(v, ck.block64));
-    store_codes(ck.codes + a.row * cols + a.col, a.valid, ckpt_codes(v, e));
-    const int per = ck.block64 ? 8 : 4;
-    if ((threadIdx.x & (per - 1)) == 0 && a.valid > 0)
-        ck.exps[a.row * ck.nblocks + a.col / (8 * per)] = (uint8_t)e;
+    const int64_t t = t0 + (int64_t)blockIdx.x * kAcTile + threadIdx.x;
+    ChunkAt a[kAcChunks];
+    RawChunk<T> raw[kAcChunks];
+#pragma unroll
+    for (int u = 0; u < kAcChunks; ++u) {
+        a[u] = chunk_at<FLAT>(t + u * kAcThreads, rows, cols, per_row);
+        raw[u].load(x + a[u].row * cols + a[u].col, a[u].valid);
+    }
+    const int per = ck.block64 ? 8 : 4, shift = ck.block64 ? 6 : 5;
+#pragma unroll
+    for (int u = 0; u < kAcChunks; ++u) {
+        float v[8];
+        raw[u].get(v);
+        const uint32_t e = ckpt_exp(block_top(v, ck.block64));
+        store_codes(ck.codes + a[u].row * cols + a[u].col, a[u].valid, ckpt_codes(v, e));
+        if ((threadIdx.x & (per - 1)) == 0 && a[u].valid > 0)
+            ck.exps[a[u].row * ck.nblocks + (a[u].col >> shift)] = (uint8_t)e;
+    }
 }
 
-template <typename T, int ACT>
+template <typename T, int ACT, bool FLAT>
 __global__ __launch_bounds__(kAcThreads) void ckpt_read_kernel(CkptDev ck, T* out, int64_t rows, int64_t cols,
                                                                int64_t per_row, int64_t t0) {
-    const int64_t t = t0 + (int64_t)blockIdx.x * kAcThreads + threadIdx.x;
-    const ChunkAt a = chunk_at(t, rows, cols, per_row);
-    if (a.valid <= 0) return;
-    const uint32_t e = ck.exps[a.row * ck.nblocks + a.col / (ck.block64 ? 64 : 32)];
-    float v[8];
-    decode_codes(load_codes(ck.codes + a.row * cols + a.col, a.valid), e, v);
-    act_chunk<ACT>(v);
-    store_chunk(out + a.row * cols + a.col, a.valid, v);
+    const int64_t t = t0 + (int64_t)blockIdx.x * kAcTile + threadIdx.x;
+    const int shift = ck.block64 ? 6 : 5;
+    ChunkAt a[kAcChunks];
+    u32x2 codes[kAcChunks];
+    uint32_t e[kAcChunks];
+#pragma unroll
+    for (int u = 0; u < kAcChunks; ++u) {
+        a[u] = chunk_at<FLAT>(t + u * kAcThreads, rows, cols, per_row);
+        codes[u] = load_codes(ck.codes + a[u].row * cols + a[u].col, a[u].valid);
+        e[u] = a[u].valid > 0 ? ck.exps[a[u].row * ck.nblocks + (a[u].col >> shift)] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kAcChunks; ++u) {
+        float v[8];
+        decode_codes(codes[u], e[u], v);
+        act_chunk<ACT>(v);
+        store_chunk(out + a[u].row * cols + a[u].col, a[u].valid, v);
+    }
 }
 
-template <typename T>
-const void* pick_read(int act) {
+template <typename T, bool FLAT>
+const void* pick_act(int act) {
     switch (act) {
-        case 1: return (const void*)&ckpt_read_kernel<T, 1>;
-        case 2: return (const void*)&ckpt_read_kernel<T, 2>;
-        case 3: return (const void*)&ckpt_read_kernel<T, 3>;
+        case 1: return (const void*)&ckpt_read_kernel<T, 1, FLAT>;
+        case 2: return (const void*)&ckpt_read_kernel<T, 2, FLAT>;
+        case 3: return (const void*)&ckpt_read_kernel<T, 3, FLAT>;
     }
-    return (const void*)&ckpt_read_kernel<T, 0>;
+    return (const void*)&ckpt_read_kernel<T, 0, FLAT>;
+}
+template <typename T>
+const void* pick_read(int act, bool flat) {
+    return flat ? pick_act<T, true>(act) : pick_act<T, false>(act);
+}
+template <typename T>
+const void* pick_write(bool flat) {
+    return flat ? (const void*)&ckpt_write_kernel<T, true> : (const void*)&ckpt_write_kernel<T, false>;
 }
 
 // Launches over all chunks, at most kMaxGrid workgroups at a time; args[5] points at t0.
 hipError_t launch_chunks(const void* k, void** args, int64_t* t0, int64_t chunks, hipStream_t stream) {
-    for (*t0 = 0; *t0 < chunks; *t0 += kMaxGrid * kAcThreads) {
+    for (*t0 = 0; *t0 < chunks; *t0 += kMaxGrid * kAcTile) {
         const int64_t left = chunks - *t0;
-        const int64_t blocks = left < kMaxGrid * kAcThreads ? (left + kAcThreads - 1) / kAcThreads : kMaxGrid;
+        const int64_t blocks = left < kMaxGrid * kAcTile ? (left + kAcTile - 1) / kAcTile : kMaxGrid;
         const hipError_t err = hipLaunchKernel(k, dim3((unsigned)blocks), dim3(kAcThreads), args, 0, stream);
         if (err != hipSuccess) return err;
     }
@@ -97,7 +129,7 @@ hipError_t launch_ckpt_write(const void* x, bool f32, int64_t rows, int64_t cols
     flatten(rows, cols, c);
     int64_t per_row = chunks_per_row(cols, c), t0 = 0;
     void* args[] = {(void*)&x, (void*)&c, (void*)&rows, (void*)&cols, (void*)&per_row, (void*)&t0};
-    const void* k = f32 ? (const void*)&ckpt_write_kernel<float> : (const void*)&ckpt_write_kernel<uint16_t>;
+    const void* k = f32 ? pick_write<float>(rows == 1) : pick_write<uint16_t>(rows == 1);
     return launch_chunks(k, args, &t0, rows * per_row, stream);
 }
 
@@ -107,7 +139,7 @@ hipError_t launch_ckpt_read(const CkptDev& ck, int64_t rows, int64_t cols, int a
     flatten(rows, cols, c);
     int64_t per_row = chunks_per_row(cols, c), t0 = 0;
     void* args[] = {(void*)&c, (void*)&out, (void*)&rows, (void*)&cols, (void*)&per_row, (void*)&t0};
-    return launch_chunks(f32 ? pick_read<float>(act) : pick_read<uint16_t>(act), args, &t0, rows * per_row, stream);
+    return launch_chunks(f32 ? pick_read<float>(act, rows == 1) : pick_read<uint16_t>(act, rows == 1), args, &t0, rows * per_row, stream);
 }
 
 }  // namespace loco

@@ -8,6 +8,8 @@
 namespace loco {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ---- chunks of eight elements ------------------------------------------------------
@@ -34,7 +36,8 @@ __device__ __forceinline__ void unpack_bf16x8(u32x4 w, float (&v)[8]) {
 __device__ __forceinline__ u32x4 pack_bf16x8(const float (&v)[8]) {
     u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16x2_rne(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i)  // one v_cvt_pk_bf16_f32 each
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v[2 * i], v[2 * i + 1]}), bf16x2));
     return w;
 }
 
@@ -85,6 +88,34 @@ __device__ __forceinline__ void store_chunk(float* p, int valid, const float (&v
             if (i < valid) p[i] = v[i];
     }
 }
+
+// A chunk as it lies in memory: half the registers of its values for bf16.
+template <typename T>
+struct RawChunk;
+template <>
+struct RawChunk<uint16_t> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t* p, int valid) {
+        if (valid >= 8) {
+            w = load16(p);
+        } else {
+            w = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < valid) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(w, v); }
+};
+template <>
+struct RawChunk<float> {
+    float w[8];
+    __device__ __forceinline__ void load(const float* p, int valid) { load_chunk(p, valid, w); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = w[i];
+    }
+};
 
 // A chunk of a buffer whose type is known at run time only (wave-uniform branch).
 __device__ __forceinline__ void load_chunk_any(const void* base, bool f32, int64_t at, int valid, float (&v)[8]) {
