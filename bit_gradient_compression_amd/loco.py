@@ -359,26 +359,35 @@ def loco_sparse_aggregate(peers, n: int, *, chunk: int, k: int, out, out_scale: 
 # together are its rows (tokens).  A checkpoint is a pair (codes int8, exps uint8), with
 # the block (32 or 64) given beside it.
 
-def _rows_cols(t, what):
-    if t.dim() < 1:
+# These calls are short beside a small kernel's launch, so the checks make few torch calls:
+# sizes and types first, then (_ptr) where each tensor lies.
+
+_F32 = (torch.float32,)
+_BF = (torch.bfloat16,)
+_FLOATS = (torch.float32, torch.bfloat16)
+_CODES = {torch.float32: LOCO_F32, torch.bfloat16: LOCO_BF16}
+
+
+def _rows_cols(t, what, dtypes):
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{what} must have at least one dimension")
-    cols = t.shape[-1]
-    return (t.numel() // cols if cols else math.prod(t.shape[:-1])), cols
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if len(shape) == 2:
+        return shape
+    cols = shape[-1]
+    return (t.numel() // cols if cols else math.prod(shape[:-1])), cols
 
 
-def _sized(t, numel: int, what: str, dtypes=None) -> None:
+def _sized(t, numel: int, what: str, dtypes) -> None:
     """t (None passes: the C call decides) must hold exactly numel elements of one of dtypes."""
     if t is None:
         return
     if t.numel() != numel:
         raise ValueError(f"{what} has {t.numel()} elements; the call needs {numel}")
-    if dtypes is not None and t.dtype not in dtypes:
+    if t.dtype not in dtypes:
         raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-
-
-_FLOATS = (torch.float32, torch.bfloat16)
-_BF = (torch.bfloat16,)
-_F32 = (torch.float32,)
 
 
 def _checkpoint(checkpoint, block, rows, cols, dev):
@@ -402,18 +411,18 @@ def loco_layer_norm(x, weight, bias, *, out, mean, rstd, eps: float = 1e-5, chec
     (float32, one per row) are written for the backward pass, and `checkpoint`, if given,
     with the 8-bit checkpoint of the output.  weight and bias may be None."""
     dev = _device()
-    rows, cols = _rows_cols(x, "x")
-    _sized(x, rows * cols, "x", _FLOATS)
+    rows, cols = _rows_cols(x, "x", _FLOATS)
     _sized(out, rows * cols, "out", (x.dtype,))
     param = weight if weight is not None else bias
-    _sized(param, cols, "weight" if weight is not None else "bias", _FLOATS)
-    _sized(bias, cols, "bias", None if param is None else (param.dtype,))
+    _sized(weight, cols, "weight", _FLOATS)
+    _sized(bias, cols, "bias", _FLOATS if weight is None else (weight.dtype,))
     _sized(mean, rows, "mean", _F32)
     _sized(rstd, rows, "rstd", _F32)
     ck = _checkpoint(checkpoint, block, rows, cols, dev)
-    st = load().loco_layer_norm(_ptr(x, dev), _dtype_code(x), _ptr(weight, dev), _ptr(bias, dev), _dtype_code(param),
-                                rows, cols, eps, _ptr(out, dev), _ptr(mean, dev), _ptr(rstd, dev),
-                                ck, _stream(stream, dev))
+    st = (_lib or load()).loco_layer_norm(
+        _ptr(x, dev), _CODES[x.dtype], _ptr(weight, dev), _ptr(bias, dev),
+        LOCO_F32 if param is None else _CODES[param.dtype], rows, cols, eps, _ptr(out, dev), _ptr(mean, dev),
+        _ptr(rstd, dev), ck, _stream(stream, dev))
     _check("loco_layer_norm", st)
 
 
@@ -423,21 +432,21 @@ def loco_layer_norm_backward(dy, x, weight, mean, rstd, *, dx, dweight=None, dbi
     rows, each optional.  workspace: a tensor of layer_norm_backward_workspace(rows, cols)
     bytes, not needed without dweight and dbias."""
     dev = _device()
-    rows, cols = _rows_cols(x, "x")
-    _sized(x, rows * cols, "x", _FLOATS)
+    rows, cols = _rows_cols(x, "x", _FLOATS)
     for t, what in ((dy, "dy"), (dx, "dx"), (residual, "residual")):
         _sized(t, rows * cols, what, (x.dtype,))
     _sized(weight, cols, "weight", _FLOATS)
     _sized(mean, rows, "mean", _F32)
     _sized(rstd, rows, "rstd", _F32)
     grad = dweight if dweight is not None else dbias
-    _sized(grad, cols, "dweight" if dweight is not None else "dbias", _FLOATS)
-    _sized(dbias, cols, "dbias", None if grad is None else (grad.dtype,))
-    st = load().loco_layer_norm_backward(_ptr(dy, dev), _ptr(x, dev), _dtype_code(x), _ptr(weight, dev),
-                                         _dtype_code(weight), _ptr(mean, dev), _ptr(rstd, dev), _ptr(residual, dev),
-                                         rows, cols, _ptr(dx, dev), _ptr(dweight, dev), _ptr(dbias, dev),
-                                         _dtype_code(grad), _ptr(workspace, dev), _nbytes(workspace),
-                                         _stream(stream, dev))
+    _sized(dweight, cols, "dweight", _FLOATS)
+    _sized(dbias, cols, "dbias", _FLOATS if dweight is None else (dweight.dtype,))
+    st = (_lib or load()).loco_layer_norm_backward(
+        _ptr(dy, dev), _ptr(x, dev), _CODES[x.dtype], _ptr(weight, dev),
+        LOCO_F32 if weight is None else _CODES[weight.dtype], _ptr(mean, dev), _ptr(rstd, dev), _ptr(residual, dev),
+        rows, cols, _ptr(dx, dev), _ptr(dweight, dev), _ptr(dbias, dev),
+        LOCO_F32 if grad is None else _CODES[grad.dtype], _ptr(workspace, dev), _nbytes(workspace),
+        _stream(stream, dev))
     _check("loco_layer_norm_backward", st)
 
 
@@ -448,22 +457,20 @@ def loco_layer_norm_backward_workspace(rows: int, cols: int) -> int:
 def loco_checkpoint_write(x, *, codes, exps, block: int = 64, stream=None) -> None:
     """The 8-bit checkpoint of x: codes int8 of x's shape, exps uint8, one per block of a row."""
     dev = _device()
-    rows, cols = _rows_cols(x, "x")
-    _sized(x, rows * cols, "x", _FLOATS)
+    rows, cols = _rows_cols(x, "x", _FLOATS)
     ck = _checkpoint((codes, exps), block, rows, cols, dev)
-    st = load().loco_checkpoint_write(_ptr(x, dev), _dtype_code(x), rows, cols,
-                                      ck, _stream(stream, dev))
+    st = (_lib or load()).loco_checkpoint_write(
+        _ptr(x, dev), _CODES[x.dtype], rows, cols, ck, _stream(stream, dev))
     _check("loco_checkpoint_write", st)
 
 
 def loco_checkpoint_read(codes, exps, *, out, block: int = 64, act: int = LOCO_ACT_NONE, stream=None) -> None:
     """out = act(the values of the checkpoint); the matrix's shape is out's."""
     dev = _device()
-    rows, cols = _rows_cols(out, "out")
-    _sized(out, rows * cols, "out", _FLOATS)
+    rows, cols = _rows_cols(out, "out", _FLOATS)
     ck = _checkpoint((codes, exps), block, rows, cols, dev)
-    st = load().loco_checkpoint_read(ck, rows, cols, act,
-                                     _ptr(out, dev), _dtype_code(out), _stream(stream, dev))
+    st = (_lib or load()).loco_checkpoint_read(
+        ck, rows, cols, act, _ptr(out, dev), _CODES[out.dtype], _stream(stream, dev))
     _check("loco_checkpoint_read", st)
 
 
@@ -473,19 +480,17 @@ def loco_linear(x, weight, *, out, bias=None, act: int = LOCO_ACT_NONE, residual
     `checkpoint`, if given, is written with the 8-bit checkpoint of the activation's input.
     bfloat16, out bfloat16 or float32."""
     dev = _device()
-    rows, k = _rows_cols(x, "x")
-    n, wk = _rows_cols(weight, "weight")
+    rows, k = _rows_cols(x, "x", _BF)
+    n, wk = _rows_cols(weight, "weight", _BF)
     if wk != k:
         raise ValueError(f"x has {k} columns, weight {wk}")
-    _sized(x, rows * k, "x", _BF)
-    _sized(weight, n * k, "weight", _BF)
     _sized(bias, n, "bias", _BF)
     _sized(residual, rows * n, "residual", _BF)
     _sized(out, rows * n, "out", _FLOATS)
     ck = _checkpoint(checkpoint, block, rows, n, dev)
-    st = load().loco_linear(_ptr(x, dev), _ptr(weight, dev), _ptr(bias, dev), _ptr(residual, dev), rows, n, k, act,
-                            _ptr(out, dev), _dtype_code(out), ck,
-                            _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    st = (_lib or load()).loco_linear(
+        _ptr(x, dev), _ptr(weight, dev), _ptr(bias, dev), _ptr(residual, dev), rows, n, k, act, _ptr(out, dev),
+        _CODES[out.dtype], ck, _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
     _check("loco_linear", st)
 
 
@@ -498,18 +503,16 @@ def loco_linear_input_grad(dy, weight, *, out, act: int = LOCO_ACT_NONE, checkpo
     """out = (dy weight) * act'(z) + residual, with z read from the 8-bit checkpoint of the
     activation's input (needed unless act is LOCO_ACT_NONE)."""
     dev = _device()
-    rows, n = _rows_cols(dy, "dy")
-    wn, k = _rows_cols(weight, "weight")
+    rows, n = _rows_cols(dy, "dy", _BF)
+    wn, k = _rows_cols(weight, "weight", _BF)
     if wn != n:
         raise ValueError(f"dy has {n} columns, weight {wn} rows")
-    _sized(dy, rows * n, "dy", _BF)
-    _sized(weight, n * k, "weight", _BF)
     _sized(residual, rows * k, "residual", _BF)
     _sized(out, rows * k, "out", _FLOATS)
     ck = _checkpoint(checkpoint, block, rows, k, dev)
-    st = load().loco_linear_input_grad(_ptr(dy, dev), _ptr(weight, dev), _ptr(residual, dev), rows, n, k, act,
-                                       ck, _ptr(out, dev), _dtype_code(out),
-                                       _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    st = (_lib or load()).loco_linear_input_grad(
+        _ptr(dy, dev), _ptr(weight, dev), _ptr(residual, dev), rows, n, k, act, ck, _ptr(out, dev), _CODES[out.dtype],
+        _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
     _check("loco_linear_input_grad", st)
 
 
@@ -523,17 +526,15 @@ def loco_linear_weight_grad(dy, checkpoint, *, out, block: int = 64, act: int = 
     over the rows; with accumulate, added to what they hold.  out and dbias are bfloat16
     or float32, alike."""
     dev = _device()
-    rows, n = _rows_cols(dy, "dy")
-    wn, k = _rows_cols(out, "out")
+    rows, n = _rows_cols(dy, "dy", _BF)
+    wn, k = _rows_cols(out, "out", _FLOATS)
     if wn != n:
         raise ValueError(f"dy has {n} columns, out {wn} rows")
-    _sized(dy, rows * n, "dy", _BF)
-    _sized(out, n * k, "out", _FLOATS)
     _sized(dbias, n, "dbias", (out.dtype,))
     ck = _checkpoint(checkpoint, block, rows, k, dev)
-    st = load().loco_linear_weight_grad(_ptr(dy, dev), ck, rows, n, k, act,
-                                        1 if accumulate else 0, _ptr(out, dev), _ptr(dbias, dev), _dtype_code(out),
-                                        _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    st = (_lib or load()).loco_linear_weight_grad(
+        _ptr(dy, dev), ck, rows, n, k, act, 1 if accumulate else 0, _ptr(out, dev), _ptr(dbias, dev),
+        _CODES[out.dtype], _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
     _check("loco_linear_weight_grad", st)
 
 
