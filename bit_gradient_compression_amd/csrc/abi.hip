@@ -524,12 +524,55 @@ LOCO_API int loco_checkpoint_read(const loco_checkpoint_t* ckpt, int64_t rows, i
                      exps_buf(ckpt, rows, cols, false)});
     if (st != LOCO_OK) return st;
     return hip_status(
-        launch_ckpt_read(ckpt_dev(ckpt, cols), rows, cols, act, out, out_dtype == LOCO_F32, (hipStream_t)stream));
+        launch_ckpt_read(ckpt_dev(ckpt, cols), rows, cols, act, out, cols,
+                                       out_dtype == LOCO_F32, (hipStream_t)stream));
 }
+
+namespace {
+
+// The three products of a linear layer, without their epilogues.
+MmParams product(const uint16_t* a, const uint16_t* b, int64_t m, int64_t n, int64_t k, bool a_kmajor, bool b_kmajor) {
+    MmParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = a;
+    p.b = b;
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    p.a_kmajor = a_kmajor;
+    p.b_kmajor = b_kmajor;
+    return p;
+}
+MmParams forward_product(const uint16_t* x, const uint16_t* w, int64_t rows, int64_t n, int64_t k) {
+    return product(x, w, rows, n, k, true, true);
+}
+MmParams input_grad_product(const uint16_t* dy, const uint16_t* w, int64_t rows, int64_t n, int64_t k) {
+    return product(dy, w, rows, k, n, true, false);
+}
+// The second operand is the checkpoint decoded to bf16 [rows, mm_padded(k)] in the workspace.
+MmParams weight_grad_product(const uint16_t* dy, const uint16_t* a, int64_t rows, int64_t n, int64_t k) {
+    MmParams p = product(dy, a, n, k, rows, false, false);
+    p.b_ld = mm_padded(k);
+    return p;
+}
+
+// The workspace of the weight gradient: the product's, the bias gradient's partial sums, the
+// decoded checkpoint.
+struct WeightGradSpace {
+    int64_t product, sums, decoded;
+    int64_t bytes() const { return product + sums + decoded; }
+};
+WeightGradSpace weight_grad_space(int64_t rows, int64_t n, int64_t k) {
+    if (n == 0) return {0, 0, 0};
+    return {round16(mm_workspace(weight_grad_product(nullptr, nullptr, rows, n, k))),
+            round16(col_sum_groups(rows, n) * n * 4), round16(rows * mm_padded(k) * 2)};
+}
+
+}  // namespace
 
 LOCO_API int64_t loco_linear_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
     if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
-    return mm_part_bytes(true, true, rows, out_features, in_features);
+    return mm_workspace(forward_product(nullptr, nullptr, rows, out_features, in_features));
 }
 
 LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16_t* bias, const uint16_t* residual,
@@ -553,27 +596,20 @@ LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16
                      exps_buf(ckpt, rows, n, true),
                      {workspace, need, true, true}});
     if (st != LOCO_OK) return st;
-    MmParams p;
-    memset(&p, 0, sizeof(p));
-    p.a = x;
-    p.b = weight;
-    p.m = rows;
-    p.n = n;
-    p.k = k;
-    p.a_kmajor = p.b_kmajor = 1;
+    MmParams p = forward_product(x, weight, rows, n, k);
     p.ep.bias = bias;
     p.ep.ckpt = ckpt_dev(ckpt, n);
     p.ep.act = act;
     p.ep.residual = residual;
     p.ep.out = out;
     p.ep.out_f32 = out_dtype == LOCO_F32;
-    p.part = (float*)workspace;
+    p.workspace = workspace;
     return hip_status(launch_mm(p, (hipStream_t)stream));
 }
 
 LOCO_API int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
     if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
-    return mm_part_bytes(true, false, rows, in_features, out_features);
+    return mm_workspace(input_grad_product(nullptr, nullptr, rows, out_features, in_features));
 }
 
 LOCO_API int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, const uint16_t* residual, int64_t rows,
@@ -596,29 +632,20 @@ LOCO_API int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, 
                      exps_buf(ckpt, rows, n, false),
                      {workspace, need, true, true}});
     if (st != LOCO_OK) return st;
-    MmParams p;
-    memset(&p, 0, sizeof(p));
-    p.a = dy;
-    p.b = weight;
-    p.m = rows;
-    p.n = n;
-    p.k = k;
-    p.a_kmajor = 1;
+    MmParams p = input_grad_product(dy, weight, rows, k, n);
     if (act != LOCO_ACT_NONE) p.ep.slope = ckpt_dev(ckpt, n);
     p.ep.act = act;
     p.ep.residual = residual;
     p.ep.out = dx;
     p.ep.out_f32 = out_dtype == LOCO_F32;
-    p.part = (float*)workspace;
+    p.workspace = workspace;
     return hip_status(launch_mm(p, (hipStream_t)stream));
 }
 
 LOCO_API int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features,
                                                    loco_act_t act) {
     if (check_product(rows, out_features, in_features) != LOCO_OK || !act_ok(act)) return 0;
-    return round16(mm_part_bytes(false, false, out_features, in_features, rows)) +
-           round16(col_sum_groups(rows, std::max<int64_t>(out_features, 1)) * out_features * 4) +
-           (mm_decodes(out_features, in_features) ? round16(rows * in_features * 2) : 0);
+    return weight_grad_space(rows, out_features, in_features).bytes();
 }
 
 LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t* ckpt, int64_t rows,
@@ -632,7 +659,8 @@ LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t
     if (st != LOCO_OK) return st;
     if (out_features == 0) return LOCO_OK;
     const int64_t n = out_features, k = in_features, gs = dtype_size(grad_dtype);
-    const int64_t need = loco_linear_weight_grad_workspace(rows, n, k, act);
+    const WeightGradSpace space = weight_grad_space(rows, n, k);
+    const int64_t need = space.bytes();
     if (workspace_bytes < need) return LOCO_ERR_INVALID;
     st = check_bufs({{dy, rows * n * 2, false, true},
                      codes_buf(ckpt, rows, k, false),
@@ -642,34 +670,21 @@ LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t
                      {workspace, need, true, true}});
     if (st != LOCO_OK) return st;
     const hipStream_t hs = (hipStream_t)stream;
-    // workspace: the product's partial sums, the bias gradient's, the decoded checkpoint
-    const int64_t part = round16(mm_part_bytes(false, false, n, k, rows)), sums = round16(col_sum_groups(rows, n) * n * 4);
+    char* at = (char*)workspace;
     if (k > 0) {
-        MmParams p;
-        memset(&p, 0, sizeof(p));
-        p.a = dy;
-        if (mm_decodes(n, k)) {
-            uint16_t* b = (uint16_t*)((char*)workspace + part + sums);
-            if (rows > 0 && launch_ckpt_read(ckpt_dev(ckpt, k), rows, k, act, b, false, hs) != hipSuccess)
-                return LOCO_ERR_HIP;
-            p.b = b;
-        } else {
-            p.b_codes = 1;
-            p.bq = ckpt_dev(ckpt, k);
-            p.bq_act = act;
-        }
-        p.m = n;
-        p.n = k;
-        p.k = rows;
+        uint16_t* a = (uint16_t*)(at + space.product + space.sums);
+        if (rows > 0 &&
+            launch_ckpt_read(ckpt_dev(ckpt, k), rows, k, act, a, mm_padded(k), false, hs) != hipSuccess)
+            return LOCO_ERR_HIP;
+        MmParams p = weight_grad_product(dy, a, rows, n, k);
         p.ep.out = dweight;
         p.ep.out_f32 = grad_dtype == LOCO_F32;
         p.ep.accumulate = accumulate != 0;
-        p.part = (float*)workspace;
-        const hipError_t e = launch_mm(p, hs);
-        if (e != hipSuccess) return LOCO_ERR_HIP;
+        p.workspace = at;
+        if (launch_mm(p, hs) != hipSuccess) return LOCO_ERR_HIP;
     }
     if (dbias)
-        return hip_status(launch_col_sum(dy, rows, n, (float*)((char*)workspace + part), dbias, grad_dtype == LOCO_F32,
+        return hip_status(launch_col_sum(dy, rows, n, (float*)(at + space.product), dbias, grad_dtype == LOCO_F32,
                                          accumulate != 0, hs));
     return LOCO_OK;
 }

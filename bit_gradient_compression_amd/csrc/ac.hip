@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kAcThreads) void ckpt_write_kernel(const T* x, Ckpt
 
 template <typename T, int ACT, bool FLAT>
 __global__ __launch_bounds__(kAcThreads) void ckpt_read_kernel(CkptDev ck, T* out, int64_t rows, int64_t cols,
-                                                               int64_t per_row, int64_t t0) {
+                                                               int64_t per_row, int64_t t0, int64_t ld) {
     const int64_t t = t0 + (int64_t)blockIdx.x * kAcTile + threadIdx.x;
     const int shift = ck.block64 ? 6 : 5;
     ChunkAt a[kAcChunks];
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kAcThreads) void ckpt_read_kernel(CkptDev ck, T* ou
         float v[8];
         decode_codes(codes[u], e[u], v);
         act_chunk<ACT>(v);
-        store_chunk(out + a[u].row * cols + a[u].col, a[u].valid, v);
+        store_chunk(out + a[u].row * ld + a[u].col, a[u].valid, v);
     }
 }
 
@@ -133,13 +133,17 @@ hipError_t launch_ckpt_write(const void* x, bool f32, int64_t rows, int64_t cols
     return launch_chunks(k, args, &t0, rows * per_row, stream);
 }
 
-hipError_t launch_ckpt_read(const CkptDev& ck, int64_t rows, int64_t cols, int act, void* out, bool f32,
+hipError_t launch_ckpt_read(const CkptDev& ck, int64_t rows, int64_t cols, int act, void* out, int64_t ld, bool f32,
                             hipStream_t stream) {
     CkptDev c = ck;
-    flatten(rows, cols, c);
+    if (ld == cols) {
+        flatten(rows, cols, c);
+        ld = cols;
+    }
     int64_t per_row = chunks_per_row(cols, c), t0 = 0;
-    void* args[] = {(void*)&c, (void*)&out, (void*)&rows, (void*)&cols, (void*)&per_row, (void*)&t0};
-    return launch_chunks(f32 ? pick_read<float>(act, rows == 1) : pick_read<uint16_t>(act, rows == 1), args, &t0, rows * per_row, stream);
+    void* args[] = {(void*)&c, (void*)&out, (void*)&rows, (void*)&cols, (void*)&per_row, (void*)&t0, (void*)&ld};
+    return launch_chunks(f32 ? pick_read<float>(act, rows == 1) : pick_read<uint16_t>(act, rows == 1), args, &t0,
+                         rows * per_row, stream);
 }
 
 }  // namespace loco

@@ -55,7 +55,8 @@ hipError_t launch_ln_bwd(const LnBwdParams& p, hipStream_t stream);
 // ---- activation checkpoints ----------------------------------------------------------
 
 hipError_t launch_ckpt_write(const void* x, bool f32, int64_t rows, int64_t cols, const CkptDev& c, hipStream_t stream);
-hipError_t launch_ckpt_read(const CkptDev& c, int64_t rows, int64_t cols, int act, void* out, bool f32,
+// out: rows of `ld` elements, of which cols are written.
+hipError_t launch_ckpt_read(const CkptDev& c, int64_t rows, int64_t cols, int act, void* out, int64_t ld, bool f32,
                             hipStream_t stream);
 
 // ---- matrix products -----------------------------------------------------------------
@@ -76,22 +77,20 @@ struct MmEpilogue {
 };
 
 // C[m, n] = sum over k of A B, with A [m, k] (a_kmajor) or [k, m], B [n, k] (b_kmajor) or
-// [k, n], row-major bf16; with b_codes, B is the checkpoint bq [k, n] through bq_act.
+// [k, n], row-major bf16.
 struct MmParams {
     const uint16_t* a;
     const uint16_t* b;
-    CkptDev bq;
-    int b_codes, bq_act;
     int64_t m, n, k;
+    int64_t b_ld;  // elements per row of B; 0: as many as it has columns
     int a_kmajor, b_kmajor;
     MmEpilogue ep;
-    float* part;  // mm_part_bytes bytes
+    void* workspace;  // mm_workspace bytes
 };
+int64_t mm_workspace(const MmParams& p);
 hipError_t launch_mm(const MmParams& p, hipStream_t stream);
-// Partial sums of a product whose contraction is worked in splits; 0: it is not split.
-int64_t mm_part_bytes(bool a_kmajor, bool b_kmajor, int64_t m, int64_t n, int64_t k);
-// Whether C [m, n] with a checkpointed B is worked from B decoded to bf16 beforehand.
-bool mm_decodes(int64_t m, int64_t n);
+// The row length at which an operand need not be copied.
+int64_t mm_padded(int64_t n);
 
 // out[n] = sum over the rows of x [rows, n]; part [col_sum_groups][n].
 int64_t col_sum_groups(int64_t rows, int64_t n);

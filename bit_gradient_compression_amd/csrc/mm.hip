@@ -8,7 +8,7 @@
 // by ds_read_b64_tr_b16.
 //   linear              x [T, K] k-major,      W [N, K] k-major
 //   linear_input_grad   dy [T, N] k-major,     W [N, K] free-major
-//   linear_weight_grad  dy [T, N] free-major,  checkpoint [T, K] free-major, decoded
+//   linear_weight_grad  dy [T, N] free-major,  decoded checkpoint [T, K] free-major
 //
 // A workgroup computes a BM x BN tile in steps of 64 k.  Both operands' tiles go through LDS
 // in two buffers: the next step's loads are in flight while this step's tiles are
@@ -118,79 +118,32 @@ __device__ __forceinline__ bf16x8 read_frag(const u32x4* tile, int free0, int k0
 // An operand: [free, k] (k-major) or [k, free], row-major with `ld` elements per row.
 struct Operand {
     const uint16_t* p;
-    const int8_t* codes;
-    const uint8_t* exps;
-    int64_t free, k, ld, nblocks;
-    int block_shift, act;
+    int64_t free, k, ld;
 };
 
 // The eight elements at (row, col) of a rows x cols matrix; 0 outside.
 __device__ __forceinline__ u32x4 load_bf16(const Operand& o, int64_t row, int64_t col, int64_t rows, int64_t cols) {
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if (row < rows && col < cols) {
-        const uint16_t* p = o.p + row * o.ld + col;
-        if (cols - col >= 8) {
-            w = load16(p);
-        } else {
-            const int n = (int)(cols - col);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-        }
-    }
-    return w;
+    RawChunk<uint16_t> c;
+    const int64_t left = cols - col;
+    c.load(o.p + row * o.ld + col, row < rows && left > 0 ? (left < 8 ? (int)left : 8) : 0);
+    return c.w;
 }
 
-// Raw form of a staged chunk: bf16 elements, or codes with their byte.
-template <bool CODES>
-struct Raw;
-template <>
-struct Raw<false> {
-    u32x4 w;
-    __device__ __forceinline__ void load(const Operand& o, int64_t row, int64_t col, int64_t rows, int64_t cols) {
-        w = load_bf16(o, row, col, rows, cols);
-    }
-    __device__ __forceinline__ u32x4 value(const Operand&) const { return w; }
-};
-template <>
-struct Raw<true> {
-    u32x2 w;
-    uint32_t e;
-    __device__ __forceinline__ void load(const Operand& o, int64_t row, int64_t col, int64_t rows, int64_t cols) {
-        w = u32x2{0u, 0u};
-        e = 0;
-        if (row < rows && col < cols) {
-            const int64_t left = cols - col;
-            w = load_codes(o.codes + row * o.ld + col, left < 8 ? (int)left : 8);
-            e = o.exps[row * o.nblocks + (col >> o.block_shift)];
-        }
-    }
-    // bf16 holds a code's value exactly; an activation's value is rounded to the nearest bf16,
-    // as the forward pass's product had it.
-    __device__ __forceinline__ u32x4 value(const Operand& o) const {
-        float v[8];
-        decode_codes(w, e, v);
-        act_chunk_any(o.act, v);
-        return pack_bf16x8(v);
-    }
-};
-
-template <bool KMAJOR, int W, int THREADS, bool CODES>
+template <bool KMAJOR, int W, int THREADS>
 struct Stage {
     using T = Tile<KMAJOR, W, kStep>;
     static constexpr int kPer = T::kChunks / THREADS;
-    Raw<CODES> raw[kPer];
+    u32x4 raw[kPer];
     __device__ __forceinline__ void load(const Operand& o, int64_t free0, int64_t k0) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int q = j * THREADS + threadIdx.x, r = T::row_of(q), c = T::chunk_of(q) * 8;
-            if constexpr (KMAJOR) raw[j].load(o, free0 + r, k0 + c, o.free, o.k);
-            else raw[j].load(o, k0 + r, free0 + c, o.k, o.free);
+            raw[j] = KMAJOR ? load_bf16(o, free0 + r, k0 + c, o.free, o.k) : load_bf16(o, k0 + r, free0 + c, o.k, o.free);
         }
     }
-    __device__ __forceinline__ void store(const Operand& o, u32x4* tile) const {
+    __device__ __forceinline__ void store(u32x4* tile) const {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) tile[j * THREADS + threadIdx.x] = raw[j].value(o);
+        for (int j = 0; j < kPer; ++j) tile[j * THREADS + threadIdx.x] = raw[j];
     }
 };
 
@@ -410,7 +363,7 @@ __device__ __forceinline__ void store_acc(const MmArgs& g, const typename Mfma<M
     }
 }
 
-template <int BM, int BN, int WM, int WN, bool AK, bool BK, bool CODES>
+template <int BM, int BN, int WM, int WN, bool AK, bool BK>
 __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
     constexpr int THREADS = WM * WN * 64;
     constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
@@ -432,13 +385,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x16{};
 
-    Stage<AK, BM, THREADS, false> sa;
-    Stage<BK, BN, THREADS, CODES> sb;
+    Stage<AK, BM, THREADS> sa;
+    Stage<BK, BN, THREADS> sb;
     if (steps > 0) {
         sa.load(g.a, m0, k_lo);
         sb.load(g.b, n0, k_lo);
-        sa.store(g.a, lds);
-        sb.store(g.b, lds + ACH);
+        sa.store(lds);
+        sb.store(lds + ACH);
     }
     __syncthreads();
     for (int it = 0; it < steps; ++it) {
@@ -464,8 +417,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
         }
         if (more) {
             u32x4* next = lds + ((it + 1) & 1) * (ACH + BCH);
-            sa.store(g.a, next);
-            sb.store(g.b, next + ACH);
+            sa.store(next);
+            sb.store(next + ACH);
         }
         __syncthreads();
     }
@@ -709,10 +662,11 @@ const Shape& shape_at(int i) {
     return shapes[i];
 }
 
-// Operands whose rows are whole 16-byte chunks go past the registers.
-bool chunked(int layout, int64_t m, int64_t n, int64_t k) {
-    return (layout == kFF ? m : k) % 8 == 0 && (layout == kKK ? k : n) % 8 == 0;
-}
+// Rows of whole 16-byte chunks can go past the registers.  A copy of an operand in such rows
+// costs its bytes twice; that is cheap beside a large product, whose steps are faster by half.
+bool chunked(const Operand& o) { return o.ld % 8 == 0; }
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+double copy_us(const Operand& o) { return 3.0 + (double)(o.free * o.k) * 4.0 / 4.5e6; }
 
 struct Plan {
     int shape;  // -1: the tile staged through registers
@@ -722,25 +676,24 @@ struct Plan {
 // The shape and the splits of the contraction that finish first: rounds of workgroups, each the
 // steps of its split, and for splits the time to write the partial sums and to join them.
 // Splits are what fills the chip where there are few tiles and many k.
-Plan plan(int layout, int64_t m, int64_t n, int64_t k) {
-    Plan best = {-1, 1};
+Plan plan(const Operand& a, const Operand& b) {
+    const int64_t m = a.free, n = b.free, steps = tiles_of(a.k, kStep);
+    const bool fast = chunked(a) && chunked(b);
+    const double copies = (chunked(a) ? 0.0 : copy_us(a)) + (chunked(b) ? 0.0 : copy_us(b));
+    Plan best = {0, 1};
     double best_us = 0.0;
-    const bool fast = chunked(layout, m, n, k);
-    const int64_t steps = tiles_of(k, kStep);
-    for (int i = 0; i < (fast ? kShapes : 1); ++i) {
-        const Shape* s = fast ? &shape_at(i) : nullptr;
-        const int bm = fast ? s->bm : 128, bn = fast ? s->bn : 128, slots = fast ? s->slots : 512;
-        const double tile_us = fast ? s->tile_us : 8.0;
-        const int64_t tiles = tiles_of(m, bm) * tiles_of(n, bn);
+    for (int i = fast ? 0 : -1; i < kShapes; ++i) {
+        // 300 TFLOP/s through the registers
+        const Shape s = i >= 0 ? shape_at(i) : Shape{128, 128, 256, 512, {0.9, 1.3}, 8.0, {}};
+        const int64_t tiles = tiles_of(m, s.bm) * tiles_of(n, s.bn);
         for (int64_t splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : splits * 5 / 4) {
             const int64_t per = tiles_of(steps, splits);
             if (splits > 1 && (per < 4 || tiles_of(steps, per) < splits)) continue;
-            const int64_t rounds = tiles_of(tiles * splits, slots);
-            const double step_us = fast ? s->step_us[tiles * splits > 256] : 1.3;
-            double us = rounds * (per * step_us + tile_us);
+            const int64_t rounds = tiles_of(tiles * splits, s.slots);
+            double us = rounds * (per * s.step_us[tiles * splits > 256] + s.tile_us) + (i >= 0 ? copies : 0.0);
             if (splits > 1) us += 4.0 + splits * (double)(m * n) * 8.0 / 6e6;
             if (best_us == 0.0 || us < best_us) {
-                best = {fast ? i : -1, (int)splits};
+                best = {i, (int)splits};
                 best_us = us;
             }
         }
@@ -748,41 +701,93 @@ Plan plan(int layout, int64_t m, int64_t n, int64_t k) {
     return best;
 }
 
-const void* pick_mm(int layout, bool codes) {
-    if (codes) return (const void*)&mm_kernel<128, 128, 2, 2, false, false, true>;
-    if (layout == kKK) return (const void*)&mm_kernel<128, 128, 2, 2, true, true, false>;
-    return (const void*)&mm_kernel<128, 128, 2, 2, true, false, false>;
+const void* pick_mm(int layout) {
+    if (layout == kKK) return (const void*)&mm_kernel<128, 128, 2, 2, true, true>;
+    if (layout == kKF) return (const void*)&mm_kernel<128, 128, 2, 2, true, false>;
+    return (const void*)&mm_kernel<128, 128, 2, 2, false, false>;
+}
+
+// An operand's copy in rows of `ld` elements, zeros past its columns: a k-major operand's zeros
+// take part in the products.
+__global__ __launch_bounds__(256) void pad_kernel(const uint16_t* in, int64_t rows, int64_t cols, uint16_t* out,
+                                                  int64_t ld, int64_t t0) {
+    const int64_t t = t0 + (int64_t)blockIdx.x * 256 + threadIdx.x, per_row = ld / 8;
+    const int64_t row = rows * per_row < (int64_t)1 << 31 ? (uint32_t)t / (uint32_t)per_row : t / per_row;
+    if (row >= rows) return;
+    const int64_t col = (t - row * per_row) * 8, left = cols - col;
+    RawChunk<uint16_t> c;
+    c.load(in + row * cols + col, left < 8 ? (int)left : 8);
+    store16(out + row * ld + col, c.w);
+}
+
+hipError_t pad(Operand& o, bool kmajor, uint16_t* to, hipStream_t stream) {
+    int64_t rows = kmajor ? o.free : o.k, cols = kmajor ? o.k : o.free, ld = padded(cols), t0 = 0;
+    const uint16_t* from = o.p;
+    void* args[] = {(void*)&from, (void*)&rows, (void*)&cols, (void*)&to, (void*)&ld, (void*)&t0};
+    const int64_t chunks = rows * (ld / 8);
+    for (; t0 < chunks; t0 += kMaxGrid * 256) {
+        const int64_t left = chunks - t0;
+        const int64_t blocks = left < kMaxGrid * 256 ? tiles_of(left, 256) : kMaxGrid;
+        const hipError_t err = hipLaunchKernel((const void*)&pad_kernel, dim3((unsigned)blocks), dim3(256), args, 0, stream);
+        if (err != hipSuccess) return err;
+    }
+    o.p = to;
+    o.ld = ld;
+    if (kmajor) o.k = ld;
+    return hipSuccess;
+}
+
+Operand operand_a(const MmParams& p) { return {p.a, p.m, p.k, p.a_kmajor ? p.k : p.m}; }
+Operand operand_b(const MmParams& p) { return {p.b, p.n, p.k, p.b_ld ? p.b_ld : p.b_kmajor ? p.k : p.n}; }
+
+// The workspace of a product: partial sums, then the operands' copies.
+struct Spaces {
+    int64_t part, a, b;
+};
+Spaces spaces(const MmParams& p, const Plan& pl) {
+    auto round16 = [](int64_t n) { return (n + 15) / 16 * 16; };
+    const Operand a = operand_a(p), b = operand_b(p);
+    Spaces s = {pl.splits > 1 ? round16(pl.splits * p.m * p.n * 4) : 0, 0, 0};
+    if (pl.shape >= 0 && !chunked(a)) s.a = (p.a_kmajor ? p.m : p.k) * padded(p.a_kmajor ? p.k : p.m) * 2;
+    if (pl.shape >= 0 && !chunked(b)) s.b = (p.b_kmajor ? p.n : p.k) * padded(p.b_kmajor ? p.k : p.n) * 2;
+    return s;
 }
 
 }  // namespace
 
-bool mm_decodes(int64_t m, int64_t n) { return chunked(kFF, m, n, 0); }
+int64_t mm_padded(int64_t n) { return padded(n); }
 
-int64_t mm_part_bytes(bool a_kmajor, bool b_kmajor, int64_t m, int64_t n, int64_t k) {
-    if (m <= 0 || n <= 0) return 0;
-    const int splits = plan(layout_of(a_kmajor, b_kmajor), m, n, k).splits;
-    return splits > 1 ? splits * m * n * 4 : 0;
+int64_t mm_workspace(const MmParams& p) {
+    if (p.m <= 0 || p.n <= 0) return 0;
+    const Spaces s = spaces(p, plan(operand_a(p), operand_b(p)));
+    return s.part + s.a + s.b;
 }
 
 hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
     MmArgs g;
-    g.a = {p.a, nullptr, nullptr, p.m, p.k, p.a_kmajor ? p.k : p.m, 0, 0, 0};
-    g.b = {p.b, p.bq.codes, p.bq.exps, p.n, p.k, p.b_kmajor ? p.k : p.n, p.bq.nblocks, p.bq.block64 ? 6 : 5, p.bq_act};
+    g.a = operand_a(p);
+    g.b = operand_b(p);
+    const Plan pl = plan(g.a, g.b);
+    const Spaces space = spaces(p, pl);
+    char* at = (char*)p.workspace;
+    hipError_t err = hipSuccess;
+    if (space.a) err = pad(g.a, p.a_kmajor, (uint16_t*)(at + space.part), stream);
+    if (err == hipSuccess && space.b) err = pad(g.b, p.b_kmajor, (uint16_t*)(at + space.part + space.a), stream);
+    if (err != hipSuccess) return err;
     g.m = p.m;
     g.n = p.n;
-    g.k = p.k;
+    g.k = g.a.k;  // with the zeros of a copy
     const int layout = layout_of(p.a_kmajor, p.b_kmajor);
-    const Plan pl = plan(layout, p.m, p.n, p.k);
-    const Shape* s = pl.shape >= 0 && !p.b_codes ? &shape_at(pl.shape) : nullptr;
+    const Shape* s = pl.shape >= 0 ? &shape_at(pl.shape) : nullptr;
     g.tiles_m = (int)tiles_of(p.m, s ? s->bm : 128);
     g.tiles_n = (int)tiles_of(p.n, s ? s->bn : 128);
     g.k_split = tiles_of(tiles_of(p.k, kStep), pl.splits) * kStep;
-    g.part = pl.splits > 1 ? p.part : nullptr;
+    g.part = pl.splits > 1 ? (float*)at : nullptr;
     g.ep = p.ep;
     void* args[] = {(void*)&g};
-    hipError_t err = hipLaunchKernel(s ? s->kernel[layout] : pick_mm(layout, p.b_codes != 0),
-                                     dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)pl.splits),
-                                     dim3(s ? s->threads : 256), args, 0, stream);
+    err = hipLaunchKernel(s ? s->kernel[layout] : pick_mm(layout),
+                          dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)pl.splits),
+                          dim3(s ? s->threads : 256), args, 0, stream);
     if (err != hipSuccess || pl.splits == 1) return err;
     int64_t per_row = tiles_of(p.n, 64) * 8, t0 = 0;
     int splits = pl.splits;

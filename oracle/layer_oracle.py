@@ -63,9 +63,11 @@ def checkpoint_write(x, block):
         fine = np.isfinite(v).all(1)
         top = np.where(fine, np.abs(np.where(np.isfinite(v), v, 0.0)).max(1), 0.0)
         s = np.full(rows, -126)
-        for r in range(rows):
-            while top[r] >= 127.5 * 2.0 ** int(s[r]):
-                s[r] += 1
+        while True:
+            small = top >= 127.5 * 2.0 ** s.astype(np.float64)
+            if not small.any():
+                break
+            s += small
         exps[:, b] = np.where(fine, s + 127, 255)
         q = np.rint(np.where(np.isfinite(v), v, 0.0) * 2.0 ** (-s[:, None].astype(np.float64)))
         codes[:, lo:hi] = np.where(fine[:, None], q, 0)

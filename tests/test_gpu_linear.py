@@ -233,7 +233,31 @@ def test_weight_grad_of_a_lost_block(gpu_lib):
     assert torch.equal(out[:, :64], clean[:, :64]) and torch.equal(out[:, 128:], clean[:, 128:])
 
 
-# -- the calls together -----------------------------------------------------------------
+# -- every tile shape, with rows, columns and k that end inside a tile -------------------
+
+# (m, n, k) of the product: the large tile, the middle one, the small ones with either side
+# short, few rows with the contraction split, rows that are not whole chunks and are copied
+# or (few) staged through registers
+TILES = [(2100, 4200, 136), (4000, 4400, 72), (1000, 1100, 200), (70000, 40, 72), (20, 9000, 1032), (16, 4096, 11008),
+         (2100, 4200, 137), (2101, 4201, 515), (701, 700, 65), (260, 264, 4136)]
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_linear_tiles(gpu_lib, m, n, k):
+    check_linear(gpu_lib, m, n, k, "silu", block=32)
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_input_grad_tiles(gpu_lib, m, n, k):
+    check_input_grad(gpu_lib, m, k, n, "gelu", True)
+
+
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_weight_grad_tiles(gpu_lib, m, n, k):
+    check_weight_grad(gpu_lib, k, m, n, "none", F32, accumulate=True)
+
+
+# -- the calls together -------------------------------------------------------------------------------------------------------------------------------
 
 def test_same_call_same_bits(gpu_lib):
     x, w, b = randn(1, 190, 2100), randn(2, 150, 2100), randn(3, 150)
