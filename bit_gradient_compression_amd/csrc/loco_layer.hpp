@@ -144,7 +144,7 @@ template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == 1) return z < 0.0f ? 0.0f : z;  // a NaN stays one
     else if constexpr (ACT == 2)
-        return z * sigmoid(kGelu2C * z * __builtin_fmaf(kGeluA * z, z, 1.0f));
+        return z * sigmoid(z * __builtin_fmaf(kGelu2C * kGeluA * z, z, kGelu2C));
     else if constexpr (ACT == 3) return z * sigmoid(z);
     else return z;
 }
@@ -158,17 +158,16 @@ __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& q) {
     q = t * s;
 }
 
-// The derivative of act_value.  Past |z| = 16 GELU's second term is 0 in fp32 while its
-// factors overflow, so it is cut there; a NaN stays one.
+// The derivative of act_value.  GELU's second term is 0 in fp32 past |z| = 16, where its factors
+// overflow, so it takes z held within that; a NaN reaches the result through s.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == 1) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
     else if constexpr (ACT == 2) {
-        const float z2 = z * z;
         float s, q;
-        sigmoid_pair(kGelu2C * z * __builtin_fmaf(kGeluA, z2, 1.0f), s, q);
-        const float t = z * (s * q) * (kGelu2C * __builtin_fmaf(3.0f * kGeluA, z2, 1.0f));
-        return s + (__builtin_fabsf(z) < 16.0f ? t : z * 0.0f);
+        sigmoid_pair(z * __builtin_fmaf(kGelu2C * kGeluA * z, z, kGelu2C), s, q);
+        const float c = __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f);
+        return __builtin_fmaf(c * (s * q), __builtin_fmaf(3.0f * kGelu2C * kGeluA * c, c, kGelu2C), s);
     } else if constexpr (ACT == 3) {
         float s, q;
         sigmoid_pair(z, s, q);

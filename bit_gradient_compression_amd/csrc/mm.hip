@@ -653,11 +653,11 @@ Shape shape(int slots, double alone_us, double full_us, double tile_us) {
 constexpr int kShapes = 5;
 const Shape& shape_at(int i) {
     static const Shape shapes[kShapes] = {
-        shape<256, 256, 2, 4, 2>(256, 1.38, 1.38, 10.0),
-        shape<128, 128, 2, 2, 2>(512, 0.78, 1.02, 5.0),
-        shape<64, 128, 1, 2, 3>(512, 0.55, 0.65, 4.0),
-        shape<128, 64, 2, 1, 3>(512, 0.55, 0.65, 4.0),
-        shape<32, 256, 1, 4, 4>(256, 0.5, 0.5, 5.0),
+        shape<256, 256, 2, 4, 2>(256, 1.38, 1.38, 12.0),
+        shape<128, 128, 2, 2, 2>(512, 0.78, 1.02, 5.5),
+        shape<64, 128, 1, 2, 3>(512, 0.55, 0.65, 5.0),
+        shape<128, 64, 2, 1, 3>(512, 0.55, 0.65, 5.0),
+        shape<32, 256, 1, 4, 4>(256, 0.48, 0.48, 2.5),
     };
     return shapes[i];
 }
@@ -806,9 +806,24 @@ hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
 
 namespace {
 
-// Partial sums of 512 columns per workgroup over every gridDim.y-th group of four rows, one
-// row per wave.
-__global__ __launch_bounds__(256) void col_sum_kernel(const uint16_t* x, int64_t rows, int64_t n, float* part) {
+// A column's sum on its way out.
+struct ColOut {
+    void* p;
+    int f32, accumulate;
+    __device__ __forceinline__ void put(int64_t c, float v) const {
+        if (f32) {
+            float* o = (float*)p + c;
+            *o = accumulate ? v + *o : v;
+        } else {
+            uint16_t* o = (uint16_t*)p + c;
+            *o = bf16_rne(accumulate ? v + __uint_as_float((uint32_t)*o << 16) : v);
+        }
+    }
+};
+
+// Sums of 512 columns per workgroup over every gridDim.y-th group of four rows, one row per
+// wave: partial sums, or with one group the result.
+__global__ __launch_bounds__(256) void col_sum_kernel(const uint16_t* x, int64_t rows, int64_t n, float* part, ColOut out) {
     __shared__ float join[4][512];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t col = (int64_t)blockIdx.x * 512 + lane * 8, left = n - col;
@@ -827,28 +842,36 @@ __global__ __launch_bounds__(256) void col_sum_kernel(const uint16_t* x, int64_t
     __syncthreads();
     for (int c = threadIdx.x; c < 512; c += 256) {
         const int64_t at = (int64_t)blockIdx.x * 512 + c;
-        if (at < n) part[blockIdx.y * n + at] = (join[0][c] + join[1][c]) + (join[2][c] + join[3][c]);
+        const float v = (join[0][c] + join[1][c]) + (join[2][c] + join[3][c]);
+        if (at < n) {
+            if (gridDim.y == 1) out.put(at, v);
+            else part[blockIdx.y * n + at] = v;
+        }
     }
 }
 
-__global__ __launch_bounds__(256) void col_join_kernel(const float* part, int64_t groups, int64_t n, void* out, int f32,
-                                                       int accumulate) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
+// The groups' partial sums: 32 columns per workgroup, 32 threads down the groups.
+__global__ __launch_bounds__(1024) void col_join_kernel(const float* part, int64_t groups, int64_t n, ColOut out) {
+    __shared__ float s[32][33];
+    const int cl = threadIdx.x & 31, g0 = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + cl;
     float v = 0.0f;
-#pragma unroll 8
-    for (int64_t g = 0; g < groups; ++g) v += part[g * n + c];
-    if (f32) ((float*)out)[c] = accumulate ? v + ((float*)out)[c] : v;
-    else {
-        uint16_t* o = (uint16_t*)out + c;
-        *o = bf16_rne(accumulate ? v + __uint_as_float((uint32_t)*o << 16) : v);
+    if (c < n)
+        for (int64_t g = g0; g < groups; g += 32) v += part[g * n + c];
+    s[g0][cl] = v;
+    __syncthreads();
+    if (threadIdx.x < 32 && c < n) {
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v += s[i][cl];
+        out.put(c, v);
     }
 }
 
 }  // namespace
 
 int64_t col_sum_groups(int64_t rows, int64_t n) {
-    const int64_t blocks = (n + 511) / 512, most = (rows + 15) / 16;
+    const int64_t blocks = (n + 511) / 512, most = (rows + 31) / 32;  // a wave takes eight rows or more
     int64_t g = 512 / blocks;
     g = g < 1 ? 1 : g > 64 ? 64 : g;
     return g < most ? g : most < 1 ? 1 : most;
@@ -857,13 +880,13 @@ int64_t col_sum_groups(int64_t rows, int64_t n) {
 hipError_t launch_col_sum(const uint16_t* x, int64_t rows, int64_t n, float* part, void* out, bool f32, bool accumulate,
                           hipStream_t stream) {
     int64_t groups = col_sum_groups(rows, n);
-    void* args[] = {(void*)&x, (void*)&rows, (void*)&n, (void*)&part};
+    ColOut to = {out, f32, accumulate};
+    void* args[] = {(void*)&x, (void*)&rows, (void*)&n, (void*)&part, (void*)&to};
     hipError_t err = hipLaunchKernel((const void*)&col_sum_kernel, dim3((unsigned)((n + 511) / 512), (unsigned)groups),
                                      dim3(256), args, 0, stream);
-    if (err != hipSuccess) return err;
-    int f = f32, acc = accumulate;
-    void* jargs[] = {(void*)&part, (void*)&groups, (void*)&n, (void*)&out, (void*)&f, (void*)&acc};
-    return hipLaunchKernel((const void*)&col_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), jargs, 0, stream);
+    if (err != hipSuccess || groups == 1) return err;
+    void* jargs[] = {(void*)&part, (void*)&groups, (void*)&n, (void*)&to};
+    return hipLaunchKernel((const void*)&col_join_kernel, dim3((unsigned)((n + 31) / 32)), dim3(1024), jargs, 0, stream);
 }
 
 }  // namespace loco
