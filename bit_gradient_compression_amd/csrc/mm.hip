@@ -821,31 +821,34 @@ struct ColOut {
     }
 };
 
-// Sums of 512 columns per workgroup over every gridDim.y-th group of four rows, one row per
-// wave: partial sums, or with one group the result.
-__global__ __launch_bounds__(256) void col_sum_kernel(const uint16_t* x, int64_t rows, int64_t n, float* part, ColOut out) {
-    __shared__ float join[4][512];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 512 + lane * 8, left = n - col;
+// Sums of 8 << lanes_log2 columns per workgroup over every gridDim.y-th group of rows, a row to
+// 1 << lanes_log2 lanes (all 64 of a wave from 512 columns on): partial sums, or with one group
+// the result.
+__global__ __launch_bounds__(256) void col_sum_kernel(const uint16_t* x, int64_t rows, int64_t n, int lanes_log2,
+                                                      float* part, ColOut out) {
+    __shared__ float join[256 * 8];
+    const int lane = threadIdx.x & ((1 << lanes_log2) - 1), team = threadIdx.x >> lanes_log2, teams = 256 >> lanes_log2;
+    const int cols = 8 << lanes_log2;
+    const int64_t col0 = (int64_t)blockIdx.x * cols, left = n - col0 - lane * 8;
     const int valid = left <= 0 ? 0 : left < 8 ? (int)left : 8;
     float s[8], v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = 0.0f;
 #pragma unroll 4
-    for (int64_t r = (int64_t)blockIdx.y * 4 + wave; r < rows; r += (int64_t)gridDim.y * 4) {
-        load_chunk(x + r * n + col, valid, v);
+    for (int64_t r = (int64_t)blockIdx.y * teams + team; r < rows; r += (int64_t)gridDim.y * teams) {
+        load_chunk(x + r * n + col0 + lane * 8, valid, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] += v[i];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) join[wave][lane * 8 + i] = s[i];
+    for (int i = 0; i < 8; ++i) join[team * cols + lane * 8 + i] = s[i];
     __syncthreads();
-    for (int c = threadIdx.x; c < 512; c += 256) {
-        const int64_t at = (int64_t)blockIdx.x * 512 + c;
-        const float v = (join[0][c] + join[1][c]) + (join[2][c] + join[3][c]);
-        if (at < n) {
-            if (gridDim.y == 1) out.put(at, v);
-            else part[blockIdx.y * n + at] = v;
+    for (int c = threadIdx.x; c < cols; c += 256) {
+        float v = 0.0f;
+        for (int t = 0; t < teams; ++t) v += join[t * cols + c];
+        if (col0 + c < n) {
+            if (gridDim.y == 1) out.put(col0 + c, v);
+            else part[blockIdx.y * n + col0 + c] = v;
         }
     }
 }
@@ -870,20 +873,31 @@ __global__ __launch_bounds__(1024) void col_join_kernel(const float* part, int64
 
 }  // namespace
 
+namespace {
+int col_lanes_log2(int64_t n) {
+    int l = 0;
+    while (l < 6 && (8 << l) < n) ++l;
+    return l;
+}
+}  // namespace
+
 int64_t col_sum_groups(int64_t rows, int64_t n) {
-    const int64_t blocks = (n + 511) / 512, most = (rows + 31) / 32;  // a wave takes eight rows or more
-    int64_t g = 512 / blocks;
-    g = g < 1 ? 1 : g > 64 ? 64 : g;
+    const int l = col_lanes_log2(n);
+    const int64_t blocks = tiles_of(n, 8 << l), teams = 256 >> l;
+    const int64_t most = tiles_of(rows, teams * 8);  // a team takes eight rows or more
+    const int64_t wanted = 2048 / blocks;  // eight workgroups on a compute unit
+    const int64_t g = wanted < 1 ? 1 : wanted > 256 ? 256 : wanted;
     return g < most ? g : most < 1 ? 1 : most;
 }
 
 hipError_t launch_col_sum(const uint16_t* x, int64_t rows, int64_t n, float* part, void* out, bool f32, bool accumulate,
                           hipStream_t stream) {
     int64_t groups = col_sum_groups(rows, n);
+    int lanes = col_lanes_log2(n);
     ColOut to = {out, f32, accumulate};
-    void* args[] = {(void*)&x, (void*)&rows, (void*)&n, (void*)&part, (void*)&to};
-    hipError_t err = hipLaunchKernel((const void*)&col_sum_kernel, dim3((unsigned)((n + 511) / 512), (unsigned)groups),
-                                     dim3(256), args, 0, stream);
+    void* args[] = {(void*)&x, (void*)&rows, (void*)&n, (void*)&lanes, (void*)&part, (void*)&to};
+    hipError_t err = hipLaunchKernel((const void*)&col_sum_kernel,
+                                     dim3((unsigned)tiles_of(n, 8 << lanes), (unsigned)groups), dim3(256), args, 0, stream);
     if (err != hipSuccess || groups == 1) return err;
     void* jargs[] = {(void*)&part, (void*)&groups, (void*)&n, (void*)&to};
     return hipLaunchKernel((const void*)&col_join_kernel, dim3((unsigned)((n + 31) / 32)), dim3(1024), jargs, 0, stream);
