@@ -1,4 +1,5 @@
-"""MI355X (gfx950) implementation of LoCo's per-GPU gradient path.
+"""MI355X (gfx950) implementation of LoCo's per-GPU gradient path and of the layer operators
+(layer norm, linear products, 8-bit activation checkpoints) whose backward pass feeds it.
 
 The work happens in hand-written HIP kernels behind the C ABI declared in
 include/loco.h (libloco.so); `loco` is its thin Python binding.
