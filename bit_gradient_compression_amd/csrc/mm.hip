@@ -435,7 +435,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
 
 struct DmaSrc {
     const char* base;
-    int64_t left;  // bytes from base to the operand's end
+    int64_t left;  // bytes from base to the operand's end (free-major: to the split's)
     int64_t step;  // bytes from one step to the next
 };
 
@@ -448,12 +448,12 @@ struct Dma {
     uint32_t off[kPer];
     int k_chunk;  // k-major: this thread's chunk within a row, the same for each of its loads
 
-    __device__ __forceinline__ void init(const Operand& o, int64_t free0, int64_t k0) {
+    __device__ __forceinline__ void init(const Operand& o, int64_t free0, int64_t k0, int64_t k_hi) {
         static_assert(THREADS % T::kPerRow == 0 && (THREADS / T::kPerRow) % 16 == 0 || !KMAJOR,
                       "a thread's loads share their chunk's place in the row");
         const int t = threadIdx.x;
         s.base = (const char*)(o.p + (KMAJOR ? free0 * o.ld + k0 : k0 * o.ld + free0));
-        s.left = ((KMAJOR ? o.free : o.k) * o.ld) * 2 - (s.base - (const char*)o.p);
+        s.left = ((KMAJOR ? o.free : min(o.k, k_hi)) * o.ld) * 2 - (s.base - (const char*)o.p);
         s.step = (KMAJOR ? STEP : STEP * o.ld) * 2;
         k_chunk = T::chunk_of(t);
 #pragma unroll
@@ -501,8 +501,8 @@ __device__ __forceinline__ void step_barrier() {
 // whose fragments are in registers by then: behind it the next step's first fragments are
 // read, the loads into the step just read out start, and the matrix cores are busy meanwhile
 // (the barrier sits where a quarter of those products is left).
-// Loads past the last step are started all the same (and write zeros, or k that are not
-// multiplied), so that the count of pending loads is the same in every step.
+// Loads past the last step are started all the same, so that the count of pending loads is the
+// same in every step.  They write zeros.
 template <int BM, int BN, int WM, int WN, int STEP, int STAGES, int MS, bool AK, bool BK>
 __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) void mm_dma_kernel(const MmArgs g) {
     constexpr int THREADS = WM * WN * 64;
@@ -531,8 +531,8 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
     DA da;
     DB db;
     bf16x8 fa[2][MI], fb[2][NI];
-    da.init(g.a, m0, k_lo);
-    db.init(g.b, n0, k_lo);
+    da.init(g.a, m0, k_lo, k_lo + g.k_split);
+    db.init(g.b, n0, k_lo, k_lo + g.k_split);
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
     int k_left = k_all;
     constexpr int LOADS = DA::kPer + DB::kPer, EARLY = LOADS / 2;
@@ -560,6 +560,9 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
     };
     constexpr int PENDING = (STAGES - 2) * LOADS;
     constexpr int MF = MI * NI, BARX = MF * 3 / 4;
+    // An odd number of steps ends with one of zeros: without a way out between the stages the
+    // compiler finds registers that save 2 % (with both operands free-major it finds too few).
+    constexpr bool EVEN = BM == 256 && BN == 256 && AK;
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i)
 #pragma unroll
@@ -572,7 +575,7 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
     for (int it = 0; it < steps; it += STAGES) {
 #pragma unroll
         for (int stage = 0; stage < STAGES; ++stage) {
-            if (it + stage >= steps) break;
+            if (!EVEN && it + stage >= steps) break;
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
                 const bool last = s + 1 == SUB;
