@@ -26,6 +26,12 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
 }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
 
+// Streaming stores, for what is not read again soon: they leave the caches to what is.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+__device__ __forceinline__ void stream16(void* p, u32x4 v) { __builtin_nontemporal_store(v, (u32x4_any*)p); }
+__device__ __forceinline__ void stream8(void* p, u32x2 v) { __builtin_nontemporal_store(v, (u32x2_any*)p); }
+
 __device__ __forceinline__ void unpack_bf16x8(u32x4 w, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -239,9 +245,10 @@ __device__ __forceinline__ u32x2 ckpt_codes(const float (&v)[8], uint32_t e) {
     return u32x2{lo, hi};
 }
 
+// Codes are read in the backward pass, long after they are written: their stores stream.
 __device__ __forceinline__ void store_codes(int8_t* p, int valid, u32x2 w) {
     if (valid >= 8) {
-        __builtin_memcpy(p, &w, 8);
+        stream8(p, w);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
