@@ -196,6 +196,7 @@ struct MmArgs {
     Operand a, b;
     int64_t m, n, k;
     int tiles_m, tiles_n;
+    int64_t m_first, n_first;  // the first tile's row and column
     int64_t k_split;  // k per split, a multiple of kStep
     float* part;      // null: epilogue
     MmEpilogue ep;
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mm_kernel(const MmArgs g) {
     const int wm = wave / WN, wn = wave % WN;
     int tm, tn;
     tile_of(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int64_t m0 = g.m_first + (int64_t)tm * BM, n0 = g.n_first + (int64_t)tn * BN;
     const int64_t k_lo = (int64_t)blockIdx.y * g.k_split;
     const int64_t k_hi = min(g.k, k_lo + g.k_split);
     const int steps = (int)((k_hi - k_lo + kStep - 1) / kStep);
@@ -517,7 +518,7 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN == 4 && BM == 256 ? 1 : 2) vo
     const int wm = wave / WN, wn = wave % WN;
     int tm, tn;
     tile_of(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+    const int64_t m0 = g.m_first + (int64_t)tm * BM, n0 = g.n_first + (int64_t)tn * BN;
     const int64_t k_lo = (int64_t)blockIdx.y * g.k_split;
     const int k_all = (int)(min(g.k, k_lo + g.k_split) - k_lo);
     const int steps = (k_all + STEP - 1) / STEP;
@@ -671,9 +672,17 @@ bool chunked(const Operand& o) { return o.ld % 8 == 0; }
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
 double copy_us(const Operand& o) { return 3.0 + (double)(o.free * o.k) * 4.0 / 4.5e6; }
 
+// Rounds of `tiles` workgroups of `steps` each.
+double round_us(const Shape& s, int64_t tiles, int64_t steps) {
+    return tiles_of(tiles, s.slots) * (steps * s.step_us[tiles > 256] + s.tile_us);
+}
+constexpr double kTailUs = 8.0;  // a second launch, and the first one's last tiles end alone
+
 struct Plan {
     int shape;  // -1: the tile staged through registers
     int splits;
+    int tail_shape;
+    int64_t tail_m, tail_n;  // rows or columns from here on go in a second launch (m and n: none)
 };
 
 // The shape and the splits of the contraction that finish first: rounds of workgroups, each the
@@ -683,7 +692,7 @@ Plan plan(const Operand& a, const Operand& b) {
     const int64_t m = a.free, n = b.free, steps = tiles_of(a.k, kStep);
     const bool fast = chunked(a) && chunked(b);
     const double copies = (chunked(a) ? 0.0 : copy_us(a)) + (chunked(b) ? 0.0 : copy_us(b));
-    Plan best = {0, 1};
+    Plan best = {0, 1, 0, m, n};
     double best_us = 0.0;
     for (int i = fast ? 0 : -1; i < kShapes; ++i) {
         // 300 TFLOP/s through the registers
@@ -692,12 +701,33 @@ Plan plan(const Operand& a, const Operand& b) {
         for (int64_t splits = 1; splits <= 64; splits = splits < 8 ? splits + 1 : splits * 5 / 4) {
             const int64_t per = tiles_of(steps, splits);
             if (splits > 1 && (per < 4 || tiles_of(steps, per) < splits)) continue;
-            const int64_t rounds = tiles_of(tiles * splits, s.slots);
-            double us = rounds * (per * s.step_us[tiles * splits > 256] + s.tile_us) + (i >= 0 ? copies : 0.0);
+            double us = round_us(s, tiles * splits, per) + (i >= 0 ? copies : 0.0);
             if (splits > 1) us += 4.0 + splits * (double)(m * n) * 8.0 / 6e6;
             if (best_us == 0.0 || us < best_us) {
-                best = {i, (int)splits};
+                best = {i, (int)splits, 0, m, n};
                 best_us = us;
+            }
+        }
+    }
+    // Where the last round would leave most of the chip idle, the columns or rows that fill whole
+    // rounds go first and a second launch takes the rest in the tiles that suit them (8192 x 4096
+    // -> 11008, 5.4 rounds of the large tile: 620 us in one launch, 608 in two; 3136 x 5347 over
+    // 3636, 1.1 rounds: 179 and 136).
+    for (int i = 0; i < kShapes; ++i) {
+        const Shape& s = shape_at(i);
+        const int64_t tm = tiles_of(m, s.bm), tn = tiles_of(n, s.bn), whole = tm * tn / s.slots * s.slots;
+        for (int rows = 0; rows < 2; ++rows) {
+            const int64_t across = rows ? tn : tm, first = whole / across, at = first * (rows ? s.bm : s.bn);
+            if (first < 1 || at >= (rows ? m : n)) continue;
+            const int64_t tail_rows = rows ? m - at : m, tail_cols = rows ? n : n - at;
+            const double us = copies + kTailUs + round_us(s, first * across, steps);
+            for (int j = 0; j < kShapes; ++j) {
+                const Shape& t = shape_at(j);
+                const double all = us + round_us(t, tiles_of(tail_rows, t.bm) * tiles_of(tail_cols, t.bn), steps);
+                if (all < best_us) {
+                    best = {i, 1, j, rows ? at : m, rows ? n : at};
+                    best_us = all;
+                }
             }
         }
     }
@@ -781,16 +811,23 @@ hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
     g.n = p.n;
     g.k = g.a.k;  // with the zeros of a copy
     const int layout = layout_of(p.a_kmajor, p.b_kmajor);
-    const Shape* s = pl.shape >= 0 ? &shape_at(pl.shape) : nullptr;
-    g.tiles_m = (int)tiles_of(p.m, s ? s->bm : 128);
-    g.tiles_n = (int)tiles_of(p.n, s ? s->bn : 128);
     g.k_split = tiles_of(tiles_of(p.k, kStep), pl.splits) * kStep;
     g.part = pl.splits > 1 ? (float*)at : nullptr;
     g.ep = p.ep;
     void* args[] = {(void*)&g};
-    err = hipLaunchKernel(s ? s->kernel[layout] : pick_mm(layout),
-                          dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)pl.splits),
-                          dim3(s ? s->threads : 256), args, 0, stream);
+    auto tiles = [&](int shape, int64_t m0, int64_t m1, int64_t n0, int64_t n1) {
+        const Shape* s = shape >= 0 ? &shape_at(shape) : nullptr;
+        g.tiles_m = (int)tiles_of(m1 - m0, s ? s->bm : 128);
+        g.tiles_n = (int)tiles_of(n1 - n0, s ? s->bn : 128);
+        g.m_first = m0;
+        g.n_first = n0;
+        return hipLaunchKernel(s ? s->kernel[layout] : pick_mm(layout),
+                               dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n), (unsigned)pl.splits),
+                               dim3(s ? s->threads : 256), args, 0, stream);
+    };
+    err = tiles(pl.shape, 0, pl.tail_m, 0, pl.tail_n);
+    if (err == hipSuccess && pl.tail_n < p.n) err = tiles(pl.tail_shape, 0, p.m, pl.tail_n, p.n);
+    if (err == hipSuccess && pl.tail_m < p.m) err = tiles(pl.tail_shape, pl.tail_m, p.m, 0, p.n);
     if (err != hipSuccess || pl.splits == 1) return err;
     int64_t per_row = tiles_of(p.n, 64) * 8, t0 = 0;
     int splits = pl.splits;

@@ -257,6 +257,25 @@ def test_weight_grad_tiles(gpu_lib, m, n, k):
     check_weight_grad(gpu_lib, k, m, n, "none", F32, accumulate=True)
 
 
+# just past whole rounds of the large tile: the last rows, or the last columns, in a second launch
+TAILS = [(4100, 4104, 520), (2056, 8200, 520), (4400, 4097, 520)]
+
+
+@pytest.mark.parametrize("m,n,k", TAILS)
+def test_linear_tails(gpu_lib, m, n, k):
+    check_linear(gpu_lib, m, n, k, "gelu", block=64)
+
+
+@pytest.mark.parametrize("m,n,k", TAILS)
+def test_input_grad_tails(gpu_lib, m, n, k):
+    check_input_grad(gpu_lib, m, k, n, "silu", True)
+
+
+@pytest.mark.parametrize("m,n,k", TAILS)
+def test_weight_grad_tails(gpu_lib, m, n, k):
+    check_weight_grad(gpu_lib, k, m, n, "relu", BF, accumulate=True)
+
+
 # -- the calls together -------------------------------------------------------------------------------------------------------------------------------
 
 def test_same_call_same_bits(gpu_lib):
