@@ -5,9 +5,12 @@
 // dw = sum over rows of dy xh, db = sum over rows of dy.
 //
 // Both are bound by HBM: each element is read once and written once.  A row stays in
-// registers between the statistics and the output: one wave holds up to 4096 columns in
-// the forward pass, a workgroup of four or eight waves wider rows.  All sums are fp32; the
+// registers between the statistics and the output: forward one wave holds up to 1024 columns,
+// four or eight waves together a wider row.  All sums are fp32; the
 // variance is the mean of squared differences from the mean, not a difference of squares.
+// Measured at 16384 x 4096 in bf16: forward 51 us (5.2 TB/s, as torch's copy of the same
+// bytes), 67 with a checkpoint of y; backward with a residual 110 (5.0 TB/s).  The smallest
+// calls take one launch's 4 us.
 
 #include "loco_layer.hpp"
 #include "loco_layer_internal.hpp"
