@@ -640,6 +640,96 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const MmArgs g, int splits
     epilogue(g.ep, row, g.n, col, valid, v);
 }
 
+// ---- few rows ---------------------------------------------------------------------------
+//
+// Up to 16 rows of k-major operands, the single tokens of serving: latencies and launches bind.
+// A workgroup takes 16 columns and all of k, so that nothing is joined in a second launch: its
+// waves take blocks of 64 k in turn, each row of a block one line of 128 bytes, straight into
+// registers, kFewAhead blocks ahead of the products, and their sums meet in LDS in a fixed
+// order.  Rows past the operands' ends read the last row, and what comes of them is not stored.
+// Rows of any alignment are read as they are.  Eight and sixteen waves were slower (16 x 4096 ->
+// 4096: 13.3 and 16.7 us against 12.0), and so were 32 and 64 columns (17 and 27).
+constexpr int kFewAhead = 4, kFewWaves = 4;
+
+// Eight elements from col on of a row of k, zeros past its end; none of the loads waits for
+// another.
+__device__ __forceinline__ u32x4 row_end(const uint16_t* row, int64_t col, int64_t k) {
+    u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t e = row[min(col + i, k - 1)];
+        w[i >> 1] |= (col + i < k ? e : 0u) << (16 * (i & 1));
+    }
+    return w;
+}
+
+__global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(const MmArgs g) {
+    using M = Mfma<16>;
+    constexpr int SUB = kStep / M::KS;
+    __shared__ float sums[kFewWaves][16][17];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int r = lane & 15, c = (lane >> 4) * 8;
+    const uint16_t* pa = g.a.p + min((int64_t)r, g.m - 1) * g.a.ld;
+    const uint16_t* pb = g.b.p + min(n0 + r, g.n - 1) * g.b.ld;
+
+    M::acc_t acc = {};
+    u32x4 fa[kFewAhead][SUB], fb[kFewAhead][SUB];
+    const int blocks = (int)(g.k / kStep), mine = blocks > wave ? (blocks - wave + kFewWaves - 1) / kFewWaves : 0;
+    auto load = [&](int slot, int x) __attribute__((always_inline)) {
+        const int64_t k0 = ((int64_t)min(x, mine - 1) * kFewWaves + wave) * kStep + c;
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+            fa[slot][s] = load16(pa + k0 + s * M::KS);
+            fb[slot][s] = load16(pb + k0 + s * M::KS);
+        }
+    };
+    auto mul = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+            acc = M::mul(__builtin_bit_cast(bf16x8, fa[slot][s]), __builtin_bit_cast(bf16x8, fb[slot][s]), acc);
+    };
+    if (mine > 0) {
+#pragma unroll
+        for (int d = 0; d < kFewAhead; ++d) load(d, d);
+        int x = 0;
+        for (; x + kFewAhead <= mine; x += kFewAhead) {
+#pragma unroll
+            for (int d = 0; d < kFewAhead; ++d) {
+                mul(d);
+                load(d, x + d + kFewAhead);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kFewAhead; ++d)
+            if (x + d < mine) mul(d);
+    }
+    if (wave == blocks % kFewWaves && (int64_t)blocks * kStep < g.k) {  // the last, short block
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+            const int64_t k0 = (int64_t)blocks * kStep + s * M::KS + c;
+            fa[0][s] = row_end(pa, k0, g.k);
+            fb[0][s] = row_end(pb, k0, g.k);
+        }
+        mul(0);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) sums[wave][M::row(x, lane)][r] = acc[x];
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int row = threadIdx.x >> 1, at = (threadIdx.x & 1) * 8;
+        const int64_t left = g.n - n0 - at;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w) v[i] += sums[w][row][at + i];
+        }
+        epilogue(g.ep, row, g.n, n0 + at, row >= g.m || left <= 0 ? 0 : left < 8 ? (int)left : 8, v);
+    }
+}
+
 constexpr int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
 // The layouts that occur: both operands k-major, the second free-major, both free-major.
@@ -780,6 +870,29 @@ hipError_t pad(Operand& o, bool kmajor, uint16_t* to, hipStream_t stream) {
 Operand operand_a(const MmParams& p) { return {p.a, p.m, p.k, p.a_kmajor ? p.k : p.m}; }
 Operand operand_b(const MmParams& p) { return {p.b, p.n, p.k, p.b_ld ? p.b_ld : p.b_kmajor ? p.k : p.n}; }
 
+// Where a few rows' products take fewer microseconds in one launch of 16 columns a workgroup than
+// in tiles with k split: 4 x 1000 -> 4000 6.4 against 11.0, 16 x 4096 -> 4096 12.0 against 14.8,
+// 16 x 1003 -> 1001, whose rows would be copied, 9.7 against 16.3.  Past 4096 columns, with more
+// than a workgroup on a compute unit, the rows of A are read too often (16 x 4096 -> 11008 29.9
+// against 23.0); past 4096 k a workgroup's waves take too long (16 x 14336 -> 1000 29.0 against
+// 21.6).  A checkpoint's blocks would span workgroups.
+bool few_rows(const MmParams& p) {
+    return p.a_kmajor && p.b_kmajor && p.m <= 16 && p.n <= 4096 && p.k <= 4096 && !p.ep.ckpt.codes;
+}
+
+hipError_t launch_few(const MmParams& p, hipStream_t stream) {
+    MmArgs g = {};
+    g.a = operand_a(p);
+    g.b = operand_b(p);
+    g.m = p.m;
+    g.n = p.n;
+    g.k = p.k;
+    g.ep = p.ep;
+    void* args[] = {(void*)&g};
+    return hipLaunchKernel((const void*)&mm_few_kernel, dim3((unsigned)tiles_of(p.n, 16)), dim3(kFewWaves * 64), args, 0,
+                           stream);
+}
+
 // The workspace of a product: partial sums, then the operands' copies.
 struct Spaces {
     int64_t part, a, b;
@@ -804,6 +917,7 @@ int64_t mm_workspace(const MmParams& p) {
 }
 
 hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
+    if (few_rows(p)) return launch_few(p, stream);
     MmArgs g;
     g.a = operand_a(p);
     g.b = operand_b(p);

@@ -257,6 +257,14 @@ def test_weight_grad_tiles(gpu_lib, m, n, k):
     check_weight_grad(gpu_lib, k, m, n, "none", F32, accumulate=True)
 
 
+# a few rows without a checkpoint: one launch, columns and k that end inside a block
+@pytest.mark.parametrize("act", sorted(ACT))
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 16, 64), (3, 17, 63), (5, 100, 65), (16, 1001, 1003), (2, 33, 4095),
+                                   (9, 250, 577), (16, 4096, 4096), (15, 4096, 200), (16, 4097, 256), (17, 64, 256)])
+def test_linear_single_tokens(gpu_lib, m, n, k, act):
+    check_linear(gpu_lib, m, n, k, act, block=0)
+
+
 # just past whole rounds of the large tile: the last rows, or the last columns, in a second launch
 TAILS = [(4100, 4104, 520), (2056, 8200, 520), (4400, 4097, 520)]
 
