@@ -524,8 +524,8 @@ LOCO_API int loco_checkpoint_read(const loco_checkpoint_t* ckpt, int64_t rows, i
                      exps_buf(ckpt, rows, cols, false)});
     if (st != LOCO_OK) return st;
     return hip_status(
-        launch_ckpt_read(ckpt_dev(ckpt, cols), rows, cols, act, out, cols,
-                                       out_dtype == LOCO_F32, (hipStream_t)stream));
+        launch_ckpt_read(ckpt_dev(ckpt, cols), rows, cols, act, out, cols, out_dtype == LOCO_F32, false,
+                         (hipStream_t)stream));
 }
 
 namespace {
@@ -673,15 +673,23 @@ LOCO_API int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t
     char* at = (char*)workspace;
     if (k > 0) {
         uint16_t* a = (uint16_t*)(at + space.product + space.sums);
-        if (rows > 0 &&
-            launch_ckpt_read(ckpt_dev(ckpt, k), rows, k, act, a, mm_padded(k), false, hs) != hipSuccess)
-            return LOCO_ERR_HIP;
-        MmParams p = weight_grad_product(dy, a, rows, n, k);
-        p.ep.out = dweight;
-        p.ep.out_f32 = grad_dtype == LOCO_F32;
-        p.ep.accumulate = accumulate != 0;
-        p.workspace = at;
-        if (launch_mm(p, hs) != hipSuccess) return LOCO_ERR_HIP;
+        // The matrix cores take bf16.  A checkpoint's values and their ReLU are bf16 numbers; GELU and
+        // SiLU are not.  For bf16 gradients they are rounded to it, as the forward product's operand
+        // was: an error of 0.0017 beside the gradient's own rounding of 0.0017.  For fp32 gradients
+        // that would be all of the error, so what the rounding leaves (at most 2^-8 of the value,
+        // itself rounded by 2^-8 of that) is a second operand, whose product is added to the first's.
+        const int parts = grad_dtype == LOCO_F32 && (act == LOCO_ACT_GELU || act == LOCO_ACT_SILU) && rows > 0 ? 2 : 1;
+        for (int part = 0; part < parts; ++part) {
+            if (rows > 0 &&
+                launch_ckpt_read(ckpt_dev(ckpt, k), rows, k, act, a, mm_padded(k), false, part == 1, hs) != hipSuccess)
+                return LOCO_ERR_HIP;
+            MmParams p = weight_grad_product(dy, a, rows, n, k);
+            p.ep.out = dweight;
+            p.ep.out_f32 = grad_dtype == LOCO_F32;
+            p.ep.accumulate = accumulate != 0 || part == 1;
+            p.workspace = at;
+            if (launch_mm(p, hs) != hipSuccess) return LOCO_ERR_HIP;
+        }
     }
     if (dbias)
         return hip_status(launch_col_sum(dy, rows, n, (float*)(at + space.product), dbias, grad_dtype == LOCO_F32,

@@ -59,7 +59,15 @@ __global__ __launch_bounds__(kAcThreads) void ckpt_write_kernel(const T* x, Ckpt
     }
 }
 
-template <typename T, int ACT, bool FLAT>
+// What the rounding of v to bf16 leaves, 0 where that is an infinity; a NaN stays one.
+__device__ __forceinline__ void rest_chunk(float (&v)[8]) {
+    float h[8];
+    unpack_bf16x8(pack_bf16x8(v), h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_fabsf(h[i]) == __builtin_inff() ? 0.0f : v[i] - h[i];
+}
+
+template <typename T, int ACT, bool FLAT, bool REST = false>
 __global__ __launch_bounds__(kAcThreads) void ckpt_read_kernel(CkptDev ck, T* out, int64_t rows, int64_t cols,
                                                                int64_t per_row, int64_t t0, int64_t ld, int stream) {
     const int64_t t = t0 + (int64_t)blockIdx.x * kAcTile + threadIdx.x;
@@ -78,6 +86,7 @@ __global__ __launch_bounds__(kAcThreads) void ckpt_read_kernel(CkptDev ck, T* ou
         float v[8];
         decode_codes(codes[u], e[u], v);
         act_chunk<ACT>(v);
+        if constexpr (REST) rest_chunk(v);
         T* to = out + a[u].row * ld + a[u].col;
         if constexpr (sizeof(T) == 2) {
             if (stream && a[u].valid >= 8) {
@@ -101,6 +110,11 @@ const void* pick_act(int act) {
 template <typename T>
 const void* pick_read(int act, bool flat) {
     return flat ? pick_act<T, true>(act) : pick_act<T, false>(act);
+}
+template <bool FLAT>
+const void* pick_rest(int act) {
+    return act == 2 ? (const void*)&ckpt_read_kernel<uint16_t, 2, FLAT, true>
+                    : (const void*)&ckpt_read_kernel<uint16_t, 3, FLAT, true>;
 }
 template <typename T>
 const void* pick_write(bool flat) {
@@ -143,7 +157,7 @@ hipError_t launch_ckpt_write(const void* x, bool f32, int64_t rows, int64_t cols
 }
 
 hipError_t launch_ckpt_read(const CkptDev& ck, int64_t rows, int64_t cols, int act, void* out, int64_t ld, bool f32,
-                            hipStream_t hip_stream) {
+                            bool rest, hipStream_t hip_stream) {
     CkptDev c = ck;
     if (ld == cols) {
         flatten(rows, cols, c);
@@ -157,8 +171,11 @@ hipError_t launch_ckpt_read(const CkptDev& ck, int64_t rows, int64_t cols, int a
     int stream = !f32 && rows * ld * 2 >= (int64_t)128 << 20;
     void* args[] = {(void*)&c, (void*)&out, (void*)&rows, (void*)&cols, (void*)&per_row, (void*)&t0, (void*)&ld,
                     (void*)&stream};
-    return launch_chunks(f32 ? pick_read<float>(act, rows == 1) : pick_read<uint16_t>(act, rows == 1), args, &t0,
-                         rows * per_row, hip_stream);
+    const bool flat = rows == 1;
+    const void* k = rest  ? (flat ? pick_rest<true>(act) : pick_rest<false>(act))
+                    : f32 ? pick_read<float>(act, flat)
+                          : pick_read<uint16_t>(act, flat);
+    return launch_chunks(k, args, &t0, rows * per_row, hip_stream);
 }
 
 }  // namespace loco

@@ -55,9 +55,10 @@ hipError_t launch_ln_bwd(const LnBwdParams& p, hipStream_t stream);
 // ---- activation checkpoints ----------------------------------------------------------
 
 hipError_t launch_ckpt_write(const void* x, bool f32, int64_t rows, int64_t cols, const CkptDev& c, hipStream_t stream);
-// out: rows of `ld` elements, of which cols are written.
+// out: rows of `ld` elements, of which cols are written.  rest (GELU or SiLU, bf16): not the
+// activation, but what its rounding to bf16 leaves.
 hipError_t launch_ckpt_read(const CkptDev& c, int64_t rows, int64_t cols, int act, void* out, int64_t ld, bool f32,
-                            hipStream_t stream);
+                            bool rest, hipStream_t stream);
 
 // ---- matrix products -----------------------------------------------------------------
 

@@ -391,8 +391,10 @@ int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int
 
 /*
  * loco_linear_weight_grad - dweight = dy^T a, dbias = sum over the rows of dy, with
- * a = act(value of the 8-bit checkpoint [rows, in]).  LOCO_ACT_NONE takes the checkpoint's
- * values as they are; an activation's value is rounded to bf16 for the product.
+ * a = act(value of the 8-bit checkpoint [rows, in]).  LOCO_ACT_NONE and LOCO_ACT_RELU take the
+ * checkpoint's values as they are, which are bf16 numbers.  A value of LOCO_ACT_GELU or
+ * LOCO_ACT_SILU is rounded to bf16 for the product if grad_dtype is LOCO_BF16; for LOCO_F32 it
+ * enters as the sum of two bf16 numbers, in two products, which take twice the time.
  *   dy          device bf16[rows, out_features]
  *   dweight     device [out_features, in] of `grad_dtype`
  *   dbias       device [out_features] of `grad_dtype`, or NULL
