@@ -155,17 +155,20 @@ __device__ __forceinline__ float act_value(float z) {
     else return z;
 }
 
-// s = sigmoid(x) and q = 1 - s = exp(-x) s, each with its own relative accuracy (1 - s formed by
-// subtraction loses it where s is near 1).  The exponent is held below 2^126 so that q = 1 and
-// not inf * 0 for x below -87.
+// s = sigmoid(x) and q = 1 - s, each with its own relative accuracy (1 - s formed by subtraction
+// loses it where s is near 1): with u = exp(-|x|) the larger of them is 1 / (1 + u) and the smaller
+// u times that.  Nothing overflows, past |x| = 87 the smaller is 0, however large a factor z it
+// meets, and a NaN is in both: no minimum or clamp, which would drop it, touches x.
 __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& q) {
-    const float t = __builtin_amdgcn_exp2f(__builtin_fminf(x * -1.4426950408889634f, 126.0f));
-    s = __builtin_amdgcn_rcpf(1.0f + t);
-    q = t * s;
+    const float u = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * -1.4426950408889634f);
+    const float large = __builtin_amdgcn_rcpf(1.0f + u), small = u * large;
+    s = x < 0.0f ? small : large;
+    q = x < 0.0f ? large : small;
 }
 
 // The derivative of act_value.  GELU's second term is 0 in fp32 past |z| = 16, where its factors
-// overflow, so it takes z held within that; a NaN reaches the result through s.
+// overflow, so it takes z held within that (the clamp turns a NaN into a number); a NaN reaches the
+// result through s.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if constexpr (ACT == 1) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
