@@ -194,13 +194,15 @@ __global__ __launch_bounds__(WAVES * 64, NP == 1 ? 6 : NP == 2 ? 4 : 2) void ln_
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = 1.0f;
             const int c = (i * LANES + lane) * 8;
-            if (weight) load_chunk_any(weight, p.param_f32, c, chunk_valid(cols, c), w);
+            const int valid = chunk_valid(cols, c);
+            if (weight) load_chunk_any(weight, p.param_f32, c, valid, w);
             x[i].get(v);
             dy[i].get(g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                // past the row's end dy is 0, so whatever xh is there counts for nothing
-                const float xh = (v[j] - mean) * rstd;
+                // Past the row's end dy is 0, and xh has to be finite for its products with it to count
+                // for nothing: -mean * rstd may overflow.
+                const float xh = j < valid ? (v[j] - mean) * rstd : 0.0f;
                 dw[i][j] = __builtin_fmaf(g[j], xh, dw[i][j]);
                 db[i][j] += g[j];
                 const float gw = g[j] * w[j];
@@ -238,7 +240,11 @@ __global__ __launch_bounds__(WAVES * 64, NP == 1 ? 6 : NP == 2 ? 4 : 2) void ln_
             x[i].get(v);
             dy[i].get(g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = (g[j] * w[j] - s1 - (v[j] - mean) * rstd * s2) * rstd;
+            for (int j = 0; j < 8; ++j) {
+                // the sums' expression, so that its value is kept: another one takes 14 registers more
+                const float xh = j < valid ? (v[j] - mean) * rstd : 0.0f;
+                g[j] = (g[j] * w[j] - s1 - xh * s2) * rstd;
+            }
             if (p.residual) {
                 if (!EARLY) res[i].load((const T*)p.residual + row * cols + c, valid);
                 res[i].get(v);
