@@ -564,7 +564,7 @@ struct WeightGradSpace {
 };
 WeightGradSpace weight_grad_space(int64_t rows, int64_t n, int64_t k) {
     if (n == 0) return {0, 0, 0};
-    return {round16(mm_workspace(weight_grad_product(nullptr, nullptr, rows, n, k))),
+    return {round16(mm_workspace(weight_grad_product(nullptr, nullptr, rows, n, k), false)),
             round16(col_sum_groups(rows, n) * n * 4), round16(rows * mm_padded(k) * 2)};
 }
 
@@ -572,7 +572,7 @@ WeightGradSpace weight_grad_space(int64_t rows, int64_t n, int64_t k) {
 
 LOCO_API int64_t loco_linear_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
     if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
-    return mm_workspace(forward_product(nullptr, nullptr, rows, out_features, in_features));
+    return mm_workspace(forward_product(nullptr, nullptr, rows, out_features, in_features), true);
 }
 
 LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16_t* bias, const uint16_t* residual,
@@ -585,7 +585,8 @@ LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16
     st = check_product(rows, out_features, in_features);
     if (st != LOCO_OK) return st;
     if (rows == 0 || out_features == 0) return LOCO_OK;
-    const int64_t n = out_features, k = in_features, need = loco_linear_workspace(rows, n, k);
+    const int64_t n = out_features, k = in_features;
+    const int64_t need = mm_workspace(forward_product(x, weight, rows, n, k), ckpt != nullptr);
     if (workspace_bytes < need) return LOCO_ERR_INVALID;
     st = check_bufs({{x, rows * k * 2, false, true},
                      {weight, n * k * 2, false, true},
@@ -609,7 +610,7 @@ LOCO_API int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16
 
 LOCO_API int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features) {
     if (check_product(rows, out_features, in_features) != LOCO_OK) return 0;
-    return mm_workspace(input_grad_product(nullptr, nullptr, rows, out_features, in_features));
+    return mm_workspace(input_grad_product(nullptr, nullptr, rows, out_features, in_features), false);
 }
 
 LOCO_API int loco_linear_input_grad(const uint16_t* dy, const uint16_t* weight, const uint16_t* residual, int64_t rows,

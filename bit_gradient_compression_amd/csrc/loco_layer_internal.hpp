@@ -88,7 +88,8 @@ struct MmParams {
     MmEpilogue ep;
     void* workspace;  // mm_workspace bytes
 };
-int64_t mm_workspace(const MmParams& p);
+// with_ckpt: whether the call writes a checkpoint, which few rows' kernel does not.
+int64_t mm_workspace(const MmParams& p, bool with_ckpt);
 hipError_t launch_mm(const MmParams& p, hipStream_t stream);
 // The row length at which an operand need not be copied.
 int64_t mm_padded(int64_t n);

@@ -876,8 +876,8 @@ Operand operand_b(const MmParams& p) { return {p.b, p.n, p.k, p.b_ld ? p.b_ld : 
 // than a workgroup on a compute unit, the rows of A are read too often (16 x 4096 -> 11008 29.9
 // against 23.0); past 4096 k a workgroup's waves take too long (16 x 14336 -> 1000 29.0 against
 // 21.6).  A checkpoint's blocks would span workgroups.
-bool few_rows(const MmParams& p) {
-    return p.a_kmajor && p.b_kmajor && p.m <= 16 && p.n <= 4096 && p.k <= 4096 && !p.ep.ckpt.codes;
+bool few_rows(const MmParams& p, bool with_ckpt) {
+    return p.a_kmajor && p.b_kmajor && p.m <= 16 && p.n <= 4096 && p.k <= 4096 && !with_ckpt;
 }
 
 hipError_t launch_few(const MmParams& p, hipStream_t stream) {
@@ -910,14 +910,14 @@ Spaces spaces(const MmParams& p, const Plan& pl) {
 
 int64_t mm_padded(int64_t n) { return padded(n); }
 
-int64_t mm_workspace(const MmParams& p) {
-    if (p.m <= 0 || p.n <= 0) return 0;
+int64_t mm_workspace(const MmParams& p, bool with_ckpt) {
+    if (p.m <= 0 || p.n <= 0 || few_rows(p, with_ckpt)) return 0;
     const Spaces s = spaces(p, plan(operand_a(p), operand_b(p)));
     return s.part + s.a + s.b;
 }
 
 hipError_t launch_mm(const MmParams& p, hipStream_t stream) {
-    if (few_rows(p)) return launch_few(p, stream);
+    if (few_rows(p, p.ep.ckpt.codes)) return launch_few(p, stream);
     MmArgs g;
     g.a = operand_a(p);
     g.b = operand_b(p);

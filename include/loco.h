@@ -368,6 +368,9 @@ int loco_checkpoint_read(const loco_checkpoint_t* ckpt, int64_t rows, int64_t co
  *   ckpt      NULL, or the 8-bit checkpoint of z to write (of the fp32 z)
  *   out       device [rows, out_features] of `out_dtype`
  *   rows >= 0; in and out_features 0 .. 2^20 (LOCO_ERR_UNSUPPORTED beyond)
+ *   workspace loco_linear_workspace(rows, out_features, in) bytes, which is what a call that
+ *             writes a checkpoint needs; without one, up to 16 rows of at most 4096 in and
+ *             out_features need none, and others need the same
  */
 int loco_linear(const uint16_t* x, const uint16_t* weight, const uint16_t* bias, const uint16_t* residual,
                 int64_t rows, int64_t out_features, int64_t in_features, loco_act_t act, void* out,
