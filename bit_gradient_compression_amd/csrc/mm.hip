@@ -482,10 +482,13 @@ struct Dma {
         const uint32_t to = tile + (uint32_t)(j * THREADS + uniform(threadIdx.x & ~63)) * 16;
         const uint32_t o = KMAJOR && k_left < STEP && k_chunk * 8 >= k_left ? kOut : off[j];
         // the wait states cover scalar registers that a vector instruction has just written
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is reserved: what is declared is that it changes
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                      :
                      : "s"(to), "v"(o), "s"(r)
-                     : "memory");
+                     : "memory", "m0");
+#pragma clang diagnostic pop
     }
     __device__ __forceinline__ void advance() {
         s.base += s.step;
