@@ -357,7 +357,8 @@ def loco_sparse_aggregate(peers, n: int, *, chunk: int, k: int, out, out_scale: 
 #
 # A matrix is a contiguous tensor whose last dimension is its columns; the leading ones
 # together are its rows (tokens).  A checkpoint is a pair (codes int8, exps uint8), with
-# the block (32 or 64) given beside it.
+# the block (32 or 64) given beside it.  The call's first matrix sets the sizes; the others
+# have its leading dimensions, or one for all rows, or are flat (one dimension for the whole).
 
 # These calls are short beside a small kernel's launch, so the checks make few torch calls:
 # sizes and types first, then (_ptr) where each tensor lies.
@@ -390,14 +391,44 @@ def _sized(t, numel: int, what: str, dtypes) -> None:
         raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
 
 
-def _checkpoint(checkpoint, block, rows, cols, dev):
+def _matrix(t, like, rows, cols, what: str, dtypes) -> None:
+    """As _sized, for a matrix whose rows are those of the shape `like`: one with as many elements
+    but laid out otherwise would be filled as another matrix."""
+    if t is None:
+        return
+    shape = t.shape
+    if shape != (rows, cols):
+        _sized(t, rows * cols, what, dtypes)
+        lead, shape = tuple(like)[:-1], tuple(shape)
+        if len(shape) > 1 and not (shape[-1] == cols and _same_rows(shape[:-1], lead)):
+            raise ValueError(f"{what} has the shape {shape}; the call's is {(*lead, cols)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+
+
+def _per_row(t, like, rows, what: str) -> None:
+    """As _sized, for one float32 per row of the shape `like`."""
+    _sized(t, rows, what, _F32)
+    if t is not None and t.dim() > 1 and not _same_rows(tuple(t.shape), tuple(like)[:-1]):
+        raise ValueError(f"{what} has the shape {tuple(t.shape)}; the call's is {tuple(like)[:-1]}")
+
+
+def _same_rows(a, b) -> bool:
+    """Whether leading dimensions a and b, of as many rows, count them in the same order."""
+    if a == b or len(a) <= 1 or len(b) <= 1:
+        return True
+    a, b = [d for d in a if d != 1], [d for d in b if d != 1]
+    return a == b or len(a) <= 1 or len(b) <= 1
+
+
+def _checkpoint(checkpoint, block, like, rows, cols, dev):
     """The C struct of (codes, exps), or None."""
     if checkpoint is None:
         return None
     codes, exps = checkpoint
-    _sized(codes, rows * cols, "checkpoint codes", (torch.int8,))
+    _matrix(codes, like, rows, cols, "checkpoint codes", (torch.int8,))
     if block in (32, 64):
-        _sized(exps, rows * num_blocks(cols, block), "checkpoint exps", (torch.uint8,))
+        _matrix(exps, like, rows, num_blocks(cols, block), "checkpoint exps", (torch.uint8,))
     return ctypes.byref(Checkpoint(_ptr(codes, dev), _ptr(exps, dev), block))
 
 
@@ -412,13 +443,14 @@ def loco_layer_norm(x, weight, bias, *, out, mean, rstd, eps: float = 1e-5, chec
     with the 8-bit checkpoint of the output.  weight and bias may be None."""
     dev = _device()
     rows, cols = _rows_cols(x, "x", _FLOATS)
-    _sized(out, rows * cols, "out", (x.dtype,))
+    like = x.shape
+    _matrix(out, like, rows, cols, "out", (x.dtype,))
     param = weight if weight is not None else bias
     _sized(weight, cols, "weight", _FLOATS)
     _sized(bias, cols, "bias", _FLOATS if weight is None else (weight.dtype,))
-    _sized(mean, rows, "mean", _F32)
-    _sized(rstd, rows, "rstd", _F32)
-    ck = _checkpoint(checkpoint, block, rows, cols, dev)
+    _per_row(mean, like, rows, "mean")
+    _per_row(rstd, like, rows, "rstd")
+    ck = _checkpoint(checkpoint, block, like, rows, cols, dev)
     st = (_lib or load()).loco_layer_norm(
         _ptr(x, dev), _CODES[x.dtype], _ptr(weight, dev), _ptr(bias, dev),
         LOCO_F32 if param is None else _CODES[param.dtype], rows, cols, eps, _ptr(out, dev), _ptr(mean, dev),
@@ -433,11 +465,12 @@ def loco_layer_norm_backward(dy, x, weight, mean, rstd, *, dx, dweight=None, dbi
     bytes, not needed without dweight and dbias."""
     dev = _device()
     rows, cols = _rows_cols(x, "x", _FLOATS)
+    like = x.shape
     for t, what in ((dy, "dy"), (dx, "dx"), (residual, "residual")):
-        _sized(t, rows * cols, what, (x.dtype,))
+        _matrix(t, like, rows, cols, what, (x.dtype,))
     _sized(weight, cols, "weight", _FLOATS)
-    _sized(mean, rows, "mean", _F32)
-    _sized(rstd, rows, "rstd", _F32)
+    _per_row(mean, like, rows, "mean")
+    _per_row(rstd, like, rows, "rstd")
     grad = dweight if dweight is not None else dbias
     _sized(dweight, cols, "dweight", _FLOATS)
     _sized(dbias, cols, "dbias", _FLOATS if dweight is None else (dweight.dtype,))
@@ -458,7 +491,7 @@ def loco_checkpoint_write(x, *, codes, exps, block: int = 64, stream=None) -> No
     """The 8-bit checkpoint of x: codes int8 of x's shape, exps uint8, one per block of a row."""
     dev = _device()
     rows, cols = _rows_cols(x, "x", _FLOATS)
-    ck = _checkpoint((codes, exps), block, rows, cols, dev)
+    ck = _checkpoint((codes, exps), block, x.shape, rows, cols, dev)
     st = (_lib or load()).loco_checkpoint_write(
         _ptr(x, dev), _CODES[x.dtype], rows, cols, ck, _stream(stream, dev))
     _check("loco_checkpoint_write", st)
@@ -468,7 +501,7 @@ def loco_checkpoint_read(codes, exps, *, out, block: int = 64, act: int = LOCO_A
     """out = act(the values of the checkpoint); the matrix's shape is out's."""
     dev = _device()
     rows, cols = _rows_cols(out, "out", _FLOATS)
-    ck = _checkpoint((codes, exps), block, rows, cols, dev)
+    ck = _checkpoint((codes, exps), block, out.shape, rows, cols, dev)
     st = (_lib or load()).loco_checkpoint_read(
         ck, rows, cols, act, _ptr(out, dev), _CODES[out.dtype], _stream(stream, dev))
     _check("loco_checkpoint_read", st)
@@ -485,9 +518,10 @@ def loco_linear(x, weight, *, out, bias=None, act: int = LOCO_ACT_NONE, residual
     if wk != k:
         raise ValueError(f"x has {k} columns, weight {wk}")
     _sized(bias, n, "bias", _BF)
-    _sized(residual, rows * n, "residual", _BF)
-    _sized(out, rows * n, "out", _FLOATS)
-    ck = _checkpoint(checkpoint, block, rows, n, dev)
+    like = x.shape
+    _matrix(residual, like, rows, n, "residual", _BF)
+    _matrix(out, like, rows, n, "out", _FLOATS)
+    ck = _checkpoint(checkpoint, block, like, rows, n, dev)
     st = (_lib or load()).loco_linear(
         _ptr(x, dev), _ptr(weight, dev), _ptr(bias, dev), _ptr(residual, dev), rows, n, k, act, _ptr(out, dev),
         _CODES[out.dtype], ck, _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
@@ -507,9 +541,10 @@ def loco_linear_input_grad(dy, weight, *, out, act: int = LOCO_ACT_NONE, checkpo
     wn, k = _rows_cols(weight, "weight", _BF)
     if wn != n:
         raise ValueError(f"dy has {n} columns, weight {wn} rows")
-    _sized(residual, rows * k, "residual", _BF)
-    _sized(out, rows * k, "out", _FLOATS)
-    ck = _checkpoint(checkpoint, block, rows, k, dev)
+    like = dy.shape
+    _matrix(residual, like, rows, k, "residual", _BF)
+    _matrix(out, like, rows, k, "out", _FLOATS)
+    ck = _checkpoint(checkpoint, block, like, rows, k, dev)
     st = (_lib or load()).loco_linear_input_grad(
         _ptr(dy, dev), _ptr(weight, dev), _ptr(residual, dev), rows, n, k, act, ck, _ptr(out, dev), _CODES[out.dtype],
         _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
@@ -531,7 +566,7 @@ def loco_linear_weight_grad(dy, checkpoint, *, out, block: int = 64, act: int = 
     if wn != n:
         raise ValueError(f"dy has {n} columns, out {wn} rows")
     _sized(dbias, n, "dbias", (out.dtype,))
-    ck = _checkpoint(checkpoint, block, rows, k, dev)
+    ck = _checkpoint(checkpoint, block, dy.shape, rows, k, dev)
     st = (_lib or load()).loco_linear_weight_grad(
         _ptr(dy, dev), ck, rows, n, k, act, 1 if accumulate else 0, _ptr(out, dev), _ptr(dbias, dev),
         _CODES[out.dtype], _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
