@@ -2,7 +2,7 @@
 // activation.  The format is described in loco_layer.hpp.
 //
 // Both kernels are bound by HBM (3 bytes per bf16 element): 8192 x 11008 is written in 38 - 50 us
-// and read through GELU in 45 (5.4 TB/s and more; a streaming copy reaches 6.4).  A lane takes
+// and read through GELU in 44 - 48 (5.4 TB/s and more; a streaming copy reaches 6.4).  A lane takes
 // a chunk of eight elements, 16 bytes of bf16; a block is an aligned group of four or eight
 // lanes, so its largest value meets in two or three lane exchanges.
 

@@ -9,8 +9,9 @@
 // four or eight waves together a wider row.  All sums are fp32; the
 // variance is the mean of squared differences from the mean, not a difference of squares.
 // Measured at 16384 x 4096 in bf16: forward 51 us (5.2 TB/s, as torch's copy of the same
-// bytes), 67 with a checkpoint of y; backward with a residual 110 (5.0 TB/s).  The smallest
-// calls take one launch's 4 us.
+// bytes), 67 with a checkpoint of y; backward with a residual 110 (5.0 TB/s).  In fp32: forward
+// 100 us (5.4 TB/s), backward without a residual 167 (4.8).  The smallest calls take one launch's
+// 4 us.
 
 #include "loco_layer.hpp"
 #include "loco_layer_internal.hpp"
@@ -149,7 +150,9 @@ const void* pick_ln(LnShape s) {
 // and db over all its rows in registers; at the end the teams' sums meet in LDS and one
 // partial sum per workgroup goes to memory, to be joined by a second kernel.  Large workgroups
 // keep those few: at 16384 x 4096 1024 workgroups of one row wrote and read 66 MB of them beside
-// 403 MB of work, 256 of four rows a quarter.
+// 403 MB of work, 256 of four rows a quarter.  With few rows they weigh more: 1023 x 2047 in fp32
+// leaves 8.4 MB of them, as much as x, and takes 11 us here (30 % of the LDS cycles are conflicts
+// of the teams' join) and 5 in the join.
 
 template <typename T, int WPR, int NP, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, NP == 1 ? 6 : NP == 2 ? 4 : 2) void ln_bwd_kernel(const LnBwdParams p) {

@@ -511,7 +511,9 @@ def loco_linear(x, weight, *, out, bias=None, act: int = LOCO_ACT_NONE, residual
                 block: int = 64, workspace=None, stream=None) -> None:
     """out = act(x weight^T + bias) + residual, with weight [out_features, in_features];
     `checkpoint`, if given, is written with the 8-bit checkpoint of the activation's input.
-    bfloat16, out bfloat16 or float32."""
+    bfloat16, out bfloat16 or float32.  workspace: a tensor of linear_workspace(rows,
+    out_features, in_features) bytes; up to 16 rows of at most 4096 features need none without
+    a checkpoint."""
     dev = _device()
     rows, k = _rows_cols(x, "x", _BF)
     n, wk = _rows_cols(weight, "weight", _BF)
@@ -559,7 +561,8 @@ def loco_linear_weight_grad(dy, checkpoint, *, out, block: int = 64, act: int = 
                             accumulate: bool = False, workspace=None, stream=None) -> None:
     """out [out_features, in_features] = dy^T act(the checkpoint's values), dbias = dy summed
     over the rows; with accumulate, added to what they hold.  out and dbias are bfloat16
-    or float32, alike."""
+    or float32, alike.  GELU's and SiLU's values are rounded to bfloat16 for bfloat16 gradients
+    and enter as two bfloat16 numbers, in twice the time, for float32 ones."""
     dev = _device()
     rows, n = _rows_cols(dy, "dy", _BF)
     wn, k = _rows_cols(out, "out", _FLOATS)

@@ -286,8 +286,9 @@ int loco_sparse_aggregate(const loco_sparse_payload_t* peers, int npeers, int64_
  * NULL); its contents before and after are unspecified.  Sums, statistics and
  * accumulators are fp32 (the matrix cores' products of bf16 are exact in it); fused
  * multiply-adds are used, and sums run in an order of the library's own that depends on
- * the sizes only, so the same call gives the same bits.  Infinities and NaNs in the
- * inputs follow IEEE arithmetic into the outputs they reach.
+ * the sizes (and, up to 16 rows of loco_linear, on whether a checkpoint is written), so the
+ * same call gives the same bits.  Infinities and NaNs in the inputs follow IEEE arithmetic
+ * into the outputs they reach.
  * ------------------------------------------------------------------------------ */
 
 /* Activations a(z). */
@@ -401,7 +402,8 @@ int64_t loco_linear_input_grad_workspace(int64_t rows, int64_t out_features, int
  *   dy          device bf16[rows, out_features]
  *   dweight     device [out_features, in] of `grad_dtype`
  *   dbias       device [out_features] of `grad_dtype`, or NULL
- *   accumulate  nonzero: added to what dweight and dbias hold (in fp32, rounded once)
+ *   accumulate  nonzero: added to what dweight and dbias hold (in fp32, rounded once per
+ *               product)
  * With rows 0 the gradients are zero.
  */
 int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t* ckpt, int64_t rows,
