@@ -562,8 +562,9 @@ def _own_adamw(s, loco):
     loco.adamw(s["plan"], grad_scale=s["grad_scale"], **ADAMW)
     if case["bits"] == 8:
         if "states" not in s:
-            s["states"] = [(st, r) for t, rs in zip(s["tensors"], s["read"]) for st, r in zip(t[2:4], rs)]
-        loco.adamw_state_read(s["states"], block=case["block"])
+            s["states"] = loco.AdamwStates([(st, r) for t, rs in zip(s["tensors"], s["read"])
+                                            for st, r in zip(t[2:4], rs)], block=case["block"])
+        loco.adamw_state_read(s["states"])
     return _adamw_outputs(s)
 
 
