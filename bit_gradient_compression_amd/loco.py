@@ -35,7 +35,7 @@ SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequ
            "loco_version", "loco_layer_norm", "loco_layer_norm_backward", "loco_layer_norm_backward_workspace",
            "loco_checkpoint_write", "loco_checkpoint_read", "loco_linear", "loco_linear_workspace",
            "loco_linear_input_grad", "loco_linear_input_grad_workspace", "loco_linear_weight_grad",
-           "loco_linear_weight_grad_workspace"]
+           "loco_linear_weight_grad_workspace", "loco_adamw", "loco_adamw_state_read", "loco_adamw_state_write"]
 
 
 class LocoError(RuntimeError):
@@ -70,6 +70,22 @@ class SparsePayload(ctypes.Structure):
 
 class Checkpoint(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("block", ctypes.c_int)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_exps", ctypes.c_void_p), ("v_exps", ctypes.c_void_p), ("param_bf16", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
+
+
+class AdamwOptions(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
+class AdamwState(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("values", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("moment", ctypes.c_int)]
 
 
 _lib = None
@@ -126,7 +142,11 @@ def load(path: str | None = None):
             ("loco_linear_input_grad", i32, [ptr, ptr, ptr, i64, i64, i64, i32, ckpt, ptr, i32, ptr, i64, ptr]),
             ("loco_linear_input_grad_workspace", i64, [i64, i64, i64]),
             ("loco_linear_weight_grad", i32, [ptr, ckpt, i64, i64, i64, i32, i32, ptr, ptr, i32, ptr, i64, ptr]),
-            ("loco_linear_weight_grad_workspace", i64, [i64, i64, i64, i32])):
+            ("loco_linear_weight_grad_workspace", i64, [i64, i64, i64, i32]),
+            ("loco_adamw", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ctypes.POINTER(AdamwOptions),
+                                 ptr, ptr]),
+            ("loco_adamw_state_read", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr]),
+            ("loco_adamw_state_write", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr])):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = res
     lib.loco_status_string.argtypes = [ctypes.c_int]
@@ -581,6 +601,134 @@ def loco_linear_weight_grad_workspace(rows: int, out_features: int, in_features:
     return load().loco_linear_weight_grad_workspace(rows, out_features, in_features, act)
 
 
+# -- AdamW over many tensors ---------------------------------------------------------------
+
+def _keep(t):
+    """The tensor's memory, held for as long as the result lives."""
+    return None if t is None else t.detach()
+
+
+def _state(state, n, nb, what, dev):
+    """(codes or values, exps or None), checked, and the bits of the state."""
+    if isinstance(state, torch.Tensor):
+        _sized(state, n, what, _F32)
+        return state, None, 32
+    codes, exps = state
+    _sized(codes, n, f"{what} codes", (torch.float8_e4m3fn if what == "m" else torch.uint8,))
+    _sized(exps, nb, f"{what} exps", (torch.uint8,))
+    return codes, exps, 8
+
+
+class AdamwTensors:
+    """The tensors of loco_adamw, checked and described once; a training loop keeps it from step to
+    step.  tensors: an iterable of (param, grad, m, v[, param_bf16[, weight_decay]]): param
+    float32 or bfloat16, grad float32 or bfloat16, m and v float32, or in 8 bits (m: (codes
+    float8_e4m3fn, exps uint8), v: (codes uint8, exps uint8), one exps byte per block); every
+    param, every grad and every state of one kind.  param_bf16 (or None) receives the bfloat16 copy
+    of a float32 param.  weight_decay is that of the tensors that do not give one.  The memory of
+    the tensors is kept alive and must not be resized; later calls use it as it is now,
+    on the device that is current now."""
+
+    def __init__(self, tensors, *, block: int = 256, weight_decay: float = 0.0):
+        self.device, self.block = _device(), block
+        dev, rows, keep = self.device, [], []
+        self.param_dtype = self.grad_dtype = self.bits = None
+        for i, t in enumerate(tensors):
+            param, grad, m, v, copy, decay = (*t, None, None)[:6] if 4 <= len(t) <= 6 else _bad_tuple(i)
+            if param.dtype not in _CODES or grad.dtype not in _CODES:
+                raise TypeError(f"tensor {i}: param and grad must be float32 or bfloat16")
+            n = param.numel()
+            nb = num_blocks(n, block) if block > 0 else 0
+            _sized(grad, n, f"tensor {i}: grad", _FLOATS)
+            m, me, bits = _state(m, n, nb, "m", dev)
+            v, ve, vbits = _state(v, n, nb, "v", dev)
+            kind = (param.dtype, grad.dtype, bits)
+            if vbits != bits or (i and kind != (self.param_dtype, self.grad_dtype, self.bits)):
+                raise TypeError(f"tensor {i}: all params, grads and states must be of one kind")
+            self.param_dtype, self.grad_dtype, self.bits = kind
+            if copy is not None and param.dtype != torch.float32:
+                raise TypeError(f"tensor {i}: param_bf16 goes with a float32 param")
+            _sized(copy, n, f"tensor {i}: param_bf16", _BF)
+            parts = (param, grad, m, v, me, ve, copy)
+            rows.append((*(_ptr(x, dev) for x in parts), n, weight_decay if decay is None else decay))
+            keep.append(tuple(_keep(x) for x in parts))
+        self._keep, self.count = keep, len(rows)
+        self.array = (AdamwTensor * max(1, len(rows)))(*(AdamwTensor(*r) for r in rows))
+
+
+def _bad_tuple(i):
+    raise ValueError(f"tensor {i}: expected (param, grad, m, v[, param_bf16[, weight_decay]])")
+
+
+def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float | None = None, block: int | None = None, grad_scale=None, stream=None) -> None:
+    """One AdamW step (decoupled weight decay, bias correction) of all tensors.  tensors: an
+    AdamwTensors, which has its own block and weight_decay, or what its constructor takes.  beta1
+    and beta2 are the weights of the old moments; step counts from 1; grad_scale is a float32 tensor of
+    one element, or None.  lr, step and the others are read during the call: a captured graph
+    repeats them."""
+    if not isinstance(tensors, AdamwTensors):
+        tensors = AdamwTensors(tensors, block=256 if block is None else block, weight_decay=weight_decay or 0.0)
+    elif block is not None or weight_decay is not None:
+        raise ValueError("an AdamwTensors has its own block and weight_decay")
+    dev = _device()
+    if dev != tensors.device:
+        raise ValueError(f"the tensors are on cuda:{tensors.device}; the call runs on the current device, cuda:{dev}")
+    _sized(grad_scale, 1, "grad_scale", _F32)
+    opt = AdamwOptions(lr, beta1, beta2, eps, step)
+    st = (_lib or load()).loco_adamw(
+        tensors.array, tensors.count, _CODES.get(tensors.param_dtype, LOCO_F32),
+        _CODES.get(tensors.grad_dtype, LOCO_F32), tensors.bits or 32, tensors.block, ctypes.byref(opt),
+        _ptr(grad_scale, dev), _stream(stream, dev))
+    _check("loco_adamw", st)
+
+
+class AdamwStates:
+    """8-bit states and the tensors of their values, checked and described once.  states: an
+    iterable of ((codes, exps), values), values float32 or bfloat16, all alike; codes in
+    float8_e4m3fn are a first moment, in uint8 a second one.  Memory as in AdamwTensors."""
+
+    def __init__(self, states, *, block: int = 256):
+        self.device, self.block, self.dtype = _device(), block, None
+        dev, rows, keep = self.device, [], []
+        for i, ((codes, exps), values) in enumerate(states):
+            n = codes.numel()
+            if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError(f"state {i}: codes must be float8_e4m3fn or uint8, not {codes.dtype}")
+            _sized(exps, num_blocks(n, block) if block > 0 else 0, f"state {i}: exps", (torch.uint8,))
+            _sized(values, n, f"state {i}: values", _FLOATS if i == 0 else (self.dtype,))
+            self.dtype = values.dtype
+            rows.append((_ptr(codes, dev), _ptr(exps, dev), _ptr(values, dev), n,
+                         1 if codes.dtype == torch.float8_e4m3fn else 2))
+            keep.append((_keep(codes), _keep(exps), _keep(values)))
+        self._keep, self.count = keep, len(rows)
+        self.array = (AdamwState * max(1, len(rows)))(*(AdamwState(*r) for r in rows))
+
+
+def _adamw_states(name, states, block, stream):
+    if not isinstance(states, AdamwStates):
+        states = AdamwStates(states, block=256 if block is None else block)
+    elif block is not None:
+        raise ValueError("an AdamwStates has its own block")
+    dev = _device()
+    if dev != states.device:
+        raise ValueError(f"the states are on cuda:{states.device}; the call runs on the current device, cuda:{dev}")
+    st = getattr(_lib or load(), name)(states.array, states.count, states.block, _CODES.get(states.dtype, LOCO_F32),
+                                       _stream(stream, dev))
+    _check(name, st)
+
+
+def loco_adamw_state_read(states, *, block: int | None = None, stream=None) -> None:
+    """values = what the 8-bit states stand for, exactly.  states: an AdamwStates, or what its
+    constructor takes."""
+    _adamw_states("loco_adamw_state_read", states, block, stream)
+
+
+def loco_adamw_state_write(states, *, block: int | None = None, stream=None) -> None:
+    """The 8-bit states of the values, rounded as loco_adamw rounds them."""
+    _adamw_states("loco_adamw_state_write", states, block, stream)
+
+
 # short names
 compensate_quantize = loco_compensate_quantize
 compensate_quantize_ex = loco_compensate_quantize_ex
@@ -599,3 +747,6 @@ linear_input_grad = loco_linear_input_grad
 linear_input_grad_workspace = loco_linear_input_grad_workspace
 linear_weight_grad = loco_linear_weight_grad
 linear_weight_grad_workspace = loco_linear_weight_grad_workspace
+adamw = loco_adamw
+adamw_state_read = loco_adamw_state_read
+adamw_state_write = loco_adamw_state_write

@@ -413,6 +413,87 @@ int loco_linear_weight_grad(const uint16_t* dy, const loco_checkpoint_t* ckpt, i
 int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_features, int64_t in_features,
                                           loco_act_t act);
 
+/* ---------------------------------------------------------------------------------
+ * AdamW over many tensors at once, with states in fp32 or in 8 bits: the step of the parameters
+ * whose gradient does not arrive as payloads of loco_dequant_reduce_adam, or whose states
+ * should take 2 bytes and not 8.
+ *
+ * An 8-bit state of n elements has blocks of `block` elements from element 0 (the last may be
+ * partial), each with one exponent byte.
+ *   first moment   codes u8[n]: float8 of 4 exponent and 3 mantissa bits (bias 7, largest 448,
+ *                  torch.float8_e4m3fn) times 2^(exps - 127), the least power of two
+ *                  (>= 2^-117) that keeps the block's largest magnitude within 448
+ *   second moment  codes u8[n]: 0 is 0; a code c > 0 is (1 + (c & 7)/8) * 2^((c >> 3) - 31 + exps -
+ *                  127), with exps (>= 32; read as 32 below) the biased exponent of the block's
+ *                  largest value rounded to 4 significant bits.  Values that are not 0 are
+ *                  never stored as 0, but as the code 1 at least; values < 0 are stored as 0
+ *   exps   u8[ceil(n/block)]
+ * Each value is rounded once, ties to even, to four significant bits (fewer where a first
+ * moment is below 2^-14 of its block's range).  A block that holds an infinity or a NaN (or a
+ * second moment that rounds to 2^128) is stored with exps 255 and codes 0 and reads as NaN.  A
+ * state whose codes are 0 is 0, whatever its exps below 255.  What changes a second moment by
+ * less than half a step (beta2 0.999 and a squared gradient below 60 times the moment) is lost in
+ * the rounding: take beta2 0.95 or so with 8 bits.
+ * ------------------------------------------------------------------------------ */
+
+/* One tensor (host struct, read during the call). */
+typedef struct {
+    void* param;          /* device, n elements of param_dtype, updated in place */
+    const void* grad;     /* device, n elements of grad_dtype */
+    void* m;              /* device, f32[n] or codes u8[n], updated in place */
+    void* v;              /* the same */
+    uint8_t* m_exps;      /* device u8[ceil(n/block)], updated; unused with states in fp32 */
+    uint8_t* v_exps;
+    uint16_t* param_bf16; /* device (written: the RNE bf16 copy of the new param), or NULL; LOCO_F32 only */
+    int64_t n;            /* elements (>= 0; 0 is a no-op) */
+    double weight_decay;  /* finite */
+} loco_adamw_tensor_t;
+
+/* Hyper-parameters (host struct, read during the call: a captured graph repeats them). */
+typedef struct {
+    double lr;           /* finite */
+    double beta1, beta2; /* in [0, 1): the weights of the OLD moments (unlike loco_adam_t) */
+    double eps;          /* > 0, and as a float too */
+    int64_t step;        /* >= 1: this step's number t */
+} loco_adamw_t;
+
+/*
+ * loco_adamw - for every element, in IEEE fp32 operations in this order:
+ *   g     = grad * grad_scale[0]                      (grad_scale NULL: g = grad)
+ *   m     = beta1 * m + (1 - beta1) * g
+ *   v     = beta2 * v + (1 - beta2) * (g * g)
+ *   param = param * (1 - lr * weight_decay)
+ *           - lr / (1 - beta1^t) * (m / (sqrt(v) * (1 / sqrt(1 - beta2^t)) + eps))
+ * with each host-side factor rounded to fp32 once.  With 8-bit states the parameter's update takes
+ * m and v before they are rounded into their codes.
+ *   tensors     host array of ntensors (>= 0); 48 of them take one launch
+ *   state_bits  32 or 8;  block  64, 128, 256 or 512 (ignored with 32)
+ *   grad_scale  device f32[1] (read), such as a clipping factor, or NULL
+ * No buffer that the call writes may overlap another of its buffers.
+ */
+int loco_adamw(const loco_adamw_tensor_t* tensors, int ntensors, loco_dtype_t param_dtype,
+               loco_dtype_t grad_dtype, int state_bits, int block, const loco_adamw_t* options,
+               const float* grad_scale, void* stream);
+
+/* One 8-bit state and its values (host struct, read during the call). */
+typedef struct {
+    uint8_t* codes; /* device u8[n] */
+    uint8_t* exps;  /* device u8[ceil(n/block)] */
+    void* values;   /* device, n elements */
+    int64_t n;
+    int moment;     /* 1 or 2 */
+} loco_adamw_state_t;
+
+/*
+ * loco_adamw_state_read  - values = what the states stand for, in `dtype` (LOCO_F32 or LOCO_BF16,
+ *                          both exact).
+ * loco_adamw_state_write - the states of the values, as loco_adamw stores them.
+ */
+int loco_adamw_state_read(const loco_adamw_state_t* states, int nstates, int block,
+                          loco_dtype_t dtype, void* stream);
+int loco_adamw_state_write(const loco_adamw_state_t* states, int nstates, int block,
+                           loco_dtype_t dtype, void* stream);
+
 /* A static, human-readable name for a status code. */
 const char* loco_status_string(int status);
 

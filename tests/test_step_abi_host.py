@@ -1,0 +1,181 @@
+"""Refusals of the step operators' C calls and of their binding, without a GPU: every bad argument
+gets its status before any HIP call.  The pointers are fake and never dereferenced."""
+import ctypes
+
+import pytest
+import torch
+
+if torch.cuda.is_available():
+    # Fake pointers must never reach a real device: these checks run only where no GPU is.
+    pytest.skip("host-only validation tests (fake device pointers)", allow_module_level=True)
+
+from bit_gradient_compression_amd import loco  # noqa: E402
+
+OK, INV, ALIGN, UNSUP = loco.LOCO_OK, loco.LOCO_ERR_INVALID, loco.LOCO_ERR_ALIGN, loco.LOCO_ERR_UNSUPPORTED
+F32, BF16, I8 = loco.LOCO_F32, loco.LOCO_BF16, loco.LOCO_I8
+NAN, INF = float("nan"), float("inf")
+P = [0x100000000 * (i + 1) for i in range(16)]  # fake, aligned, 4 GiB apart
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return loco.load()
+
+
+# -- AdamW ------------------------------------------------------------------------------------
+
+def tensor(param=P[0], grad=P[1], m=P[2], v=P[3], me=P[4], ve=P[5], copy=P[6], n=1000, wd=0.1):
+    return loco.AdamwTensor(param, grad, m, v, me, ve, copy, n, wd)
+
+
+def adamw(lib, ts=None, nt=None, pd=F32, gd=BF16, bits=8, block=256, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, step=1,
+          scale=P[7], null=False):
+    ts = [tensor()] if ts is None else ts
+    arr = (loco.AdamwTensor * max(1, len(ts)))(*ts)
+    opt = loco.AdamwOptions(lr, b1, b2, eps, step)
+    return lib.loco_adamw(arr if ts else None, len(ts) if nt is None else nt, pd, gd, bits, block,
+                          None if null else ctypes.byref(opt), scale, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(nt=-1), INV), (dict(ts=[], nt=1), INV), (dict(ts=[]), OK), (dict(null=True), INV),
+    (dict(pd=I8), INV), (dict(gd=I8), INV), (dict(pd=5), INV), (dict(bits=4), INV), (dict(bits=16), INV),
+    (dict(block=0), INV), (dict(block=-64), INV), (dict(block=100), UNSUP), (dict(block=1024), UNSUP),
+    (dict(lr=NAN), INV), (dict(lr=INF), INV), (dict(lr=1e300), INV), (dict(b1=1.0), INV), (dict(b1=-0.1), INV),
+    (dict(b2=1.0), INV), (dict(b2=NAN), INV), (dict(eps=0.0), INV), (dict(eps=-1e-8), INV), (dict(eps=1e-60), INV),
+    (dict(eps=1e39), INV), (dict(eps=NAN), INV), (dict(step=0), INV), (dict(step=-3), INV), (dict(scale=P[7] + 4), ALIGN),
+    (dict(scale=P[0] + 16), INV), (dict(scale=P[5]), INV), (dict(scale=None, ts=[tensor(n=0)]), OK),
+])
+def test_adamw_arguments(lib, kw, want):
+    assert adamw(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), INV), (dict(n=(1 << 52) + 1), INV), (dict(wd=NAN), INV), (dict(wd=INF), INV), (dict(wd=1e300), INV),
+    (dict(param=None), INV), (dict(grad=None), INV), (dict(m=None), INV), (dict(v=None), INV), (dict(me=None), INV),
+    (dict(ve=None), INV), (dict(param=P[0] + 4), ALIGN), (dict(grad=P[1] + 2), ALIGN), (dict(m=P[2] + 1), ALIGN),
+    (dict(v=P[3] + 8), ALIGN), (dict(me=P[4] + 1), ALIGN), (dict(ve=P[5] + 2), ALIGN), (dict(copy=P[6] + 2), ALIGN),
+    (dict(grad=P[0]), INV), (dict(m=P[0] + 3984), INV), (dict(v=P[2]), INV), (dict(me=P[4], ve=P[4]), INV),
+    (dict(copy=P[0]), INV), (dict(copy=P[1]), INV), (dict(ve=P[6] + 1984), INV),
+    (dict(n=0, param=None, grad=None, m=None, v=None, me=None, ve=None, copy=None), OK),
+])
+def test_adamw_tensor(lib, kw, want):
+    assert adamw(lib, [tensor(**kw)]) == want
+    # the same with a good tensor before it, elsewhere
+    far = tensor(*(p + (1 << 30) for p in P[8:15]))
+    if want != OK:
+        assert adamw(lib, [far, tensor(**kw)]) == want
+
+
+def test_adamw_across_tensors(lib):
+    far = [p + (1 << 30) for p in P[8:15]]
+    assert adamw(lib, [tensor(), tensor()]) == INV  # the same tensor twice
+    for i in (0, 2, 3, 4, 5, 6):  # one buffer shared with another tensor's
+        q = list(far)
+        q[i] = P[i]
+        assert adamw(lib, [tensor(), tensor(*q)]) == INV, i
+    q = list(far)
+    q[1] = P[2]  # a gradient over another tensor's state
+    assert adamw(lib, [tensor(), tensor(*q)]) == INV
+
+
+def test_adamw_copy_needs_fp32_params(lib):
+    assert adamw(lib, pd=BF16) == INV
+
+
+def state(codes=P[0], exps=P[1], values=P[2], n=1000, moment=1):
+    return loco.AdamwState(codes, exps, values, n, moment)
+
+
+@pytest.mark.parametrize("s,kw,want", [
+    ([], dict(), OK), ([], dict(ns=1), INV), ([state()], dict(ns=-1), INV), ([state()], dict(block=96), UNSUP),
+    ([state()], dict(block=0), INV), ([state()], dict(dtype=I8), INV), ([state(n=-1)], dict(), INV),
+    ([state(moment=0)], dict(), INV), ([state(moment=3)], dict(), INV), ([state(codes=None)], dict(), INV),
+    ([state(exps=None)], dict(), INV), ([state(values=None)], dict(), INV), ([state(codes=P[0] + 1)], dict(), ALIGN),
+    ([state(exps=P[1] + 4)], dict(), ALIGN), ([state(values=P[2] + 2)], dict(), ALIGN),
+    ([state(values=P[0] + 16)], dict(), INV), ([state(values=P[1])], dict(), INV), ([state(n=0)], dict(), OK),
+])
+def test_adamw_states(lib, s, kw, want):
+    a = dict(ns=len(s), block=256, dtype=BF16)
+    a.update(kw)
+    arr = (loco.AdamwState * max(1, len(s)))(*s)
+    for fn in (lib.loco_adamw_state_read, lib.loco_adamw_state_write):
+        assert fn(arr if s else None, a["ns"], a["block"], a["dtype"], None) == want
+
+
+def test_adamw_states_that_share(lib):
+    """Read, values must not be written twice but codes may be read twice; written, the other way round."""
+    for shared, bad in ((dict(values=P[2]), lib.loco_adamw_state_read), (dict(codes=P[0]), lib.loco_adamw_state_write)):
+        arr = (loco.AdamwState * 2)(state(), state(**{**dict(codes=P[3], exps=P[4], values=P[5]), **shared}))
+        assert bad(arr, 2, 256, BF16, None) == INV
+
+
+@pytest.fixture
+def no_device(monkeypatch):
+    """Host tensors: what passes the checks of sizes and types is refused for its memory, and says so."""
+    monkeypatch.setattr(loco, "_device", lambda: 0)
+
+
+def t(n, dtype=torch.float32):
+    return torch.zeros(n, dtype=dtype)
+
+
+F8, U8, BF = torch.float8_e4m3fn, torch.uint8, torch.bfloat16
+
+
+def eight(n, block=256):
+    return (t(n, F8), t(-(-n // block), U8)), (t(n, U8), t(-(-n // block), U8))
+
+
+@pytest.mark.parametrize("make,err,match", [
+    (lambda: (t(8), t(8), t(8), t(8)), ValueError, "device memory"),
+    (lambda: (t(8), t(8), *eight(8), None, 0.1), ValueError, "device memory"),
+    (lambda: (t(8), t(8), t(8)), ValueError, "expected"),
+    (lambda: (t(8), t(8), t(8), t(8), None, 0.1, 3), ValueError, "expected"),
+    (lambda: (t(8), t(9), t(8), t(8)), ValueError, "9 elements"),
+    (lambda: (t(8), t(8), t(7), t(8)), ValueError, "7 elements"),
+    (lambda: (t(8), t(8), t(8), t(8), t(9, BF)), ValueError, "9 elements"),
+    (lambda: (t(8, torch.float16), t(8), t(8), t(8)), TypeError, "float32 or bfloat16"),
+    (lambda: (t(8), t(8), t(8, BF), t(8)), TypeError, "m must be"),
+    (lambda: (t(8), t(8), t(8), t(8), t(8)), TypeError, "param_bf16"),
+    (lambda: (t(8, BF), t(8), t(8), t(8), t(8, BF)), TypeError, "param_bf16"),
+    (lambda: (t(8), t(8), t(8), eight(8)[1]), TypeError, "one kind"),
+    (lambda: (t(8), t(8), eight(8)[1], eight(8)[1]), TypeError, "m codes"),
+    (lambda: (t(8), t(8), eight(8)[0], eight(8)[0]), TypeError, "v codes"),
+    (lambda: (t(600), t(600), *eight(600, 128)), ValueError, "exps"),
+])
+def test_adamw_binding(no_device, make, err, match):
+    with pytest.raises(err, match=match):
+        loco.AdamwTensors([make()])
+
+
+def test_adamw_binding_kinds_and_plans(no_device, monkeypatch):
+    monkeypatch.setattr(loco, "_ptr", lambda t, dev: None if t is None else t.data_ptr())
+    with pytest.raises(TypeError, match="one kind"):
+        loco.AdamwTensors([(t(8), t(8), t(8), t(8)), (t(8), t(8, BF), t(8), t(8))])
+    plan = loco.AdamwTensors([(t(8), t(8), t(8), t(8))])
+    with pytest.raises(ValueError, match="its own"):
+        loco.adamw(plan, step=1, lr=1e-3, weight_decay=0.1)
+    with pytest.raises(ValueError, match="its own"):
+        loco.adamw(plan, step=1, lr=1e-3, block=256)
+    monkeypatch.setattr(loco, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        loco.adamw(plan, step=1, lr=1e-3)
+    states = loco.AdamwStates([])
+    monkeypatch.setattr(loco, "_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device"):
+        loco.adamw_state_read(states)
+    with pytest.raises(ValueError, match="its own"):
+        loco.adamw_state_write(loco.AdamwStates([]), block=128)
+
+
+@pytest.mark.parametrize("make,err,match", [
+    (lambda: ((t(8, F8), t(1, U8)), t(8)), ValueError, "device memory"),
+    (lambda: ((t(8, torch.int8), t(1, U8)), t(8)), TypeError, "codes"),
+    (lambda: ((t(8, F8), t(2, U8)), t(8)), ValueError, "exps"),
+    (lambda: ((t(8, F8), t(1, U8)), t(9)), ValueError, "9 elements"),
+    (lambda: ((t(8, U8), t(1, U8)), t(8, torch.float16)), TypeError, "values"),
+])
+def test_adamw_states_binding(no_device, make, err, match):
+    with pytest.raises(err, match=match):
+        loco.AdamwStates([make()])
