@@ -180,3 +180,106 @@ LOCO_API int loco_adamw_state_write(const loco_adamw_state_t* states, int nstate
                                     void* stream) {
     return adamw_states(states, nstates, block, dtype, true, stream);
 }
+
+// ---- the norms around a block -----------------------------------------------------------------
+
+namespace {
+
+bool gate_ok(int kind, const void* gate) {
+    return kind >= LOCO_GATE_NONE && kind <= LOCO_GATE_ELEMENT && (kind == LOCO_GATE_NONE) == (gate == nullptr);
+}
+
+}  // namespace
+
+LOCO_API int loco_residual_norm(const void* y, const void* residual, loco_dtype_t dtype, const void* gate,
+                                loco_gate_t gate_kind, const void* post_weight, const void* weight,
+                                loco_dtype_t param_dtype, int64_t rows, int64_t cols, float scale, float eps, void* h,
+                                void* out, float* post_rstd, float* rstd, const loco_checkpoint_t* ckpt, void* stream) {
+    if (!sizes_ok(rows, cols) || cols < 1) return LOCO_ERR_INVALID;
+    if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return LOCO_ERR_INVALID;
+    if (!isfinite(eps) || eps < 0.0f || !isfinite(scale)) return LOCO_ERR_INVALID;
+    if (ckpt) {
+        const int st = check_ckpt(*ckpt);
+        if (st != LOCO_OK) return st;
+    }
+    if (cols > kLnMaxCols) return LOCO_ERR_UNSUPPORTED;
+    if (gate_kind < LOCO_GATE_NONE || gate_kind > LOCO_GATE_ELEMENT) return LOCO_ERR_INVALID;
+    if (rows == 0) return LOCO_OK;
+    if (!gate_ok(gate_kind, gate)) return LOCO_ERR_INVALID;
+    if ((!y && !residual) || (!h && !out)) return LOCO_ERR_INVALID;
+    if (!y && (gate || post_rstd || post_weight)) return LOCO_ERR_INVALID;
+    if (post_weight && !post_rstd) return LOCO_ERR_INVALID;
+    if (out ? !rstd : rstd || ckpt || weight) return LOCO_ERR_INVALID;
+    const int64_t s = dtype_size(dtype), ps = dtype_size(param_dtype);
+    const int st = check_bufs({{y, rows * cols * s, false, false},
+                               {residual, rows * cols * s, false, false},
+                               {gate, gate_kind == LOCO_GATE_ELEMENT ? rows * cols * s : cols * ps, false, false},
+                               {post_weight, cols * ps, false, false},
+                               {weight, cols * ps, false, false},
+                               {h, rows * cols * s, true, false},
+                               {out, rows * cols * s, true, false},
+                               {post_rstd, rows * 4, true, false},
+                               {rstd, rows * 4, true, false},
+                               codes_buf(ckpt, rows, cols, true),
+                               exps_buf(ckpt, rows, cols, true)});
+    if (st != LOCO_OK) return st;
+    const RnParams p = {y, residual, gate, weight, post_weight, h, out, rstd, post_rstd, ckpt_dev(ckpt, cols), rows,
+                        (int)cols, scale, eps, gate_kind, dtype == LOCO_F32, param_dtype == LOCO_F32};
+    return hip_status(launch_rn(p, (hipStream_t)stream));
+}
+
+LOCO_API int64_t loco_residual_norm_backward_workspace(int64_t rows, int64_t cols) {
+    if (!sizes_ok(rows, cols) || cols < 1 || cols > kLnMaxCols) return 0;
+    return rn_bwd_groups(rows, cols) * 3 * cols * 4;
+}
+
+LOCO_API int loco_residual_norm_backward(const void* dout, const void* dh, const void* h, const void* y,
+                                         loco_dtype_t dtype, const void* gate, loco_gate_t gate_kind,
+                                         const void* post_weight, const void* weight, loco_dtype_t param_dtype,
+                                         const float* post_rstd, const float* rstd, int64_t rows, int64_t cols,
+                                         float scale, void* dresidual, void* dy, void* dgate, void* dpost_weight,
+                                         void* dweight, loco_dtype_t grad_dtype, void* workspace,
+                                         int64_t workspace_bytes, void* stream) {
+    if (!sizes_ok(rows, cols) || cols < 1) return LOCO_ERR_INVALID;
+    if (!dtype_ok(dtype) || !dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return LOCO_ERR_INVALID;
+    if (!isfinite(scale)) return LOCO_ERR_INVALID;
+    if (cols > kLnMaxCols) return LOCO_ERR_UNSUPPORTED;
+    if (gate_kind < LOCO_GATE_NONE || gate_kind > LOCO_GATE_ELEMENT) return LOCO_ERR_INVALID;
+    const bool elements = gate_kind == LOCO_GATE_ELEMENT;
+    void* sums[3] = {dweight, dpost_weight, elements ? nullptr : dgate};
+    const bool any_sum = sums[0] || sums[1] || sums[2];
+    if (rows > 0) {
+        if (!gate_ok(gate_kind, gate) || (!dout && !dh)) return LOCO_ERR_INVALID;
+        if (dout ? (!h || !rstd) : (dweight != nullptr)) return LOCO_ERR_INVALID;
+        if (post_weight && !post_rstd) return LOCO_ERR_INVALID;
+        if ((post_rstd || gate) && !y) return LOCO_ERR_INVALID;
+        if (dpost_weight && !post_rstd) return LOCO_ERR_INVALID;
+        if (!dresidual && !dy && !dgate && !any_sum) return LOCO_ERR_INVALID;
+    }
+    if (dgate && gate_kind == LOCO_GATE_NONE) return LOCO_ERR_INVALID;
+    const int64_t need = any_sum ? loco_residual_norm_backward_workspace(rows, cols) : 0;
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    if (rows == 0 && !any_sum) return LOCO_OK;
+    const int64_t s = dtype_size(dtype), ps = dtype_size(param_dtype), gs = dtype_size(grad_dtype);
+    const int st = check_bufs({{dout, rows * cols * s, false, false},
+                               {dh, rows * cols * s, false, false},
+                               {h, rows * cols * s, false, false},
+                               {y, rows * cols * s, false, false},
+                               {gate, elements ? rows * cols * s : cols * ps, false, false},
+                               {post_weight, cols * ps, false, false},
+                               {weight, cols * ps, false, false},
+                               {post_rstd, rows * 4, false, false},
+                               {rstd, rows * 4, false, false},
+                               {dresidual, rows * cols * s, true, false},
+                               {dy, rows * cols * s, true, false},
+                               {dgate, elements ? rows * cols * s : cols * gs, true, false},
+                               {dpost_weight, cols * gs, true, false},
+                               {dweight, cols * gs, true, false},
+                               {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    const RnBwdParams p = {dout, dh, h, y, gate, weight, post_weight, rstd, post_rstd, dresidual, dy,
+                           elements ? dgate : nullptr, {sums[0], sums[1], sums[2]}, any_sum ? (float*)workspace : nullptr,
+                           rows, (int)cols, scale, gate_kind, dtype == LOCO_F32, param_dtype == LOCO_F32,
+                           grad_dtype == LOCO_F32};
+    return hip_status(launch_rn_bwd(p, (hipStream_t)stream));
+}

@@ -55,4 +55,51 @@ struct AwStateParams {
 };
 hipError_t launch_aw_state(const AwStateParams& p, int block, bool f32, bool write, hipStream_t stream);
 
+// ---- the norms around a block ----------------------------------------------------------
+
+enum : int { kGateNone = 0, kGateColumn = 1, kGateElement = 2 };
+
+struct RnParams {
+    const void* y;            // may be null: only the residual
+    const void* residual;     // may be null: 0
+    const void* gate;         // [cols] of the parameters' type, or [rows, cols]
+    const void* weight;       // may be null: ones
+    const void* post_weight;  // may be null: ones
+    void* h;                  // may be null
+    void* out;                // may be null
+    float* rstd;              // with out
+    float* post_rstd;         // null: y is not normed
+    CkptDev ckpt;
+    int64_t rows;
+    int cols;
+    float scale, eps;
+    int gate_kind;
+    int f32, param_f32;
+};
+hipError_t launch_rn(const RnParams& p, hipStream_t stream);
+
+struct RnBwdParams {
+    const void* dout;  // may be null: 0
+    const void* dh;    // may be null: 0
+    const void* h;     // with dout
+    const void* y;     // where post_rstd, dgate or dpost_weight need it
+    const void* gate;
+    const void* weight;
+    const void* post_weight;
+    const float* rstd;
+    const float* post_rstd;
+    void* dresidual;  // may be null
+    void* dy;         // may be null
+    void* dgate_rows; // gradient of a gate of elements; may be null
+    void* sums[3];    // dweight, dpost_weight, a column gate's gradient; each may be null
+    float* part;      // [groups][3][cols] partial sums; null: no sums
+    int64_t rows;
+    int cols;
+    float scale;
+    int gate_kind;
+    int f32, param_f32, grad_f32;
+};
+int64_t rn_bwd_groups(int64_t rows, int64_t cols);
+hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream);
+
 }  // namespace loco

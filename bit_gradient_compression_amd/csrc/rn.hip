@@ -1,0 +1,647 @@
+// The norms around a transformer block, fused with its gate and residual, forward and backward.
+//
+// Forward, per row: rp = 1/sqrt(mean y^2 + eps), u = y rp wp (or u = y); h = residual + s g u;
+// r = 1/sqrt(mean h^2 + eps), out = h r w.  Backward, with xh = h r and yh = y rp:
+//   dh' = dh + r (dout w - xh mean(dout w xh))            the gradient of h, and of the residual
+//   dy  = rp (t - yh mean(t yh)),  t = s g dh' wp         (or dy = s g dh')
+//   dw = sum over rows of dout xh,  dwp = sum of s g dh' yh,  dg = s dh' u, summed for a gate of columns
+//
+// Both are bound by HBM: each element is read once and written once.  A row stays in registers from
+// its loads to its stores, through both of its sums; all sums are fp32.
+
+#include "loco_layer.hpp"
+#include "loco_step_internal.hpp"
+
+namespace loco {
+
+namespace {
+
+__device__ __forceinline__ int chunk_valid(int cols, int c) { return cols - c < 8 ? cols - c : 8; }
+
+// Sum over the WPR waves of a row; every lane gets it.  `slot` alternates between calls so that one
+// barrier per call is enough.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* red, int slot) {
+    v = wave_sum(v);
+    if constexpr (WPR > 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) red[slot * WPR + wave] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) v += red[slot * WPR + i];
+    }
+    return v;
+}
+
+__device__ __forceinline__ void fill(float (&v)[8], float x) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x;
+}
+
+// ---- forward --------------------------------------------------------------------------
+
+// WPR waves per row, NP chunks of eight per lane.
+template <typename T, int WPR, int NP>
+__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void rn_kernel(const RnParams p, int64_t row0) {
+    __shared__ float red[2 * WPR];
+    constexpr int RPW = WPR == 1 ? 4 : 1;  // rows per workgroup
+    constexpr int LANES = WPR * 64;
+    const int64_t row = row0 + (int64_t)blockIdx.x * RPW + (WPR == 1 ? uniform(threadIdx.x >> 6) : 0);
+    if (row >= p.rows) return;  // whole waves (WPR == 1: no barrier follows)
+    const int lane = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
+    const int cols = p.cols;
+    const float inv_cols = 1.0f / (float)cols;
+    RawChunk<T> y[NP], res[NP], gate[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int c = (i * LANES + lane) * 8;
+        const int valid = chunk_valid(cols, c);
+        if (p.y) y[i].load((const T*)p.y + row * cols + c, valid);
+        if (p.residual) res[i].load((const T*)p.residual + row * cols + c, valid);
+        if (p.gate_kind == kGateElement) gate[i].load((const T*)p.gate + row * cols + c, valid);
+    }
+    float v[8], h[NP][8];
+    float rp = 1.0f;
+    if (p.post_rstd) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            y[i].get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[j], v[j], sq);
+        }
+        rp = 1.0f / __builtin_sqrtf(row_sum<WPR>(sq, red, 0) * inv_cols + p.eps);
+        if (lane == 0) p.post_rstd[row] = rp;
+    }
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int c = (i * LANES + lane) * 8;
+        const int valid = chunk_valid(cols, c);
+        fill(h[i], 0.0f);
+        if (p.residual) res[i].get(h[i]);
+        if (p.y) {
+            float k[8], w[8];
+            fill(k, p.scale);
+            if (p.gate_kind != kGateNone) {
+                if (p.gate_kind == kGateElement) gate[i].get(w);
+                else load_chunk_any(p.gate, p.param_f32, c, valid, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) k[j] *= w[j];
+            }
+            y[i].get(v);
+            if (p.post_rstd) {
+                fill(w, 1.0f);
+                if (p.post_weight) load_chunk_any(p.post_weight, p.param_f32, c, valid, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * rp * w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] = __builtin_fmaf(k[j], v[j], h[i][j]);
+        }
+        if (p.h) store_chunk((T*)p.h + row * cols + c, valid, h[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            h[i][j] = j < valid ? h[i][j] : 0.0f;  // past the end 0 * rp may be a NaN
+            sq = __builtin_fmaf(h[i][j], h[i][j], sq);
+        }
+    }
+    if (!p.out) return;  // the whole grid
+    const float r = 1.0f / __builtin_sqrtf(row_sum<WPR>(sq, red, 1) * inv_cols + p.eps);
+    if (lane == 0) p.rstd[row] = r;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int c = (i * LANES + lane) * 8;
+        const int valid = chunk_valid(cols, c);
+        float w[8];
+        fill(w, 1.0f);
+        if (p.weight) load_chunk_any(p.weight, p.param_f32, c, valid, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < valid ? h[i][j] * r * w[j] : 0.0f;
+        store_chunk((T*)p.out + row * cols + c, valid, v);
+        if (p.ckpt.codes) {
+            // of the fp32 values, before their rounding to the output's type
+            const uint32_t e = ckpt_exp(block_top(v, p.ckpt.block64));
+            store_codes(p.ckpt.codes + row * cols + c, valid, ckpt_codes(v, e));
+            const int per = p.ckpt.block64 ? 8 : 4;
+            if ((lane & (per - 1)) == 0 && valid > 0)
+                p.ckpt.exps[row * p.ckpt.nblocks + c / (8 * per)] = (uint8_t)e;
+        }
+    }
+}
+
+struct RnShape {
+    int wpr, np;
+};
+RnShape rn_shape(int64_t cols) {
+    if (cols <= 512) return {1, 1};
+    if (cols <= 1024) return {1, 2};
+    if (cols <= 2048) return {4, 1};
+    if (cols <= 4096) return {4, 2};
+    if (cols <= 8192) return {8, 2};
+    return {8, 4};
+}
+template <typename T>
+const void* pick_rn(RnShape s) {
+    switch (s.wpr * 16 + s.np) {
+        case 16 + 1: return (const void*)&rn_kernel<T, 1, 1>;
+        case 16 + 2: return (const void*)&rn_kernel<T, 1, 2>;
+        case 64 + 1: return (const void*)&rn_kernel<T, 4, 1>;
+        case 64 + 2: return (const void*)&rn_kernel<T, 4, 2>;
+        case 128 + 2: return (const void*)&rn_kernel<T, 8, 2>;
+    }
+    return (const void*)&rn_kernel<T, 8, 4>;
+}
+
+// ---- backward -------------------------------------------------------------------------
+//
+// A workgroup of WAVES waves works TEAMS = WAVES / WPR rows at a time and keeps the column sums over
+// all its rows: dweight's in registers, the other two in LDS, where each lane has its own columns
+// (all three in registers leave room for too few rows at a time).  At the end the teams' sums meet in
+// LDS and one partial sum per workgroup goes to memory, to be joined by a second kernel in a fixed
+// order.
+//
+// A lane holds NP whole chunks of eight columns and, in the first lanes of a team, one of the up to
+// seven columns past the last whole chunk.  All of them are moved through buffer resources over the
+// row's whole chunks, or over its tail: the address is a scalar base and a 32-bit lane offset, and what
+// lies past the row's end reads as 0 and is not written, without a branch.  Branches for the columns
+// of a partial chunk and 64-bit lane addresses of each matrix took more registers than the values.
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+// `count` elements of a matrix or a vector of T from element `at` on.
+template <typename T>
+__device__ __forceinline__ Rsrc span_of(const void* p, int64_t at, uint32_t count) {
+    return buffer_rsrc((const T*)p + at, count * (uint32_t)sizeof(T));
+}
+
+// W consecutive elements, the first of them element i of a span, as they lie in memory.
+template <typename T, int W>
+struct Piece;
+template <>
+struct Piece<uint16_t, 8> {
+    u32x4 w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b128(r, i * 2, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(w, v); }
+    // Makes the compiler unpack the values again, instead of keeping them from one phase of a row to the
+    // next in registers of their own.
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(w)); }
+    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[8]) {
+        __builtin_amdgcn_raw_buffer_store_b128(pack_bf16x8(v), r, i * 2, 0, 0);
+    }
+};
+template <>
+struct Piece<float, 8> {
+    u32x4 a, b;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) {
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, 0);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4 + 16, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(a[j]);
+            v[4 + j] = __uint_as_float(b[j]);
+        }
+    }
+    __device__ __forceinline__ void forget() {}
+    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[8]) {
+        u32x4 a, b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = __float_as_uint(v[j]);
+            b[j] = __float_as_uint(v[4 + j]);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(a, r, i * 4, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(b, r, i * 4 + 16, 0, 0);
+    }
+};
+template <>
+struct Piece<uint16_t, 4> {
+    u32x2 w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b64(r, i * 2, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = bf16_lo(w.x);
+        v[1] = bf16_hi(w.x);
+        v[2] = bf16_lo(w.y);
+        v[3] = bf16_hi(w.y);
+    }
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(w)); }
+    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[4]) {
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])}, r, i * 2, 0, 0);
+    }
+};
+template <>
+struct Piece<float, 4> {
+    u32x4 a;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(a[j]);
+    }
+    __device__ __forceinline__ void forget() {}
+    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[4]) {
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                     __float_as_uint(v[3])}, r, i * 4, 0, 0);
+    }
+};
+template <>
+struct Piece<uint16_t, 1> {
+    uint32_t w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b16(r, i * 2, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float(w << 16); }
+    __device__ __forceinline__ void forget() {}
+    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[1]) {
+        __builtin_amdgcn_raw_buffer_store_b16(bf16_rne(v[0]), r, i * 2, 0, 0);
+    }
+};
+template <>
+struct Piece<float, 1> {
+    uint32_t w;
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b32(r, i * 4, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float(w); }
+    __device__ __forceinline__ void forget() {}
+    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[1]) {
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, i * 4, 0, 0);
+    }
+};
+
+// Elements i .. of a parameter vector from column c0 on, `count` of them; null: ones.
+template <int W>
+__device__ __forceinline__ void get_param(const void* p, bool f32, uint32_t c0, uint32_t count, uint32_t i, float (&v)[W]) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = 1.0f;
+    if (!p) return;
+    if (f32) {
+        Piece<float, W> x;
+        x.load(span_of<float>(p, c0, count), i);
+        x.get(v);
+    } else {
+        Piece<uint16_t, W> x;
+        x.load(span_of<uint16_t>(p, c0, count), i);
+        x.get(v);
+    }
+}
+
+// The part of one row that a lane's piece belongs to: elements at .. at + count of each matrix, columns
+// c0 .. of the parameters.  in: whether the piece, the span's element i on, lies inside.
+struct RowPart {
+    int64_t at;
+    uint32_t c0, count, live, i;  // live: count, or 0 for a team without a row
+    bool in;
+};
+
+// W columns of a row through the three phases of the pass.
+template <typename T, int W, bool POST, int GATE>
+struct RnBwdPiece {
+    using P = Piece<T, W>;
+    P h, dout, y, dh;
+    float dw[W];  // dweight's sum over the rows
+    float t[W];   // the gradient of the normed y
+
+    // A matrix that is not there is loaded as a span of no elements: values kept from the last row in
+    // its place would need registers of their own.
+    __device__ __forceinline__ void load_first(const RnBwdParams& p, const RowPart& q) {
+        const uint32_t live = p.dout ? q.live : 0u;
+        h.load(span_of<T>(p.h, q.at, live), q.i);
+        dout.load(span_of<T>(p.dout, q.at, live), q.i);
+    }
+    __device__ __forceinline__ void load_y(const RnBwdParams& p, const RowPart& q) {
+        if constexpr (POST || GATE != kGateNone) y.load(span_of<T>(p.y, q.at, q.live), q.i);
+    }
+    __device__ __forceinline__ void load_rest(const RnBwdParams& p, const RowPart& q) {
+        load_y(p, q);
+        dh.load(span_of<T>(p.dh, q.at, p.dh ? q.live : 0u), q.i);
+    }
+    // The sum of dout weight xh.  Outside the row the values are 0, and so has to be r, which may be
+    // infinite.
+    __device__ __forceinline__ void first(const RnBwdParams& p, const RowPart& q, float r, float& s) {
+        float w[W], v[W], g[W];
+        get_param(p.weight, p.param_f32, q.c0, q.count, q.i, w);
+        h.get(v);
+        dout.get(g);
+        const float rc = q.in ? r : 0.0f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float gx = g[j] * (v[j] * rc);
+            dw[j] += gx;
+            s = __builtin_fmaf(gx, w[j], s);
+        }
+        h.forget();
+        dout.forget();
+    }
+    // dresidual and what follows from it; the sums over the rows of the gate's and the post-norm's
+    // gradients are added by `add`.
+    template <typename Add>
+    __device__ __forceinline__ void second(const RnBwdParams& p, const RowPart& q, float r, float s, float rp, float& s2,
+                                           Add add) {
+        float w[W], v[W], g[W];
+        get_param(p.dout ? p.weight : nullptr, p.param_f32, q.c0, q.count, q.i, w);
+        h.get(v);
+        dout.get(g);
+#pragma unroll
+        for (int j = 0; j < W; ++j) g[j] = (g[j] * w[j] - v[j] * r * s) * r;  // 0 without dout, whose r is 0
+        dh.get(v);
+#pragma unroll
+        for (int j = 0; j < W; ++j) g[j] += v[j];
+        if (p.dresidual) P::store(span_of<T>(p.dresidual, q.at, q.live), q.i, g);
+#pragma unroll
+        for (int j = 0; j < W; ++j) t[j] = q.in ? g[j] * p.scale : 0.0f;
+        if constexpr (POST || GATE != kGateNone) {
+            float yh[W];
+            y.get(yh);
+            const float rc = q.in ? rp : 0.0f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) yh[j] *= rc;
+            if constexpr (POST) get_param(p.post_weight, p.param_f32, q.c0, q.count, q.i, w);
+            if constexpr (GATE != kGateNone) {
+                float k[W];
+                if constexpr (GATE == kGateElement) {
+                    P gate;
+                    gate.load(span_of<T>(p.gate, q.at, q.live), q.i);
+                    gate.get(k);
+                } else {
+                    get_param(p.gate, p.param_f32, q.c0, q.count, q.i, k);
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    v[j] = t[j] * (POST ? yh[j] * w[j] : yh[j]);
+                    t[j] *= k[j];
+                }
+                if constexpr (GATE == kGateColumn) add(1, v);
+                else if (p.dgate_rows) P::store(span_of<T>(p.dgate_rows, q.at, q.live), q.i, v);
+            }
+            if constexpr (POST) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    v[j] = t[j] * yh[j];
+                    s2 = __builtin_fmaf(v[j], w[j], s2);
+                    t[j] *= w[j];
+                }
+                add(0, v);
+                y.forget();
+            }
+        }
+    }
+    __device__ __forceinline__ void third(const RnBwdParams& p, const RowPart& q, float rp, float s2) {
+        if constexpr (POST) {
+            float yh[W];
+            y.get(yh);
+#pragma unroll
+            for (int j = 0; j < W; ++j) t[j] = (t[j] - yh[j] * rp * s2) * rp;
+        }
+        P::store(span_of<T>(p.dy, q.at, q.live), q.i, t);
+    }
+};
+
+// WPR waves per row, NP pieces of W columns per lane.
+template <typename T, int WPR, int W, int NP, int WAVES, bool POST, int GATE>
+__global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p) {
+    constexpr int TEAMS = WAVES / WPR;
+    constexpr int LANES = WPR * 64;
+    constexpr int COLS = NP * LANES * W;
+    constexpr int Q = W / 4;  // fours of columns per piece
+    // Two chunks per lane do not fit: h, dout and y are read again for the phase that needs them, from the caches.
+    constexpr bool ONCE = NP == 1;
+    constexpr int LSUMS = POST || GATE == kGateColumn ? 2 : 1;  // the join needs one
+    __shared__ float red[2][2][WAVES];
+    __shared__ float ltail[3][TEAMS][8];
+    // [which][team][COLS], a lane's four columns together: column W (i LANES + lane) + 4 q + j at
+    // ((Q i + q) LANES + lane) 4 + j, free of bank conflicts
+    __shared__ f32x4 lsum[LSUMS * TEAMS * COLS / 4];
+    const int wave = uniform(threadIdx.x >> 6), team = wave / WPR;
+    const int lane = threadIdx.x - team * LANES;
+    const uint32_t cols = p.cols, whole = cols & ~(W - 1u);
+    const float inv_cols = 1.0f / (float)p.cols;
+    f32x4* mine = lsum + team * (COLS / 4) + lane;
+    RnBwdPiece<T, W, POST, GATE> pc[NP];
+    RnBwdPiece<T, 1, POST, GATE> tail;
+    const bool tailed = (uint32_t)lane < cols - whole;
+    float tsum[2] = {0.0f, 0.0f};
+    tail.dw[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) pc[i].dw[j] = 0.0f;
+    if (LSUMS == 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < Q * NP; ++i) mine[k * (TEAMS * COLS / 4) + i * LANES] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // Sum over the row's waves; the two slots of a turn and the turns' flip keep one barrier enough.
+    auto team_sum = [&](float v, int flip, int slot) {
+        v = wave_sum(v);
+        if constexpr (WPR > 1) {
+            if ((threadIdx.x & 63) == 0) red[flip][slot][wave] = v;
+            __syncthreads();
+            v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) v += red[flip][slot][team * WPR + i];
+        }
+        return v * inv_cols;
+    };
+    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+    // every team takes part in every turn's barriers, with or without a row
+    for (int flip = 0; row - team < p.rows; row += step, flip ^= 1) {
+        const bool here = row < p.rows;
+        const int64_t at = row * cols;
+        const float r = here && p.dout ? p.rstd[row] : 0.0f;
+        const float rp = !POST ? 1.0f : here ? p.post_rstd[row] : 0.0f;
+        auto part = [&](int i) {
+            const uint32_t c = (uint32_t)(i * LANES + lane) * W;
+            return RowPart{at, 0, whole, here ? whole : 0u, c, here && c < whole};
+        };
+        const RowPart rest = {at + whole, whole, cols - whole, here ? cols - whole : 0u, (uint32_t)lane, here && tailed};
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            pc[i].load_first(p, part(i));
+            if (ONCE) pc[i].load_rest(p, part(i));
+        }
+        if (whole != cols) {
+            tail.load_first(p, rest);
+            tail.load_rest(p, rest);
+        }
+        float s = 0.0f, s2 = 0.0f;
+        if (p.dout) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                if (!ONCE) __builtin_amdgcn_sched_barrier(0);
+                pc[i].first(p, part(i), r, s);
+            }
+            if (whole != cols) tail.first(p, rest, r, s);
+            s = team_sum(s, flip, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            RowPart q = part(i);
+            if (!ONCE) {
+                __builtin_amdgcn_sched_barrier(0);  // one chunk after the other
+                asm volatile("" : "+v"(q.i));       // loads of their own, not the first phase's kept
+                pc[i].load_first(p, q);
+                pc[i].load_rest(p, q);
+            }
+            pc[i].second(p, q, r, s, rp, s2, [&](int which, const float(&v)[W]) {
+#pragma unroll
+                for (int k = 0; k < Q; ++k)
+                    mine[which * (TEAMS * COLS / 4) + (Q * i + k) * LANES] +=
+                        f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+            });
+        }
+        if (whole != cols)
+            tail.second(p, rest, r, s, rp, s2, [&](int which, const float(&v)[1]) { tsum[which] += v[0]; });
+        if constexpr (POST) s2 = team_sum(s2, flip, 1);
+        if (!p.dy) continue;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            RowPart q = part(i);
+            if (!ONCE) {
+                __builtin_amdgcn_sched_barrier(0);
+                asm volatile("" : "+v"(q.i));
+                pc[i].load_y(p, q);
+            }
+            pc[i].third(p, q, rp, s2);
+        }
+        if (whole != cols) tail.third(p, rest, rp, s2);
+    }
+    if (!p.part) return;
+    if (tailed) {
+        ltail[0][team][lane] = tail.dw[0];
+        ltail[1][team][lane] = tsum[0];
+        ltail[2][team][lane] = tsum[1];
+    }
+    // What LDS holds first, then dweight's sums through the first's place.
+    auto join = [&](int which, const f32x4* teams) {
+        float* part = p.part + ((int64_t)blockIdx.x * 3 + which) * cols;
+        __syncthreads();
+        for (uint32_t q = threadIdx.x; q < COLS / 4; q += WAVES * 64) {
+            const uint32_t c = (q / (Q * LANES) * LANES + q % LANES) * W + q / LANES % Q * 4;
+            if (c >= whole) continue;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < TEAMS; ++k) v += teams[k * (COLS / 4) + q];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[c + j] = v[j];
+        }
+        if (threadIdx.x < cols - whole) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < TEAMS; ++k) v += ltail[which][k][threadIdx.x];
+            part[whole + threadIdx.x] = v;
+        }
+    };
+    if constexpr (LSUMS == 2) {
+        if (p.sums[1]) join(1, lsum);
+        if (p.sums[2]) join(2, lsum + TEAMS * COLS / 4);
+    }
+    if (p.sums[0]) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const float(&d)[W] = pc[i].dw;
+                mine[(Q * i + k) * LANES] = f32x4{d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]};
+            }
+        join(0, lsum);
+    }
+}
+
+// The column sums from the groups' partial ones: 32 columns per workgroup, 32 threads down the
+// groups, joined in LDS in a fixed order.  blockIdx.y: which sum.
+__global__ __launch_bounds__(1024) void rn_bwd_join_kernel(const RnBwdParams p, int64_t groups) {
+    __shared__ float s[32][33];
+    const int which = blockIdx.y;
+    void* out = p.sums[which];
+    if (!out) return;
+    const int cl = threadIdx.x & 31, g0 = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + cl;
+    float v = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 8
+        for (int64_t g = g0; g < groups; g += 32) v += p.part[(g * 3 + which) * p.cols + c];
+    }
+    s[g0][cl] = v;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v += s[i][cl];
+        if (c < p.cols) {
+            if (p.grad_f32) ((float*)out)[c] = v;
+            else ((uint16_t*)out)[c] = bf16_rne(v);
+        }
+    }
+}
+
+struct RnBwdShape {
+    int wpr, np, waves, groups;  // groups: the workgroups that are at work at once
+};
+RnBwdShape rn_bwd_shape(int64_t cols) {
+    if (cols <= 512) return {1, 1, 8, 512};
+    if (cols <= 1024) return {2, 1, 8, 512};
+    if (cols <= 2048) return {4, 1, 8, 512};
+    if (cols <= 4096) return {8, 1, 8, 512};
+    if (cols <= 8192) return {16, 1, 16, 256};
+    return {8, 8, 8, 256};
+}
+template <typename T, bool POST, int GATE>
+const void* pick_rn_bwd_shape(RnBwdShape s) {
+    switch (s.wpr * 16 + s.np) {
+        case 16 + 1: return (const void*)&rn_bwd_kernel<T, 1, 8, 1, 8, POST, GATE>;
+        case 32 + 1: return (const void*)&rn_bwd_kernel<T, 2, 8, 1, 8, POST, GATE>;
+        case 64 + 1: return (const void*)&rn_bwd_kernel<T, 4, 8, 1, 8, POST, GATE>;
+        case 128 + 1: return (const void*)&rn_bwd_kernel<T, 8, 8, 1, 8, POST, GATE>;
+        case 256 + 1: return (const void*)&rn_bwd_kernel<T, 16, 8, 1, 16, POST, GATE>;
+    }
+    return (const void*)&rn_bwd_kernel<T, 8, 4, 8, 8, POST, GATE>;
+}
+template <typename T, bool POST>
+const void* pick_rn_bwd_gate(RnBwdShape s, int gate) {
+    return gate == kGateNone     ? pick_rn_bwd_shape<T, POST, kGateNone>(s)
+           : gate == kGateColumn ? pick_rn_bwd_shape<T, POST, kGateColumn>(s)
+                                 : pick_rn_bwd_shape<T, POST, kGateElement>(s);
+}
+template <typename T>
+const void* pick_rn_bwd(RnBwdShape s, bool post, int gate) {
+    return post ? pick_rn_bwd_gate<T, true>(s, gate) : pick_rn_bwd_gate<T, false>(s, gate);
+}
+
+}  // namespace
+
+hipError_t launch_rn(const RnParams& p, hipStream_t stream) {
+    const RnShape s = rn_shape(p.cols);
+    const int rpw = s.wpr == 1 ? 4 : 1, threads = s.wpr == 1 ? 256 : s.wpr * 64;
+    const void* k = p.f32 ? pick_rn<float>(s) : pick_rn<uint16_t>(s);
+    for (int64_t row0 = 0; row0 < p.rows; row0 += kMaxGrid * rpw) {
+        const int64_t rows = p.rows - row0 < kMaxGrid * rpw ? p.rows - row0 : kMaxGrid * rpw;
+        void* args[] = {(void*)&p, (void*)&row0};
+        const hipError_t err =
+            hipLaunchKernel(k, dim3((unsigned)((rows + rpw - 1) / rpw)), dim3(threads), args, 0, stream);
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+int64_t rn_bwd_groups(int64_t rows, int64_t cols) {
+    const RnBwdShape s = rn_bwd_shape(cols);
+    const int64_t teams = s.waves / s.wpr, wanted = (rows + teams - 1) / teams;
+    return wanted < 1 ? 1 : wanted < s.groups ? wanted : s.groups;
+}
+
+hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream) {
+    const RnBwdShape s = rn_bwd_shape(p.cols);
+    const int64_t groups = rn_bwd_groups(p.rows, p.cols);
+    const bool post = p.post_rstd != nullptr;
+    const void* k = p.f32 ? pick_rn_bwd<float>(s, post, p.gate_kind) : pick_rn_bwd<uint16_t>(s, post, p.gate_kind);
+    void* args[] = {(void*)&p};
+    hipError_t err = hipLaunchKernel(k, dim3((unsigned)groups), dim3(s.waves * 64), args, 0, stream);
+    if (err != hipSuccess || !p.part) return err;
+    void* jargs[] = {(void*)&p, (void*)&groups};
+    return hipLaunchKernel((const void*)&rn_bwd_join_kernel, dim3((unsigned)((p.cols + 31) / 32), 3), dim3(1024), jargs,
+                           0, stream);
+}
+
+}  // namespace loco

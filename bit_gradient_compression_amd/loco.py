@@ -29,13 +29,17 @@ LOCO_ACT_NONE = 0
 LOCO_ACT_RELU = 1
 LOCO_ACT_GELU = 2
 LOCO_ACT_SILU = 3
+LOCO_GATE_NONE = 0
+LOCO_GATE_COLUMN = 1
+LOCO_GATE_ELEMENT = 2
 
 SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequant_reduce",
            "loco_dequant_reduce_adam", "loco_topk_quantize", "loco_sparse_aggregate", "loco_status_string",
            "loco_version", "loco_layer_norm", "loco_layer_norm_backward", "loco_layer_norm_backward_workspace",
            "loco_checkpoint_write", "loco_checkpoint_read", "loco_linear", "loco_linear_workspace",
            "loco_linear_input_grad", "loco_linear_input_grad_workspace", "loco_linear_weight_grad",
-           "loco_linear_weight_grad_workspace", "loco_adamw", "loco_adamw_state_read", "loco_adamw_state_write"]
+           "loco_linear_weight_grad_workspace", "loco_adamw", "loco_adamw_state_read", "loco_adamw_state_write",
+           "loco_residual_norm", "loco_residual_norm_backward", "loco_residual_norm_backward_workspace"]
 
 
 class LocoError(RuntimeError):
@@ -143,6 +147,11 @@ def load(path: str | None = None):
             ("loco_linear_input_grad_workspace", i64, [i64, i64, i64]),
             ("loco_linear_weight_grad", i32, [ptr, ckpt, i64, i64, i64, i32, i32, ptr, ptr, i32, ptr, i64, ptr]),
             ("loco_linear_weight_grad_workspace", i64, [i64, i64, i64, i32]),
+            ("loco_residual_norm", i32, [ptr, ptr, i32, ptr, i32, ptr, ptr, i32, i64, i64, f32, f32, ptr, ptr, ptr, ptr,
+                                         ckpt, ptr]),
+            ("loco_residual_norm_backward", i32, [ptr, ptr, ptr, ptr, i32, ptr, i32, ptr, ptr, i32, ptr, ptr, i64, i64,
+                                                  f32, ptr, ptr, ptr, ptr, ptr, i32, ptr, i64, ptr]),
+            ("loco_residual_norm_backward_workspace", i64, [i64, i64]),
             ("loco_adamw", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ctypes.POINTER(AdamwOptions),
                                  ptr, ptr]),
             ("loco_adamw_state_read", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr]),
@@ -601,6 +610,97 @@ def loco_linear_weight_grad_workspace(rows: int, out_features: int, in_features:
     return load().loco_linear_weight_grad_workspace(rows, out_features, in_features, act)
 
 
+# -- the norms around a block -----------------------------------------------------------------
+
+def _params(cols, *named) -> int:
+    """The type code of the parameters given (all alike), each of cols elements."""
+    dtype = None
+    for t, what in named:
+        if t is None:
+            continue
+        _sized(t, cols, what, _FLOATS if dtype is None else (dtype,))
+        dtype = t.dtype
+    return LOCO_F32 if dtype is None else _CODES[dtype]
+
+
+def _gate(gate, like, rows, cols, dtype) -> int:
+    """LOCO_GATE_COLUMN for one dimension of cols elements, else LOCO_GATE_ELEMENT."""
+    if gate is None:
+        return LOCO_GATE_NONE
+    if gate.dim() == 1 and gate.shape[0] == cols:
+        return LOCO_GATE_COLUMN
+    _matrix(gate, like, rows, cols, "gate", (dtype,))
+    return LOCO_GATE_ELEMENT
+
+
+def loco_residual_norm(y, residual, *, out=None, rstd=None, h=None, weight=None, post_rstd=None, post_weight=None,
+                       gate=None, scale: float = 1.0, eps: float = 1e-5, checkpoint=None, block: int = 64,
+                       stream=None) -> None:
+    """What lies between two blocks, over the last dimension: u is y's RMS norm times post_weight if
+    post_rstd (float32, one per row, written) is given, else y; h = residual + scale * gate * u; out =
+    the RMS norm of h times weight, with rstd (float32, one per row) written for the backward pass, and
+    `checkpoint`, if given, with the 8-bit checkpoint of out.  y may be None: the norm of the residual
+    alone; so may residual.  gate has one dimension (a factor per column, of the weights' type) or the
+    shape of y.  Without h the stream is not stored, without out (and rstd) it is not normed.
+    post_weight goes with post_rstd."""
+    dev = _device()
+    x = residual if y is None else y
+    if x is None:
+        raise ValueError("y or residual is needed")
+    rows, cols = _rows_cols(x, "residual" if y is None else "y", _FLOATS)
+    like, dt = x.shape, (x.dtype,)
+    for t, what in ((residual, "residual"), (h, "h"), (out, "out")):
+        _matrix(t, like, rows, cols, what, dt)
+    _per_row(rstd, like, rows, "rstd")
+    _per_row(post_rstd, like, rows, "post_rstd")
+    kind = _gate(gate, like, rows, cols, x.dtype)
+    param = _params(cols, (weight, "weight"), (post_weight, "post_weight"),
+                    (gate if kind == LOCO_GATE_COLUMN else None, "gate"))
+    ck = _checkpoint(checkpoint, block, like, rows, cols, dev)
+    st = (_lib or load()).loco_residual_norm(
+        _ptr(y, dev), _ptr(residual, dev), _CODES[x.dtype], _ptr(gate, dev), kind, _ptr(post_weight, dev),
+        _ptr(weight, dev), param, rows, cols, scale, eps, _ptr(h, dev), _ptr(out, dev), _ptr(post_rstd, dev),
+        _ptr(rstd, dev), ck, _stream(stream, dev))
+    _check("loco_residual_norm", st)
+
+
+def loco_residual_norm_backward(dout, h=None, *, rstd=None, weight=None, dh=None, y=None, post_rstd=None,
+                                post_weight=None, gate=None, scale: float = 1.0, dresidual=None, dy=None, dgate=None,
+                                dweight=None, dpost_weight=None, workspace=None, stream=None) -> None:
+    """The gradients of loco_residual_norm from those of out (dout) and of h (dh), either of which may be
+    None, and what the forward pass left: h as stored (the norm's input), rstd, y, post_rstd.
+    dresidual, dy and a gate of elements' dgate have their matrix's shape and type; dweight,
+    dpost_weight and a gate of columns' dgate are summed over the rows, float32 or bfloat16,
+    alike.  Each is optional.  workspace: a tensor of residual_norm_backward_workspace(rows, cols)
+    bytes, not needed without sums over the rows."""
+    dev = _device()
+    x = dh if dout is None else dout
+    if x is None:
+        raise ValueError("dout or dh is needed")
+    rows, cols = _rows_cols(x, "dh" if dout is None else "dout", _FLOATS)
+    like, dt = x.shape, (x.dtype,)
+    for t, what in ((dh, "dh"), (h, "h"), (y, "y"), (dresidual, "dresidual"), (dy, "dy")):
+        _matrix(t, like, rows, cols, what, dt)
+    _per_row(rstd, like, rows, "rstd")
+    _per_row(post_rstd, like, rows, "post_rstd")
+    kind = _gate(gate, like, rows, cols, x.dtype)
+    columns = kind == LOCO_GATE_COLUMN
+    if dgate is not None and not columns:
+        _matrix(dgate, like, rows, cols, "dgate", dt)
+    param = _params(cols, (weight, "weight"), (post_weight, "post_weight"), (gate if columns else None, "gate"))
+    grad = _params(cols, (dweight, "dweight"), (dpost_weight, "dpost_weight"), (dgate if columns else None, "dgate"))
+    st = (_lib or load()).loco_residual_norm_backward(
+        _ptr(dout, dev), _ptr(dh, dev), _ptr(h, dev), _ptr(y, dev), _CODES[x.dtype], _ptr(gate, dev), kind,
+        _ptr(post_weight, dev), _ptr(weight, dev), param, _ptr(post_rstd, dev), _ptr(rstd, dev), rows, cols, scale,
+        _ptr(dresidual, dev), _ptr(dy, dev), _ptr(dgate, dev), _ptr(dpost_weight, dev), _ptr(dweight, dev), grad,
+        _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
+    _check("loco_residual_norm_backward", st)
+
+
+def loco_residual_norm_backward_workspace(rows: int, cols: int) -> int:
+    return load().loco_residual_norm_backward_workspace(rows, cols)
+
+
 # -- AdamW over many tensors ---------------------------------------------------------------
 
 def _keep(t):
@@ -750,3 +850,6 @@ linear_weight_grad_workspace = loco_linear_weight_grad_workspace
 adamw = loco_adamw
 adamw_state_read = loco_adamw_state_read
 adamw_state_write = loco_adamw_state_write
+residual_norm = loco_residual_norm
+residual_norm_backward = loco_residual_norm_backward
+residual_norm_backward_workspace = loco_residual_norm_backward_workspace

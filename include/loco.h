@@ -414,6 +414,73 @@ int64_t loco_linear_weight_grad_workspace(int64_t rows, int64_t out_features, in
                                           loco_act_t act);
 
 /* ---------------------------------------------------------------------------------
+ * The norms around a transformer block: the RMS norm of its output, its gate, the residual
+ * stream, and the RMS norm before the next block, in one pass.  The conventions are the layer
+ * operators'.
+ * ------------------------------------------------------------------------------ */
+
+/* What multiplies a block's output beside the scale. */
+typedef enum {
+    LOCO_GATE_NONE = 0,
+    LOCO_GATE_COLUMN = 1,  /* device [cols] of param_dtype */
+    LOCO_GATE_ELEMENT = 2  /* device [rows, cols] of dtype */
+} loco_gate_t;
+
+/*
+ * loco_residual_norm - per row:
+ *   u   = y * post_rstd * post_weight,  post_rstd = 1/sqrt(sum(y^2)/cols + eps)
+ *         (post_rstd NULL: u = y, and post_weight must be NULL)
+ *   h   = residual + scale * gate * u   (residual NULL: without it)
+ *   out = h * rstd * weight,  rstd = 1/sqrt(sum(h^2)/cols + eps)
+ *   y, residual          device [rows, cols] of `dtype`; one may be NULL.  y NULL: h = residual, the
+ *                        norm alone (gate and post-norm must be absent)
+ *   gate                 as gate_kind says; NULL with LOCO_GATE_NONE
+ *   weight, post_weight  device [cols] of `param_dtype`; NULL: ones
+ *   scale, eps           finite; eps >= 0
+ *   h                    device [rows, cols] of `dtype` (written), or NULL.  out is formed from the
+ *                        fp32 h, before its rounding
+ *   out, rstd            device [rows, cols] of `dtype`, f32[rows] (written); NULL both (then weight
+ *                        and ckpt too): h alone
+ *   post_rstd            device f32[rows] (written), for the backward pass
+ *   ckpt                 NULL, or the 8-bit checkpoint of out to write (of its fp32 values)
+ *   cols                 1 .. 16384 (LOCO_ERR_UNSUPPORTED beyond); rows 0 is a no-op
+ * A sum of squares past FLT_MAX (values around 1e19) gives rstd 0.
+ */
+int loco_residual_norm(const void* y, const void* residual, loco_dtype_t dtype, const void* gate,
+                       loco_gate_t gate_kind, const void* post_weight, const void* weight,
+                       loco_dtype_t param_dtype, int64_t rows, int64_t cols, float scale, float eps,
+                       void* h, void* out, float* post_rstd, float* rstd,
+                       const loco_checkpoint_t* ckpt, void* stream);
+
+/*
+ * loco_residual_norm_backward - from the gradients dout of out and dh of h (either may be NULL: 0),
+ * with xh = h * rstd and yh = y * post_rstd (post_rstd NULL: yh = y, post_weight ones):
+ *   dresidual = dh + rstd * (dout * weight - xh * sum(dout * weight * xh)/cols)
+ *   dweight   = sum over the rows of dout * xh
+ *   t         = scale * gate * dresidual * post_weight
+ *   dy        = post_rstd * (t - yh * sum(t * yh)/cols)     (post_rstd NULL: dy = t)
+ *   dpost_weight = sum over the rows of scale * gate * dresidual * yh
+ *   dgate     = scale * dresidual * yh * post_weight, summed over the rows for LOCO_GATE_COLUMN
+ * all formed from the fp32 dresidual, before its rounding.
+ *   dout, dh, h, y       device [rows, cols] of `dtype`; h (as stored) is needed with dout, y with
+ *                        post_rstd or a gate
+ *   dresidual, dy        device [rows, cols] of `dtype` (written), each may be NULL
+ *   dgate                device [cols] of `grad_dtype`, or [rows, cols] of `dtype` (written); may be NULL
+ *   dweight, dpost_weight  device [cols] of `grad_dtype` (written), each may be NULL
+ *   workspace            loco_residual_norm_backward_workspace(rows, cols) bytes; may be NULL without
+ *                        sums over the rows
+ * With rows 0 the sums are written as zeros.
+ */
+int loco_residual_norm_backward(const void* dout, const void* dh, const void* h, const void* y,
+                                loco_dtype_t dtype, const void* gate, loco_gate_t gate_kind,
+                                const void* post_weight, const void* weight, loco_dtype_t param_dtype,
+                                const float* post_rstd, const float* rstd, int64_t rows, int64_t cols,
+                                float scale, void* dresidual, void* dy, void* dgate, void* dpost_weight,
+                                void* dweight, loco_dtype_t grad_dtype, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+int64_t loco_residual_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/* ---------------------------------------------------------------------------------
  * AdamW over many tensors at once, with states in fp32 or in 8 bits: the step of the parameters
  * whose gradient does not arrive as payloads of loco_dequant_reduce_adam, or whose states
  * should take 2 bytes and not 8.

@@ -179,3 +179,119 @@ def test_adamw_binding_kinds_and_plans(no_device, monkeypatch):
 def test_adamw_states_binding(no_device, make, err, match):
     with pytest.raises(err, match=match):
         loco.AdamwStates([make()])
+
+
+# -- the norms around a block --------------------------------------------------------------------
+
+def ck(codes=P[12], exps=P[13], block=64):
+    return ctypes.byref(loco.Checkpoint(codes, exps, block))
+
+
+def rnorm(lib, **kw):
+    a = dict(y=P[0], res=P[1], dtype=BF16, gate=P[2], kind=1, pw=P[3], w=P[4], param=BF16, rows=4, cols=64, scale=1.0,
+             eps=1e-5, h=P[5], out=P[6], pr=P[7], r=P[8], ckpt=None)
+    a.update(kw)
+    return lib.loco_residual_norm(a["y"], a["res"], a["dtype"], a["gate"], a["kind"], a["pw"], a["w"], a["param"],
+                                  a["rows"], a["cols"], a["scale"], a["eps"], a["h"], a["out"], a["pr"], a["r"], a["ckpt"],
+                                  None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INV), (dict(cols=0), INV), (dict(cols=16385), UNSUP), (dict(rows=1 << 50), INV), (dict(dtype=I8), INV),
+    (dict(param=I8), INV), (dict(eps=-1.0), INV), (dict(eps=NAN), INV), (dict(scale=INF), INV), (dict(kind=3), INV),
+    (dict(kind=-1), INV), (dict(kind=0), INV), (dict(gate=None), INV), (dict(y=None, res=None), INV),
+    (dict(y=None), INV), (dict(y=None, gate=None, kind=0, pw=None), INV), (dict(y=None, gate=None, kind=0, pr=None), INV),
+    (dict(h=None, out=None), INV), (dict(r=None), INV), (dict(out=None), INV), (dict(out=None, w=None, r=None, ckpt=ck()), INV),
+    (dict(out=None, r=None), INV), (dict(pr=None), INV), (dict(ckpt=ck(block=0)), INV), (dict(ckpt=ck(block=16)), UNSUP),
+    (dict(ckpt=ck(codes=None)), INV), (dict(ckpt=ck(exps=P[13] + 1)), ALIGN),
+    (dict(y=P[0] + 2), ALIGN), (dict(res=P[1] + 2), ALIGN), (dict(gate=P[2] + 2), ALIGN), (dict(pw=P[3] + 2), ALIGN),
+    (dict(w=P[4] + 4), ALIGN), (dict(h=P[5] + 2), ALIGN), (dict(out=P[6] + 8), ALIGN), (dict(pr=P[7] + 4), ALIGN),
+    (dict(r=P[8] + 4), ALIGN), (dict(h=P[0]), INV), (dict(out=P[1] + 496), INV), (dict(out=P[5]), INV), (dict(r=P[7]), INV),
+    (dict(h=P[2]), INV), (dict(kind=2, h=P[2] + 496), INV), (dict(ckpt=ck(codes=P[6])), INV),
+    (dict(rows=0), OK), (dict(rows=0, y=None, res=None, gate=None, h=None, out=None), OK),
+])
+def test_residual_norm(lib, kw, want):
+    assert rnorm(lib, **kw) == want
+
+
+def rback(lib, **kw):
+    a = dict(dout=P[0], dh=P[1], h=P[2], y=P[3], dtype=BF16, gate=P[4], kind=1, pw=P[5], w=P[6], param=BF16, pr=P[7], r=P[8],
+             rows=4, cols=64, scale=1.0, dres=P[9], dy=P[10], dg=P[11], dpw=P[12], dw=P[13], grad=F32, ws=P[14], nws=1 << 20)
+    a.update(kw)
+    return lib.loco_residual_norm_backward(a["dout"], a["dh"], a["h"], a["y"], a["dtype"], a["gate"], a["kind"], a["pw"],
+                                           a["w"], a["param"], a["pr"], a["r"], a["rows"], a["cols"], a["scale"],
+                                           a["dres"], a["dy"], a["dg"], a["dpw"], a["dw"], a["grad"], a["ws"], a["nws"], None)
+
+
+NONE = dict(dres=None, dy=None, dg=None, dpw=None, dw=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INV), (dict(cols=0), INV), (dict(cols=16385), UNSUP), (dict(dtype=I8), INV), (dict(param=7), INV),
+    (dict(grad=I8), INV), (dict(scale=NAN), INV), (dict(kind=5), INV), (dict(kind=0), INV), (dict(gate=None), INV),
+    (dict(dout=None, dh=None), INV), (dict(h=None), INV), (dict(r=None), INV), (dict(dout=None), INV),
+    (dict(pr=None), INV), (dict(pr=None, pw=None), INV), (dict(y=None), INV),
+    (dict(y=None, pr=None, pw=None, dpw=None), INV), (NONE, INV), (dict(gate=None, kind=0), INV),
+    (dict(ws=None), INV), (dict(nws=0), INV), (dict(ws=P[14] + 4), ALIGN), (dict(dout=P[0] + 2), ALIGN),
+    (dict(dh=P[1] + 2), ALIGN), (dict(h=P[2] + 2), ALIGN), (dict(y=P[3] + 2), ALIGN), (dict(gate=P[4] + 2), ALIGN),
+    (dict(dres=P[9] + 2), ALIGN), (dict(dy=P[10] + 2), ALIGN), (dict(dg=P[11] + 4), ALIGN), (dict(dw=P[13] + 4), ALIGN),
+    (dict(dres=P[0]), INV), (dict(dy=P[9]), INV), (dict(dg=P[4]), INV), (dict(dw=P[12]), INV), (dict(ws=P[1]), INV),
+    (dict(dy=P[3] + 496), INV), (dict(kind=2, dg=P[10]), INV),
+    (dict(rows=0, **NONE, ws=None, nws=0), OK), (dict(rows=0, ws=None), INV),
+])
+def test_residual_norm_backward(lib, kw, want):
+    assert rback(lib, **kw) == want
+
+
+def test_residual_norm_backward_workspace(lib):
+    w = lib.loco_residual_norm_backward_workspace
+    assert w(0, 64) >= 3 * 64 * 4 and w(1000, 4096) >= w(1, 4096) > 0
+    assert w(-1, 64) == 0 and w(5, 0) == 0 and w(5, 16385) == 0 and w(1 << 50, 64) == 0
+    assert rback(lib, rows=1000, cols=4096, nws=w(1000, 4096) - 1) == INV
+
+
+def b(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def rows32(*shape):
+    return torch.zeros(*shape)
+
+
+def refused(match, fn, *a, err=ValueError, **kw):
+    with pytest.raises(err, match=match):
+        fn(*a, **kw)
+
+
+def test_residual_norm_binding(no_device):
+    f, x = loco.residual_norm, b(4, 96)
+    ok = dict(out=b(4, 96), rstd=rows32(4))
+    refused("device memory", f, x, b(4, 96), **ok)
+    refused("device memory", f, None, x, **ok)
+    refused("needed", f, None, None, **ok)
+    refused("shape", f, x, b(96, 4), **ok)
+    refused("shape", f, x, None, h=b(96, 4))
+    refused("elements", f, x, b(4, 95), **ok)
+    refused("must be", f, x, x.float(), err=TypeError, **ok)
+    refused("elements", f, x, None, weight=b(95), **ok)
+    refused("must be", f, x, None, weight=b(96), gate=rows32(96), err=TypeError, **ok)
+    refused("must be", f, x, None, gate=rows32(4, 96), err=TypeError, **ok)
+    refused("device memory", f, x, None, gate=rows32(96), weight=rows32(96), **ok)
+    refused("shape", f, x, None, gate=b(96, 4), **ok)
+    refused("elements", f, x, None, gate=b(4), **ok)
+    refused("elements", f, x, None, post_rstd=rows32(5), **ok)
+    refused("must be", f, x, None, rstd=b(4), out=b(4, 96), err=TypeError)
+
+
+def test_residual_norm_backward_binding(no_device):
+    f, d, r = loco.residual_norm_backward, b(4, 96), rows32(4)
+    refused("device memory", f, d, b(4, 96), rstd=r, dresidual=b(4, 96))
+    refused("needed", f, None, d, rstd=r)
+    refused("shape", f, d, b(96, 4), rstd=r)
+    refused("must be", f, d, d.float(), rstd=r, err=TypeError)
+    refused("shape", f, d, d, rstd=r, dy=b(96, 4))
+    refused("elements", f, d, d, rstd=r, dweight=b(95))
+    refused("must be", f, d, d, rstd=r, dweight=b(96), dpost_weight=rows32(96), err=TypeError)
+    refused("elements", f, d, d, rstd=r, gate=b(4, 96), y=d, dgate=b(96))
+    refused("must be", f, d, d, rstd=r, gate=b(4, 96), y=d, dgate=rows32(4, 96), err=TypeError)
+    refused("elements", f, d, d, rstd=r, gate=b(96), y=d, dgate=b(4, 96))
