@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libloco.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["abi.hip", "cq.hip", "dr.hip", "tk.hip", "sa.hip", "ln.hip", "ac.hip", "mm.hip", "aw.hip", "rn.hip"]
+SOURCES = ["abi.hip", "cq.hip", "dr.hip", "tk.hip", "sa.hip", "ln.hip", "ac.hip", "mm.hip",
+           "aw.hip", "rn.hip", "lp.hip"]
 # Traffic twins of the kernels, for the benchmark only: a library of their own, outside
 # the API that include/loco.h declares.
 TWINS_SOURCES = ["twins.hip"]

@@ -283,3 +283,77 @@ LOCO_API int loco_residual_norm_backward(const void* dout, const void* dh, const
                            grad_dtype == LOCO_F32};
     return hip_status(launch_rn_bwd(p, (hipStream_t)stream));
 }
+
+// ---- log probabilities of tokens -----------------------------------------------------------------
+
+namespace {
+
+// Rows of `vocab` elements, `ld` apart; their elements, from the first to the last.
+int64_t span_elems(int64_t rows, int64_t vocab, int64_t ld) { return rows > 0 ? (rows - 1) * ld + vocab : 0; }
+
+int check_logits(int64_t rows, int64_t vocab, int64_t ld, int dtype, float scale) {
+    if (rows < 0 || vocab < 1 || ld < vocab || !sizes_ok(rows, ld) || !dtype_ok(dtype)) return LOCO_ERR_INVALID;
+    if (!(scale >= 1e-6f && scale <= 1e6f)) return LOCO_ERR_INVALID;
+    return vocab > kLpMaxVocab ? LOCO_ERR_UNSUPPORTED : LOCO_OK;
+}
+
+}  // namespace
+
+LOCO_API int64_t loco_token_logprobs_workspace(int64_t rows, int64_t vocab, int top) {
+    (void)rows;
+    (void)vocab;
+    (void)top;
+    return 0;
+}
+
+LOCO_API int loco_token_logprobs(const void* logits, loco_dtype_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                 const int64_t* targets, float scale, float* logprob, float* entropy, float* stats,
+                                 int top, int32_t* top_ids, float* top_logprobs, void* workspace,
+                                 int64_t workspace_bytes, void* stream) {
+    int st = check_logits(rows, vocab, ld, dtype, scale);
+    if (st != LOCO_OK) return st;
+    if (top < 0) return LOCO_ERR_INVALID;
+    if (top > kLpMaxTop) return LOCO_ERR_UNSUPPORTED;
+    const int64_t need = loco_token_logprobs_workspace(rows, vocab, top);
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    if (rows == 0) return LOCO_OK;
+    if (!logits || (logprob && !targets) || (!logprob && !entropy && !stats && top == 0)) return LOCO_ERR_INVALID;
+    st = check_bufs({{logits, span_elems(rows, vocab, ld) * dtype_size(dtype), false, true},
+                     {targets, rows * 8, false, false},
+                     {logprob, rows * 4, true, false},
+                     {entropy, rows * 4, true, false},
+                     {stats, rows * 8, true, false},
+                     {top_ids, rows * top * 4, true, true},
+                     {top_logprobs, rows * top * 4, true, true},
+                     {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    const LpParams p = {logits, rows, ld, (int)vocab, targets, scale, logprob, entropy, stats, top_ids, top_logprobs, top,
+                        dtype == LOCO_F32};
+    return hip_status(launch_lp(p, (hipStream_t)stream));
+}
+
+LOCO_API int loco_token_logprobs_backward(const void* logits, loco_dtype_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                          const int64_t* targets, float scale, const float* stats, const float* entropy,
+                                          const float* dlogprob, const float* dentropy, void* dlogits, int64_t dld,
+                                          void* stream) {
+    int st = check_logits(rows, vocab, ld, dtype, scale);
+    if (st != LOCO_OK) return st;
+    if (dld < vocab || !sizes_ok(rows, dld)) return LOCO_ERR_INVALID;
+    if (rows == 0) return LOCO_OK;
+    if (!logits || !stats || !dlogits || (!dlogprob && !dentropy)) return LOCO_ERR_INVALID;
+    if ((dlogprob && !targets) || (dentropy && !entropy)) return LOCO_ERR_INVALID;
+    // in place: each element is read by the lane that then writes it
+    const bool in_place = dlogits == logits && dld == ld;
+    const int64_t bytes = span_elems(rows, vocab, ld) * dtype_size(dtype);
+    st = check_bufs({{logits, in_place ? 0 : bytes, false, true},
+                     {targets, rows * 8, false, false},
+                     {stats, rows * 8, false, true},
+                     {entropy, rows * 4, false, false},
+                     {dlogprob, rows * 4, false, false},
+                     {dentropy, rows * 4, false, false},
+                     {dlogits, span_elems(rows, vocab, dld) * dtype_size(dtype), true, true}});
+    if (st != LOCO_OK) return st;
+    const LpBwdParams p = {logits, dlogits, rows, ld, dld, (int)vocab, targets, stats, entropy, dlogprob, dentropy, scale,
+                           dtype == LOCO_F32};
+    return hip_status(launch_lp_bwd(p, (hipStream_t)stream));
+}

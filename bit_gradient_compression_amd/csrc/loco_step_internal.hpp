@@ -102,4 +102,40 @@ struct RnBwdParams {
 int64_t rn_bwd_groups(int64_t rows, int64_t cols);
 hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream);
 
+// ---- log probabilities of tokens ---------------------------------------------------------
+
+constexpr int kLpMaxTop = 32;
+constexpr int64_t kLpMaxVocab = (int64_t)1 << 24;
+
+struct LpParams {
+    const void* logits;
+    int64_t rows, ld;
+    int vocab;
+    const int64_t* targets;  // may be null
+    float scale;
+    float* logprob;  // may be null
+    float* entropy;  // may be null
+    float* stats;    // [rows][2]; may be null
+    int32_t* top_ids;
+    float* top_logprobs;
+    int top;
+    int f32;
+};
+hipError_t launch_lp(const LpParams& p, hipStream_t stream);
+
+struct LpBwdParams {
+    const void* logits;
+    void* dlogits;
+    int64_t rows, ld, dld;
+    int vocab;
+    const int64_t* targets;
+    const float* stats;
+    const float* entropy;
+    const float* dlogprob;  // may be null: 0
+    const float* dentropy;  // may be null: 0
+    float scale;
+    int f32;
+};
+hipError_t launch_lp_bwd(const LpBwdParams& p, hipStream_t stream);
+
 }  // namespace loco

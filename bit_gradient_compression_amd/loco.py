@@ -32,6 +32,7 @@ LOCO_ACT_SILU = 3
 LOCO_GATE_NONE = 0
 LOCO_GATE_COLUMN = 1
 LOCO_GATE_ELEMENT = 2
+LOCO_MAX_TOP = 32
 
 SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequant_reduce",
            "loco_dequant_reduce_adam", "loco_topk_quantize", "loco_sparse_aggregate", "loco_status_string",
@@ -39,7 +40,8 @@ SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequ
            "loco_checkpoint_write", "loco_checkpoint_read", "loco_linear", "loco_linear_workspace",
            "loco_linear_input_grad", "loco_linear_input_grad_workspace", "loco_linear_weight_grad",
            "loco_linear_weight_grad_workspace", "loco_adamw", "loco_adamw_state_read", "loco_adamw_state_write",
-           "loco_residual_norm", "loco_residual_norm_backward", "loco_residual_norm_backward_workspace"]
+           "loco_residual_norm", "loco_residual_norm_backward", "loco_residual_norm_backward_workspace",
+           "loco_token_logprobs", "loco_token_logprobs_workspace", "loco_token_logprobs_backward"]
 
 
 class LocoError(RuntimeError):
@@ -152,6 +154,9 @@ def load(path: str | None = None):
             ("loco_residual_norm_backward", i32, [ptr, ptr, ptr, ptr, i32, ptr, i32, ptr, ptr, i32, ptr, ptr, i64, i64,
                                                   f32, ptr, ptr, ptr, ptr, ptr, i32, ptr, i64, ptr]),
             ("loco_residual_norm_backward_workspace", i64, [i64, i64]),
+            ("loco_token_logprobs", i32, [ptr, i32, i64, i64, i64, ptr, f32, ptr, ptr, ptr, i32, ptr, ptr, ptr, i64, ptr]),
+            ("loco_token_logprobs_workspace", i64, [i64, i64, i32]),
+            ("loco_token_logprobs_backward", i32, [ptr, i32, i64, i64, i64, ptr, f32, ptr, ptr, ptr, ptr, ptr, i64, ptr]),
             ("loco_adamw", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ctypes.POINTER(AdamwOptions),
                                  ptr, ptr]),
             ("loco_adamw_state_read", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr]),
@@ -701,6 +706,100 @@ def loco_residual_norm_backward_workspace(rows: int, cols: int) -> int:
     return load().loco_residual_norm_backward_workspace(rows, cols)
 
 
+# -- log probabilities of tokens ----------------------------------------------------------------
+
+def _logits(t, what):
+    """(rows, vocab, elements from row to row) of a tensor whose last dimension is the vocabulary: the
+    rows, of one or more leading dimensions, lie one such step apart, each of them in one piece."""
+    rows, vocab = _rows_cols(t, what, _FLOATS)
+    if rows <= 1 or vocab == 0 or t.is_contiguous():
+        if vocab > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{what}: a row must be contiguous")
+        return rows, vocab, vocab
+    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    ld = lead[-1][1]
+    apart = all(a[1] == b[0] * b[1] for a, b in zip(lead, lead[1:]))
+    if not apart or ld < vocab or (vocab > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what}: rows must be contiguous and one step of at least {vocab} elements apart")
+    return rows, vocab, ld
+
+
+def _strided_ptr(t, dev):
+    d = t.get_device()
+    if d != dev:
+        if d < 0:
+            raise ValueError("tensor must be in device memory")
+        raise ValueError(f"tensor is on cuda:{d}; the call runs on the current device, cuda:{dev}")
+    return t.data_ptr()
+
+
+def _row_values(t, like, rows, what, dtypes=_F32) -> None:
+    """As _per_row, of other types too."""
+    _sized(t, rows, what, dtypes)
+    if t is not None and t.dim() > 1 and not _same_rows(tuple(t.shape), tuple(like)[:-1]):
+        raise ValueError(f"{what} has the shape {tuple(t.shape)}; the call's is {tuple(like)[:-1]}")
+
+
+_I64, _I32 = (torch.int64,), (torch.int32,)
+
+
+def loco_token_logprobs(logits, targets=None, *, logprob=None, entropy=None, stats=None, top_ids=None, top_logprobs=None,
+                        scale: float = 1.0, workspace=None, stream=None) -> None:
+    """Log probabilities of the targets (int64, one per row; below 0: not scored) under softmax(scale *
+    logits) over the last dimension, float32 or bfloat16; the entropy of each row; and its best
+    alternatives, top_ids (int32) and top_logprobs (float32), whose last dimension says how many (up to
+    LOCO_MAX_TOP), ties to the lower index.  stats (float32, two per row: the largest logit and the
+    sum of exp(scale * (logit - it))) is for the backward pass.  Each output is optional.  logits may be a
+    slice of wider rows.  workspace: a tensor of token_logprobs_workspace(rows, vocab, top) bytes."""
+    dev = _device()
+    rows, vocab, ld = _logits(logits, "logits")
+    like = logits.shape
+    _row_values(targets, like, rows, "targets", _I64)
+    _row_values(logprob, like, rows, "logprob")
+    _row_values(entropy, like, rows, "entropy")
+    _matrix(stats, like, rows, 2, "stats", _F32)
+    top = 0
+    if top_ids is not None or top_logprobs is not None:
+        if top_ids is None or top_logprobs is None or not top_ids.dim():
+            raise ValueError("top_ids and top_logprobs go together, with at least one dimension")
+        top = top_ids.shape[-1]
+        _matrix(top_ids, like, rows, top, "top_ids", _I32)
+        _matrix(top_logprobs, like, rows, top, "top_logprobs", _F32)
+    st = (_lib or load()).loco_token_logprobs(
+        _strided_ptr(logits, dev), _CODES[logits.dtype], rows, vocab, ld, _ptr(targets, dev), scale, _ptr(logprob, dev),
+        _ptr(entropy, dev), _ptr(stats, dev), top, _ptr(top_ids, dev), _ptr(top_logprobs, dev), _ptr(workspace, dev),
+        _nbytes(workspace), _stream(stream, dev))
+    _check("loco_token_logprobs", st)
+
+
+def loco_token_logprobs_workspace(rows: int, vocab: int, top: int = 0) -> int:
+    return load().loco_token_logprobs_workspace(rows, vocab, top)
+
+
+def loco_token_logprobs_backward(logits, targets, stats, *, dlogits, dlogprob=None, entropy=None, dentropy=None,
+                                 scale: float = 1.0, stream=None) -> None:
+    """dlogits = the gradient of sum(dlogprob * logprob + dentropy * entropy), with stats and entropy as
+    loco_token_logprobs wrote them (entropy is needed with dentropy only).  One of dlogprob and dentropy
+    may be None.  dlogits has the type and shape of logits, and may be logits itself."""
+    dev = _device()
+    rows, vocab, ld = _logits(logits, "logits")
+    like = logits.shape
+    drows, dvocab, dld = _logits(dlogits, "dlogits")
+    if (drows, dvocab) != (rows, vocab) or not _same_rows(tuple(dlogits.shape[:-1]), tuple(like[:-1])):
+        raise ValueError(f"dlogits has the shape {tuple(dlogits.shape)}; the call's is {tuple(like)}")
+    if dlogits.dtype != logits.dtype:
+        raise TypeError(f"dlogits must be {logits.dtype}, not {dlogits.dtype}")
+    _row_values(targets, like, rows, "targets", _I64)
+    _matrix(stats, like, rows, 2, "stats", _F32)
+    for t, what in ((dlogprob, "dlogprob"), (entropy, "entropy"), (dentropy, "dentropy")):
+        _row_values(t, like, rows, what)
+    st = (_lib or load()).loco_token_logprobs_backward(
+        _strided_ptr(logits, dev), _CODES[logits.dtype], rows, vocab, ld, _ptr(targets, dev), scale, _ptr(stats, dev),
+        _ptr(entropy, dev), _ptr(dlogprob, dev), _ptr(dentropy, dev), _strided_ptr(dlogits, dev), dld,
+        _stream(stream, dev))
+    _check("loco_token_logprobs_backward", st)
+
+
 # -- AdamW over many tensors ---------------------------------------------------------------
 
 def _keep(t):
@@ -853,3 +952,6 @@ adamw_state_write = loco_adamw_state_write
 residual_norm = loco_residual_norm
 residual_norm_backward = loco_residual_norm_backward
 residual_norm_backward_workspace = loco_residual_norm_backward_workspace
+token_logprobs = loco_token_logprobs
+token_logprobs_workspace = loco_token_logprobs_workspace
+token_logprobs_backward = loco_token_logprobs_backward

@@ -481,6 +481,59 @@ int loco_residual_norm_backward(const void* dout, const void* dh, const void* h,
 int64_t loco_residual_norm_backward_workspace(int64_t rows, int64_t cols);
 
 /* ---------------------------------------------------------------------------------
+ * Log probabilities of given tokens under the logits of a head, with the entropy of each row's
+ * distribution and its best alternatives; and the gradient that starts a backward pass.  The
+ * conventions are the layer operators', but the rows of logits and dlogits may be any number of
+ * elements >= vocab apart (ld, dld); what lies between them is neither read nor written.
+ *
+ * A row that holds a NaN or plus infinity has no distribution: its outputs are NaN (top_ids -1), and so
+ * is its gradient.  A row of minus infinities only has the log probability minus infinity, the entropy 0
+ * and the gradient 0.  Minus infinity elsewhere (a masked token) has the probability 0.
+ * ------------------------------------------------------------------------------ */
+
+/* Largest number of alternatives. */
+#define LOCO_MAX_TOP 32
+
+/*
+ * loco_token_logprobs - per row, with m = max x, S = sum exp(scale (x - m)), p = exp(scale (x - m)) / S:
+ *   logprob = scale (x[target] - m) - ln S       0 for target < 0 (a token that is not scored),
+ *                                                NaN for target >= vocab
+ *   entropy = - sum p ln p
+ *   top_ids, top_logprobs: the `top` largest logits in order, ties to the lower index, and their log
+ *             probabilities; past vocab the id -1 and minus infinity
+ *   logits   device [rows, vocab] of `dtype`, rows `ld` elements apart
+ *   targets  device i64[rows]; may be NULL without logprob
+ *   scale    1e-6 .. 1e6: an inverse temperature
+ *   logprob, entropy  device f32[rows] (written), each may be NULL
+ *   stats    device f32[rows][2] (written: m and S, for the backward pass), or NULL; ln sum exp(scale x) is
+ *            scale m + ln S
+ *   top      0 .. LOCO_MAX_TOP (LOCO_ERR_UNSUPPORTED beyond); top_ids i32, top_logprobs f32 [rows, top]
+ *   workspace  loco_token_logprobs_workspace(rows, vocab, top) bytes
+ *   vocab    1 .. 2^24 (LOCO_ERR_UNSUPPORTED beyond); rows 0 is a no-op
+ */
+int loco_token_logprobs(const void* logits, loco_dtype_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                        const int64_t* targets, float scale, float* logprob, float* entropy,
+                        float* stats, int top, int32_t* top_ids, float* top_logprobs,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+int64_t loco_token_logprobs_workspace(int64_t rows, int64_t vocab, int top);
+
+/*
+ * loco_token_logprobs_backward - the gradient of sum(dlogprob * logprob + dentropy * entropy):
+ *   dlogits[j] = scale * (dlogprob * ((j == target) - p[j]) - dentropy * p[j] * (ln p[j] + entropy))
+ * A target < 0 takes its row's dlogprob for 0, one >= vocab makes its row's gradient NaN.  Rows without
+ * anything to differentiate (no dentropy, target < 0) are written as zeros and not read.
+ *   stats, entropy      as loco_token_logprobs wrote them; entropy with dentropy only
+ *   dlogprob, dentropy  device f32[rows]; one may be NULL: 0.  targets go with dlogprob
+ *   dlogits             device [rows, vocab] of `dtype` (written), rows dld elements apart.  It may be
+ *                       logits itself (with dld = ld): in place; else, from first to last element, it may
+ *                       not overlap them
+ */
+int loco_token_logprobs_backward(const void* logits, loco_dtype_t dtype, int64_t rows, int64_t vocab,
+                                 int64_t ld, const int64_t* targets, float scale, const float* stats,
+                                 const float* entropy, const float* dlogprob, const float* dentropy,
+                                 void* dlogits, int64_t dld, void* stream);
+
+/* ---------------------------------------------------------------------------------
  * AdamW over many tensors at once, with states in fp32 or in 8 bits: the step of the parameters
  * whose gradient does not arrive as payloads of loco_dequant_reduce_adam, or whose states
  * should take 2 bytes and not 8.

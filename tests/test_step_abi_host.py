@@ -295,3 +295,83 @@ def test_residual_norm_backward_binding(no_device):
     refused("elements", f, d, d, rstd=r, gate=b(4, 96), y=d, dgate=b(96))
     refused("must be", f, d, d, rstd=r, gate=b(4, 96), y=d, dgate=rows32(4, 96), err=TypeError)
     refused("elements", f, d, d, rstd=r, gate=b(96), y=d, dgate=b(4, 96))
+
+
+# -- log probabilities of tokens ---------------------------------------------------------------------
+
+def logp(lib, **kw):
+    a = dict(x=P[0], dtype=BF16, rows=4, vocab=100, ld=100, t=P[1], scale=1.0, lp=P[2], h=P[3], st=P[4], top=3, ids=P[5],
+             tl=P[6], ws=P[7], nws=1 << 30)
+    a.update(kw)
+    return lib.loco_token_logprobs(a["x"], a["dtype"], a["rows"], a["vocab"], a["ld"], a["t"], a["scale"], a["lp"], a["h"],
+                                   a["st"], a["top"], a["ids"], a["tl"], a["ws"], a["nws"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INV), (dict(vocab=0), INV), (dict(vocab=-1), INV), (dict(ld=99), INV), (dict(ld=-100), INV),
+    (dict(rows=1 << 45), INV), (dict(vocab=(1 << 24) + 1, ld=1 << 25), UNSUP), (dict(dtype=I8), INV),
+    (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=NAN), INV), (dict(scale=INF), INV), (dict(scale=1e-7), INV),
+    (dict(scale=1e7), INV), (dict(top=-1), INV), (dict(top=33), UNSUP), (dict(x=None), INV), (dict(t=None), INV),
+    (dict(ids=None), INV), (dict(tl=None), INV), (dict(lp=None, h=None, st=None, top=0), INV),
+    (dict(x=P[0] + 2), ALIGN), (dict(t=P[1] + 8), ALIGN), (dict(lp=P[2] + 4), ALIGN), (dict(h=P[3] + 4), ALIGN),
+    (dict(st=P[4] + 8), ALIGN), (dict(ids=P[5] + 4), ALIGN), (dict(tl=P[6] + 4), ALIGN),
+    (dict(lp=P[0] + 16), INV), (dict(lp=P[0] + 784), INV), (dict(h=P[2]), INV), (dict(st=P[3]), INV), (dict(ids=P[6]), INV),
+    (dict(lp=P[1]), INV), (dict(ld=200, lp=P[0] + 1200), INV), (dict(rows=0), OK), (dict(rows=0, x=None, t=None), OK),
+])
+def test_token_logprobs(lib, kw, want):
+    assert logp(lib, **kw) == want
+
+
+def lback(lib, **kw):
+    a = dict(x=P[0], dtype=F32, rows=4, vocab=100, ld=100, t=P[1], scale=1.0, st=P[2], h=P[3], dl=P[4], dh=P[5], dx=P[6],
+             dld=100)
+    a.update(kw)
+    return lib.loco_token_logprobs_backward(a["x"], a["dtype"], a["rows"], a["vocab"], a["ld"], a["t"], a["scale"], a["st"],
+                                            a["h"], a["dl"], a["dh"], a["dx"], a["dld"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), INV), (dict(vocab=0), INV), (dict(ld=99), INV), (dict(dld=99), INV), (dict(rows=1 << 45), INV),
+    (dict(vocab=(1 << 24) + 1, ld=1 << 25, dld=1 << 25), UNSUP), (dict(dtype=I8), INV), (dict(scale=0.0), INV),
+    (dict(x=None), INV), (dict(st=None), INV), (dict(dx=None), INV), (dict(dl=None, dh=None), INV), (dict(t=None), INV),
+    (dict(h=None), INV), (dict(x=P[0] + 4), ALIGN), (dict(st=P[2] + 8), ALIGN), (dict(dl=P[4] + 4), ALIGN),
+    (dict(dx=P[6] + 4), ALIGN), (dict(dx=P[0] + 16), INV), (dict(dx=P[0], dld=104), INV), (dict(dx=P[2]), INV),
+    (dict(dx=P[4]), INV), (dict(dx=P[1]), INV), (dict(dx=P[0] + 1584), INV), (dict(rows=0), OK),
+    (dict(rows=0, x=None, dx=None), OK),
+])
+def test_token_logprobs_backward(lib, kw, want):
+    assert lback(lib, **kw) == want
+
+
+def test_token_logprobs_workspace(lib):
+    assert lib.loco_token_logprobs_workspace(0, 100, 0) == 0
+    assert lib.loco_token_logprobs_workspace(-1, 100, 0) == 0
+
+
+def test_token_logprobs_binding(no_device):
+    f, x, t = loco.token_logprobs, b(4, 96), torch.zeros(4, dtype=torch.int64)
+    r = rows32(4)
+    refused("device memory", f, x, t, logprob=r)
+    refused("elements", f, x, t[:3], logprob=r)
+    refused("must be", f, x, t.int(), logprob=r, err=TypeError)
+    refused("elements", f, x, t, logprob=rows32(5))
+    refused("must be", f, x, t, logprob=b(4), err=TypeError)
+    refused("shape", f, x, t, stats=rows32(2, 4))
+    refused("go together", f, x, top_ids=torch.zeros(4, 2, dtype=torch.int32))
+    refused("elements", f, x, top_ids=torch.zeros(4, 2, dtype=torch.int32), top_logprobs=rows32(4, 3))
+    refused("must be", f, x, top_ids=torch.zeros(4, 2, dtype=torch.int64), top_logprobs=rows32(4, 2), err=TypeError)
+    refused("must be", f, x.half(), t, logprob=r, err=TypeError)
+    refused("apart", f, b(96, 4).t(), t, logprob=r)
+    refused("apart", f, b(1, 96).expand(4, 96), t, logprob=r)
+    refused("apart", f, b(4, 2, 96)[:, 0].unsqueeze(1).expand(4, 2, 96), torch.zeros(8, dtype=torch.int64), logprob=rows32(8))
+    refused("row must be contiguous", f, b(192)[::2], t[:1], logprob=rows32(1))
+    refused("device memory", f, b(4, 100)[:, :96], t, logprob=r)
+    refused("device memory", f, b(2, 2, 100)[..., :96], t, logprob=r)
+    refused("shape", f, b(2, 3, 96), torch.zeros(3, 2, dtype=torch.int64), logprob=rows32(6))
+    g, s = loco.token_logprobs_backward, rows32(4, 2)
+    refused("device memory", g, x, t, s, dlogprob=r, dlogits=b(4, 96))
+    refused("shape", g, x, t, s, dlogprob=r, dlogits=b(96, 4))
+    refused("must be", g, x, t, s, dlogprob=r, dlogits=rows32(4, 96), err=TypeError)
+    refused("apart", g, x, t, s, dlogprob=r, dlogits=b(1, 96).expand(4, 96))
+    refused("elements", g, x, t, rows32(4, 1), dlogprob=r, dlogits=b(4, 96))
+    refused("elements", g, x, t, s, dlogprob=rows32(3), dlogits=b(4, 96))
