@@ -18,31 +18,43 @@ int check_state_block(int block) {
     return block_ok(block) ? LOCO_OK : LOCO_ERR_UNSUPPORTED;
 }
 
-// The tiles of the tensors before index i in one launch; `add` describes tensor i there.
-template <typename Add, typename Size, typename Launch>
-int launch_batches(int count, int most, Size size, Add add, Launch launch) {
-    int i = 0;
-    while (i < count) {
-        int used = 0;
-        int64_t tiles = 0;
-        for (; i < count && used < most; ++i) {
-            const int64_t n = size(i);
-            if (n == 0) continue;
-            add(used++, i, tiles);
-            tiles += (n + kAwTile - 1) / kAwTile;
+// Fills a table of the `count` segments that are not empty; describe(d, i) describes segment i.
+template <typename Size, typename Describe>
+int fill_table(int count, int64_t live, int tile, Size size, Describe describe, void* table, int64_t& tiles,
+               hipStream_t st) {
+    AwFillParams p;
+    memset(&p, 0, sizeof(p));
+    p.table = table;
+    p.n = live;
+    tiles = 0;
+    for (int i = 0; i < count; ++i) {
+        const int64_t n = size(i);
+        if (n > 0) {
+            memset(&p.seg[p.count], 0, sizeof(AwSegDev));
+            describe(p.seg[p.count], i);
+            p.seg[p.count].n = n;
+            p.tile0[p.count++] = tiles;
+            tiles += (n + tile - 1) / tile;
         }
-        if (used > 0 && launch(used, tiles) != hipSuccess) return LOCO_ERR_HIP;
+        if (p.count == kAwFill || (i == count - 1 && p.count > 0)) {
+            if (launch_aw_fill(p, st) != hipSuccess) return LOCO_ERR_HIP;
+            p.first += p.count;
+            p.count = 0;
+        }
     }
     return LOCO_OK;
 }
 
+constexpr int kAdamwPlan = 0x61647721, kStatePlan = 0x61647722;  // what a plan was made for
+
 int check_adamw_tensors(const loco_adamw_tensor_t* ts, int nt, int param_dtype, int grad_dtype, int bits, int block,
-                        double lr, const float* grad_scale) {
+                        const void* table, int64_t& live) {
     const int ps = dtype_size(param_dtype), gs = dtype_size(grad_dtype), ss = bits == 8 ? 1 : 4;
     for (int i = 0; i < nt; ++i) {
         const loco_adamw_tensor_t& t = ts[i];
-        if (t.n < 0 || t.n > kMaxElems || !isfinite((float)(1.0 - lr * t.weight_decay))) return LOCO_ERR_INVALID;
+        if (t.n < 0 || t.n > kMaxElems || !isfinite(t.weight_decay)) return LOCO_ERR_INVALID;
         if (t.n == 0) continue;
+        ++live;
         if (!t.param || !t.grad || !t.m || !t.v || (bits == 8 && (!t.m_exps || !t.v_exps))) return LOCO_ERR_INVALID;
         if (t.param_bf16 && param_dtype != LOCO_F32) return LOCO_ERR_INVALID;
     }
@@ -54,7 +66,8 @@ int check_adamw_tensors(const loco_adamw_tensor_t* ts, int nt, int param_dtype, 
         if (bits == 8) bits_of |= (uintptr_t)t.m_exps | (uintptr_t)t.v_exps;
         if (bits_of & 15u) return LOCO_ERR_ALIGN;
     }
-    if (grad_scale && !aligned16(grad_scale)) return LOCO_ERR_ALIGN;
+    if (live > 0 && !table) return LOCO_ERR_INVALID;
+    if (live > 0 && !aligned16(table)) return LOCO_ERR_ALIGN;
     std::vector<Span> spans;
     spans.reserve(7 * (size_t)nt + 1);
     for (int i = 0; i < nt; ++i) {
@@ -70,29 +83,57 @@ int check_adamw_tensors(const loco_adamw_tensor_t* ts, int nt, int param_dtype, 
         }
         if (t.param_bf16) spans.push_back({range_of(t.param_bf16, t.n * 2), true});
     }
-    if (grad_scale) spans.push_back({range_of(grad_scale, 4), false});
+    spans.push_back({range_of(table, live > 0 ? aw_table_bytes(live) : 0), true});
     return any_write_overlap(spans) ? LOCO_ERR_INVALID : LOCO_OK;
 }
 
 }  // namespace
 
-LOCO_API int loco_adamw(const loco_adamw_tensor_t* tensors, int ntensors, loco_dtype_t param_dtype,
-                        loco_dtype_t grad_dtype, int state_bits, int block, const loco_adamw_t* options,
-                        const float* grad_scale, void* stream) {
-    if (ntensors < 0 || (ntensors > 0 && !tensors) || !options) return LOCO_ERR_INVALID;
+LOCO_API int64_t loco_adamw_table_bytes(int n) { return n > 0 ? aw_table_bytes(n) : 0; }
+
+LOCO_API int loco_adamw_plan(const loco_adamw_tensor_t* tensors, int ntensors, loco_dtype_t param_dtype,
+                             loco_dtype_t grad_dtype, int state_bits, int block, void* table, int64_t table_bytes,
+                             loco_adamw_plan_t* plan, void* stream) {
+    if (ntensors < 0 || (ntensors > 0 && !tensors) || !plan) return LOCO_ERR_INVALID;
     if (!dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return LOCO_ERR_INVALID;
     if (state_bits != 8 && state_bits != 32) return LOCO_ERR_INVALID;
     if (state_bits == 8) {
         const int st = check_state_block(block);
         if (st != LOCO_OK) return st;
     }
+    if (table_bytes < loco_adamw_table_bytes(ntensors)) return LOCO_ERR_INVALID;
+    int64_t live = 0, tiles = 0;
+    try {
+        const int st = check_adamw_tensors(tensors, ntensors, param_dtype, grad_dtype, state_bits, block, table, live);
+        if (st != LOCO_OK) return st;
+    } catch (const std::bad_alloc&) {
+        return LOCO_ERR_INVALID;  // more tensors than the host has memory to check
+    }
+    const int st = fill_table(
+        ntensors, live, kAwTile, [&](int i) { return tensors[i].n; },
+        [&](AwSegDev& d, int i) {
+            const loco_adamw_tensor_t& t = tensors[i];
+            d = {t.param, t.grad, t.m, t.v, t.m_exps, t.v_exps, t.param_bf16, t.n, t.weight_decay, 0};
+        },
+        table, tiles, (hipStream_t)stream);
+    if (st != LOCO_OK) return st;
+    *plan = {kAdamwPlan, ntensors, live, tiles, table, tensors, param_dtype, grad_dtype, state_bits, block};
+    return LOCO_OK;
+}
+
+LOCO_API int loco_adamw(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale, void* stream) {
+    if (!plan || plan->kind != kAdamwPlan || !options) return LOCO_ERR_INVALID;
     const loco_adamw_t& o = *options;
     if (!isfinite(o.lr) || !isfinite(o.eps) || !((float)o.eps > 0.0f) || !isfinite((float)o.eps)) return LOCO_ERR_INVALID;
     if (!(o.beta1 >= 0.0 && o.beta1 < 1.0 && o.beta2 >= 0.0 && o.beta2 < 1.0) || o.step < 1) return LOCO_ERR_INVALID;
     const double bias1 = 1.0 - pow(o.beta1, (double)o.step), bias2 = 1.0 - pow(o.beta2, (double)o.step);
     AwParams p;
     memset(&p, 0, sizeof(p));
+    p.table = plan->table;
+    p.n = plan->live;
+    p.ntiles = plan->tiles;
     p.grad_scale = grad_scale;
+    p.lr = o.lr;
     p.beta1 = (float)o.beta1;
     p.omb1 = (float)(1.0 - o.beta1);
     p.beta2 = (float)o.beta2;
@@ -101,85 +142,87 @@ LOCO_API int loco_adamw(const loco_adamw_tensor_t* tensors, int ntensors, loco_d
     p.root = (float)(1.0 / sqrt(bias2));
     p.eps = (float)o.eps;
     if (!isfinite(p.step_size)) return LOCO_ERR_INVALID;
-    try {
-        const int st = check_adamw_tensors(tensors, ntensors, param_dtype, grad_dtype, state_bits, block, o.lr,
-                                           grad_scale);
-        if (st != LOCO_OK) return st;
-    } catch (const std::bad_alloc&) {
-        return LOCO_ERR_INVALID;  // more tensors than the host has memory to check
+    const int ps = dtype_size(plan->param_dtype), ss = plan->state_bits == 8 ? 1 : 4;
+    const Range scale = range_of(grad_scale, grad_scale ? 4 : 0);
+    for (int i = 0; i < plan->ntensors; ++i) {
+        const loco_adamw_tensor_t& t = plan->tensors[i];
+        if (!isfinite((float)(1.0 - o.lr * t.weight_decay))) return LOCO_ERR_INVALID;
+        if (!grad_scale || t.n == 0) continue;
+        const int64_t nb = plan->state_bits == 8 ? nblocks(t.n, plan->block) : 0;
+        if (overlap(scale, range_of(t.param, t.n * ps)) || overlap(scale, range_of(t.m, t.n * ss)) ||
+            overlap(scale, range_of(t.v, t.n * ss)) || overlap(scale, range_of(t.m_exps, nb)) ||
+            overlap(scale, range_of(t.v_exps, nb)) || overlap(scale, range_of(t.param_bf16, t.param_bf16 ? t.n * 2 : 0)))
+            return LOCO_ERR_INVALID;
     }
-    return launch_batches(
-        ntensors, kAwMaxSeg, [&](int i) { return tensors[i].n; },
-        [&](int at, int i, int64_t tile0) {
-            const loco_adamw_tensor_t& t = tensors[i];
-            p.seg[at] = {t.param, t.grad, t.m, t.v, t.m_exps, t.v_exps, t.param_bf16, t.n};
-            p.tile0[at] = tile0;
-            p.decay[at] = (float)(1.0 - o.lr * t.weight_decay);
-        },
-        [&](int used, int64_t tiles) {
-            p.nseg = used;
-            p.ntiles = tiles;
-            return launch_aw(p, param_dtype == LOCO_F32, grad_dtype == LOCO_F32, state_bits == 8 ? block : 0,
-                             (hipStream_t)stream);
-        });
+    if (grad_scale && !aligned16(grad_scale)) return LOCO_ERR_ALIGN;
+    if (p.ntiles == 0) return LOCO_OK;
+    return hip_status(launch_aw(p, plan->param_dtype == LOCO_F32, plan->grad_dtype == LOCO_F32,
+                                plan->state_bits == 8 ? plan->block : 0, (hipStream_t)stream));
 }
 
-namespace {
-
-int adamw_states(const loco_adamw_state_t* states, int nstates, int block, int dtype, bool write, void* stream) {
-    if (nstates < 0 || (nstates > 0 && !states) || !dtype_ok(dtype)) return LOCO_ERR_INVALID;
+LOCO_API int loco_adamw_state_plan(const loco_adamw_state_t* states, int nstates, int block, loco_dtype_t dtype,
+                                   void* table, int64_t table_bytes, loco_adamw_plan_t* plan, void* stream) {
+    if (nstates < 0 || (nstates > 0 && !states) || !dtype_ok(dtype) || !plan) return LOCO_ERR_INVALID;
     int st = check_state_block(block);
     if (st != LOCO_OK) return st;
+    if (table_bytes < loco_adamw_table_bytes(nstates)) return LOCO_ERR_INVALID;
+    int64_t live = 0, tiles = 0;
     for (int i = 0; i < nstates; ++i) {
         const loco_adamw_state_t& s = states[i];
         if (s.n < 0 || s.n > kMaxElems || (s.moment != 1 && s.moment != 2)) return LOCO_ERR_INVALID;
         if (s.n > 0 && (!s.codes || !s.exps || !s.values)) return LOCO_ERR_INVALID;
+        live += s.n > 0;
     }
+    if (live > 0 && !table) return LOCO_ERR_INVALID;
     for (int i = 0; i < nstates; ++i) {
         const loco_adamw_state_t& s = states[i];
         if (s.n > 0 && (!aligned16(s.codes) || !aligned16(s.exps) || !aligned16(s.values))) return LOCO_ERR_ALIGN;
     }
+    if (live > 0 && !aligned16(table)) return LOCO_ERR_ALIGN;
     try {
+        // each may be written, the states by one call and the values by the other
         std::vector<Span> spans;
-        spans.reserve(3 * (size_t)nstates);
+        spans.reserve(3 * (size_t)nstates + 1);
         for (int i = 0; i < nstates; ++i) {
             const loco_adamw_state_t& s = states[i];
             if (s.n == 0) continue;
-            spans.push_back({range_of(s.codes, s.n), write});
-            spans.push_back({range_of(s.exps, nblocks(s.n, block)), write});
-            spans.push_back({range_of(s.values, s.n * dtype_size(dtype)), !write});
+            spans.push_back({range_of(s.codes, s.n), true});
+            spans.push_back({range_of(s.exps, nblocks(s.n, block)), true});
+            spans.push_back({range_of(s.values, s.n * dtype_size(dtype)), true});
         }
+        spans.push_back({range_of(table, live > 0 ? aw_table_bytes(live) : 0), true});
         if (any_write_overlap(spans)) return LOCO_ERR_INVALID;
     } catch (const std::bad_alloc&) {
         return LOCO_ERR_INVALID;
     }
-    AwStateParams p;
-    memset(&p, 0, sizeof(p));
-    return launch_batches(
-        nstates, kAwMaxStates, [&](int i) { return states[i].n; },
-        [&](int at, int i, int64_t tile0) {
+    st = fill_table(
+        nstates, live, kAwStateTile, [&](int i) { return states[i].n; },
+        [&](AwSegDev& d, int i) {
             const loco_adamw_state_t& s = states[i];
-            p.st[at] = {s.codes, s.exps, s.values, s.n};
-            p.tile0[at] = tile0;
-            p.second = (at == 0 ? 0u : p.second) | ((uint64_t)(s.moment == 2) << at);
+            d.param = s.values;
+            d.m = s.codes;
+            d.mexp = s.exps;
+            d.second = s.moment == 2;
         },
-        [&](int used, int64_t tiles) {
-            p.nst = used;
-            p.ntiles = tiles;
-            return launch_aw_state(p, block, dtype == LOCO_F32, write, (hipStream_t)stream);
-        });
+        table, tiles, (hipStream_t)stream);
+    if (st != LOCO_OK) return st;
+    *plan = {kStatePlan, nstates, live, tiles, table, nullptr, dtype, dtype, 8, block};
+    return LOCO_OK;
+}
+
+namespace {
+
+int adamw_states(const loco_adamw_plan_t* plan, bool write, void* stream) {
+    if (!plan || plan->kind != kStatePlan) return LOCO_ERR_INVALID;
+    if (plan->tiles == 0) return LOCO_OK;
+    return hip_status(launch_aw_state(plan->table, plan->live, plan->tiles, plan->block, plan->param_dtype == LOCO_F32,
+                                      write, (hipStream_t)stream));
 }
 
 }  // namespace
 
-LOCO_API int loco_adamw_state_read(const loco_adamw_state_t* states, int nstates, int block, loco_dtype_t dtype,
-                                   void* stream) {
-    return adamw_states(states, nstates, block, dtype, false, stream);
-}
-LOCO_API int loco_adamw_state_write(const loco_adamw_state_t* states, int nstates, int block, loco_dtype_t dtype,
-                                    void* stream) {
-    return adamw_states(states, nstates, block, dtype, true, stream);
-}
+LOCO_API int loco_adamw_state_read(const loco_adamw_plan_t* plan, void* stream) { return adamw_states(plan, false, stream); }
+LOCO_API int loco_adamw_state_write(const loco_adamw_plan_t* plan, void* stream) { return adamw_states(plan, true, stream); }
 
 // ---- the norms around a block -----------------------------------------------------------------
 

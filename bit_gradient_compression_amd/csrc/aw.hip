@@ -132,6 +132,56 @@ __device__ __forceinline__ void store4b(uint8_t* p, int64_t i0, int valid, uint3
             if (j < valid) p[i0 + j] = (uint8_t)(w >> (8 * j));
     }
 }
+// Eight elements in two pieces of four: SPLIT, 256 apart; else consecutive ones, moved together.
+template <int K, bool SPLIT>
+__device__ __forceinline__ void load8(const void* p, const int64_t (&i0)[2], const int (&valid)[2], float (&x)[8]) {
+    if constexpr (!SPLIT && K == kBF16) {
+        if (valid[1] >= 4) {
+            const u32x4 w = __builtin_nontemporal_load((const u32x4*)((const uint16_t*)p + i0[0]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = bf16_lo(w[i]);
+                x[2 * i + 1] = bf16_hi(w[i]);
+            }
+            return;
+        }
+    }
+    load4<K>(p, i0[0], valid[0], x);
+    load4<K>(p, i0[1], valid[1], x + 4);
+}
+template <int K, bool SPLIT>
+__device__ __forceinline__ void store8(void* p, const int64_t (&i0)[2], const int (&valid)[2], const float (&x)[8]) {
+    if constexpr (!SPLIT && K == kBF16) {
+        if (valid[1] >= 4) {
+            __builtin_nontemporal_store(u32x4{bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]),
+                                              bf16x2_rne(x[6], x[7])}, (u32x4*)((uint16_t*)p + i0[0]));
+            return;
+        }
+    }
+    store4<K>(p, i0[0], valid[0], x);
+    store4<K>(p, i0[1], valid[1], x + 4);
+}
+template <bool SPLIT>
+__device__ __forceinline__ void load8b(const uint8_t* p, const int64_t (&i0)[2], const int (&valid)[2], uint32_t (&w)[2]) {
+    if (!SPLIT && valid[1] >= 4) {
+        const u32x2 v = __builtin_nontemporal_load((const u32x2*)(p + i0[0]));
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        w[0] = load4b(p, i0[0], valid[0]);
+        w[1] = load4b(p, i0[1], valid[1]);
+    }
+}
+template <bool SPLIT>
+__device__ __forceinline__ void store8b(uint8_t* p, const int64_t (&i0)[2], const int (&valid)[2], const uint32_t (&w)[2]) {
+    if (!SPLIT && valid[1] >= 4) {
+        __builtin_nontemporal_store(u32x2{w[0], w[1]}, (u32x2*)(p + i0[0]));
+    } else {
+        store4b(p, i0[0], valid[0], w[0]);
+        store4b(p, i0[1], valid[1], w[1]);
+    }
+}
+
 __device__ __forceinline__ int valid4(int64_t n, int64_t i0) {
     const int64_t left = n - i0;
     return left >= 4 ? 4 : left > 0 ? (int)left : 0;
@@ -160,99 +210,154 @@ __device__ __forceinline__ int piece(int lane, int pc) {
     return SPLIT ? pc * 256 + lane * 4 : lane * 8 + pc * 4;
 }
 
-// The last of the `n` starts that is not past `tile` (lane i holds start i).
-__device__ __forceinline__ int find_segment(const int64_t* tile0, int n, int64_t tile, int lane) {
-    const bool before = lane < n && tile0[lane < n ? lane : 0] <= tile;
-    return uniform(__builtin_popcountll(ballot(before)) - 1);
+// The tensor of a tile: the last one whose first tile is not past it.  Every dependent load of the table costs
+// a small call a microsecond, so up to 256 starts are counted at once; of more, every 64th part first.
+__device__ __forceinline__ int64_t find_segment(const int64_t* tile0, int64_t n, int64_t tile, int lane) {
+    int64_t lo = 0;
+    while (n > 256) {
+        const int64_t step = (n + 63) / 64, i = lane * step;
+        const bool before = i < n && tile0[lo + (i < n ? i : 0)] <= tile;
+        const int64_t j = uniform(__builtin_popcountll(ballot(before))) - 1;
+        lo += j * step;
+        n = n - j * step < step ? n - j * step : step;
+    }
+    int64_t first[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t i = k * 64 + lane;
+        first[k] = k * 64 < n ? tile0[lo + (i < n ? i : 0)] : 0;
+    }
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) count += __builtin_popcountll(ballot(k * 64 + lane < n && first[k] <= tile));
+    return lo + uniform(count) - 1;
+}
+__device__ __forceinline__ const AwSegDev* segments(const void* table, int64_t n) {
+    return (const AwSegDev*)((const char*)table + (n * 8 + 15) / 16 * 16);
+}
+
+__global__ __launch_bounds__(256) void aw_fill_kernel(const AwFillParams p) {
+    // descriptions move as words: a lane's share of one of them
+    constexpr int WORDS = sizeof(AwSegDev) / 4;
+    uint32_t* seg = (uint32_t*)((char*)p.table + (p.n * 8 + 15) / 16 * 16) + p.first * WORDS;
+    for (int i = threadIdx.x; i < p.count * WORDS; i += 256) seg[i] = ((const uint32_t*)p.seg)[i];
+    if ((int)threadIdx.x < p.count) ((int64_t*)p.table)[p.first + threadIdx.x] = p.tile0[threadIdx.x];
 }
 
 // ---- the step ---------------------------------------------------------------------------
 
-constexpr int kAwThreads = 256;
+// One-wave workgroups in runs of 128 on one XCD.  One LLaMA-7B layer (202 million elements), us with fp32 /
+// 8-bit states, the latter read back: 967 / 739, against 1019 / 750 in workgroups of four waves in dispatch
+// order, 992 / 763 in ones of one wave, 988 / 762 in runs of 64; two or four sub-tiles per wave are as fast here
+// and slower for small tensors (19.6 and 24.5 against 17.3 for 200 of them).
+constexpr int kAwThreads = 64;
+constexpr int kAwXcdRun = 128;
 
-// One wave per tile of 512 elements.  BLOCK: 0 for states in fp32.
-template <int PK, int GK, int BLOCK>
-__global__ __launch_bounds__(kAwThreads) void aw_kernel(const AwParams p, int64_t tbase) {
-    constexpr bool SPLIT = PK == kF32 || GK == kF32 || BLOCK == 0;
-    const int lane = threadIdx.x & 63;
-    const int64_t tile = tbase + (int64_t)blockIdx.x * (kAwThreads / 64) + uniform(threadIdx.x >> 6);
-    if (tile >= p.ntiles) return;  // whole waves
-    const int si = find_segment(p.tile0, p.nseg, tile, lane);
-    const AwSegDev sg = p.seg[si];
-    const float decay = p.decay[si];
-    const int64_t t0 = (tile - p.tile0[si]) * kAwTile;
+// A sub-tile of 512 elements of a tensor.  FULL: all of them exist.
+template <int PK, int GK, int BLOCK, bool FULL>
+struct AwSub {
+    static constexpr bool SPLIT = PK == kF32 || GK == kF32 || BLOCK == 0;
+    int64_t i0[2];
+    int valid[2];
     float th[8], g[8], m[8], v[8];
     uint32_t mw[2], vw[2], me[2], ve[2];
+
+    __device__ __forceinline__ void load(const AwSegDev& sg, int64_t t0, int lane) {
 #pragma unroll
-    for (int pc = 0; pc < 2; ++pc) {
-        const int64_t i0 = t0 + piece<SPLIT>(lane, pc);
-        const int valid = valid4(sg.n, i0);
-        load4<GK>(sg.grad, i0, valid, g + 4 * pc);
-        load4<PK>(sg.param, i0, valid, th + 4 * pc);
+        for (int pc = 0; pc < 2; ++pc) {
+            i0[pc] = t0 + piece<SPLIT>(lane, pc);
+            valid[pc] = FULL ? 4 : valid4(sg.n, i0[pc]);
+        }
+        load8<GK, SPLIT>(sg.grad, i0, valid, g);
+        load8<PK, SPLIT>(sg.param, i0, valid, th);
         if constexpr (BLOCK == 0) {
-            load4<kF32>(sg.m, i0, valid, m + 4 * pc);
-            load4<kF32>(sg.v, i0, valid, v + 4 * pc);
+            load8<kF32, SPLIT>(sg.m, i0, valid, m);
+            load8<kF32, SPLIT>(sg.v, i0, valid, v);
         } else {
-            mw[pc] = load4b((const uint8_t*)sg.m, i0, valid);
-            vw[pc] = load4b((const uint8_t*)sg.v, i0, valid);
-            me[pc] = valid ? sg.mexp[i0 / BLOCK] : 0u;
-            ve[pc] = valid ? sg.vexp[i0 / BLOCK] : 0u;
+            load8b<SPLIT>((const uint8_t*)sg.m, i0, valid, mw);
+            load8b<SPLIT>((const uint8_t*)sg.v, i0, valid, vw);
+#pragma unroll
+            for (int pc = 0; pc < 2; ++pc) {
+                me[pc] = valid[pc] ? sg.mexp[i0[pc] / BLOCK] : 0u;
+                ve[pc] = valid[pc] ? sg.vexp[i0[pc] / BLOCK] : 0u;
+            }
         }
     }
+    __device__ __forceinline__ void step(const AwSegDev& sg, const AwParams& p, float gs, float decay) {
+        if constexpr (BLOCK != 0) {
+#pragma unroll
+            for (int pc = 0; pc < 2; ++pc) {
+                m_decode4(mw[pc], me[pc], m + 4 * pc);
+                v_decode4(vw[pc], ve[pc], v + 4 * pc);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = g[j] * gs;
+            m[j] = p.beta1 * m[j] + p.omb1 * x;
+            v[j] = p.beta2 * v[j] + p.omb2 * (x * x);
+            const float u = m[j] / (__builtin_sqrtf(v[j]) * p.root + p.eps);
+            th[j] = th[j] * decay - p.step_size * u;
+        }
+        store8<PK, SPLIT>(sg.param, i0, valid, th);
+        if (PK == kF32 && sg.copy) store8<kBF16, SPLIT>(sg.copy, i0, valid, th);
+        if constexpr (BLOCK == 0) {
+            store8<kF32, SPLIT>(sg.m, i0, valid, m);
+            store8<kF32, SPLIT>(sg.v, i0, valid, v);
+        } else {
+            if constexpr (!FULL) {
+                // elements past the end, whose m and v are 0 * inf under an infinite gradient scale, do not count
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    m[j] = (j & 3) < valid[j / 4] ? m[j] : 0.0f;
+                    v[j] = (j & 3) < valid[j / 4] ? v[j] : 0.0f;
+                }
+            }
+            uint32_t mt[2], vt[2];
+            block_tops<BLOCK, SPLIT>(m, mt);
+            block_tops<BLOCK, SPLIT>(v, vt);
+#pragma unroll
+            for (int pc = 0; pc < 2; ++pc) {
+                me[pc] = m_exp(mt[pc]);
+                ve[pc] = v_exp(vt[pc]);
+                mw[pc] = m_encode4(m + 4 * pc, me[pc]);
+                vw[pc] = v_encode4(v + 4 * pc, ve[pc]);
+                if (valid[pc] && i0[pc] % BLOCK == 0) {
+                    sg.mexp[i0[pc] / BLOCK] = (uint8_t)me[pc];
+                    sg.vexp[i0[pc] / BLOCK] = (uint8_t)ve[pc];
+                }
+            }
+            store8b<SPLIT>((uint8_t*)sg.m, i0, valid, mw);
+            store8b<SPLIT>((uint8_t*)sg.v, i0, valid, vw);
+        }
+    }
+};
+
+// One wave per tile of kAwTile elements.  BLOCK: 0 for states in fp32.
+template <int PK, int GK, int BLOCK>
+__global__ __launch_bounds__(kAwThreads) void aw_kernel(const AwParams p, int64_t tbase) {
+    constexpr int U = kAwTile / 512;
+    const int lane = threadIdx.x;
+    const int64_t group = xcd_remap<kXcds, kAwXcdRun>(blockIdx.x, gridDim.x);
+    const int64_t tile = tbase + group;
+    if (tile >= p.ntiles) return;
+    const int64_t* tile0 = (const int64_t*)p.table;
+    const int64_t si = find_segment(tile0, p.n, tile, lane);
+    const AwSegDev sg = segments(p.table, p.n)[si];
+    const float decay = (float)(1.0 - p.lr * sg.weight_decay);
+    const int64_t t0 = (tile - tile0[si]) * kAwTile;
     const float gs = p.grad_scale ? *p.grad_scale : 1.0f;
-    if constexpr (BLOCK != 0) {
+    if (t0 + kAwTile <= sg.n) {
+        AwSub<PK, GK, BLOCK, true> s[U];
 #pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            m_decode4(mw[pc], me[pc], m + 4 * pc);
-            v_decode4(vw[pc], ve[pc], v + 4 * pc);
-        }
-    }
+        for (int u = 0; u < U; ++u) s[u].load(sg, t0 + u * 512, lane);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = g[j] * gs;
-        m[j] = p.beta1 * m[j] + p.omb1 * x;
-        v[j] = p.beta2 * v[j] + p.omb2 * (x * x);
-        const float u = m[j] / (__builtin_sqrtf(v[j]) * p.root + p.eps);
-        th[j] = th[j] * decay - p.step_size * u;
-    }
-    if constexpr (BLOCK != 0) {
-        // elements past the end, whose m and v are 0 * inf under an infinite gradient scale, do not count
-        uint32_t mt[2], vt[2];
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            const int valid = valid4(sg.n, t0 + piece<SPLIT>(lane, pc));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[4 * pc + j] = j < valid ? m[4 * pc + j] : 0.0f;
-                v[4 * pc + j] = j < valid ? v[4 * pc + j] : 0.0f;
-            }
-        }
-        block_tops<BLOCK, SPLIT>(m, mt);
-        block_tops<BLOCK, SPLIT>(v, vt);
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            me[pc] = m_exp(mt[pc]);
-            ve[pc] = v_exp(vt[pc]);
-            mw[pc] = m_encode4(m + 4 * pc, me[pc]);
-            vw[pc] = v_encode4(v + 4 * pc, ve[pc]);
-        }
-    }
-#pragma unroll
-    for (int pc = 0; pc < 2; ++pc) {
-        const int64_t i0 = t0 + piece<SPLIT>(lane, pc);
-        const int valid = valid4(sg.n, i0);
-        store4<PK>(sg.param, i0, valid, th + 4 * pc);
-        if (PK == kF32 && sg.copy) store4<kBF16>(sg.copy, i0, valid, th + 4 * pc);
-        if constexpr (BLOCK == 0) {
-            store4<kF32>(sg.m, i0, valid, m + 4 * pc);
-            store4<kF32>(sg.v, i0, valid, v + 4 * pc);
-        } else {
-            store4b((uint8_t*)sg.m, i0, valid, mw[pc]);
-            store4b((uint8_t*)sg.v, i0, valid, vw[pc]);
-            if (valid && i0 % BLOCK == 0) {
-                sg.mexp[i0 / BLOCK] = (uint8_t)me[pc];
-                sg.vexp[i0 / BLOCK] = (uint8_t)ve[pc];
-            }
+        for (int u = 0; u < U; ++u) s[u].step(sg, p, gs, decay);
+    } else {
+        for (int64_t t = t0; t < sg.n; t += 512) {
+            AwSub<PK, GK, BLOCK, false> s;
+            s.load(sg, t, lane);
+            s.step(sg, p, gs, decay);
         }
     }
 }
@@ -270,48 +375,57 @@ const void* pick_aw(int block) {
 }
 
 // ---- 8-bit states to and from values ------------------------------------------------------
+//
+// 2 x 202 million elements, us: read into bf16 / fp32 201 / 383 (6.0 / 5.3 TB/s), written from them 211 /
+// 315; with 1024 elements per wave 243 and 512 324 into bf16, in runs of workgroups per XCD the same.
 
 template <int K, int BLOCK, bool WRITE>
-__global__ __launch_bounds__(kAwThreads) void aw_state_kernel(const AwStateParams p, int64_t tbase) {
-    const int lane = threadIdx.x & 63;
-    const int64_t tile = tbase + (int64_t)blockIdx.x * (kAwThreads / 64) + uniform(threadIdx.x >> 6);
-    if (tile >= p.ntiles) return;
-    const int si = find_segment(p.tile0, p.nst, tile, lane);
-    const AwStateDev st = p.st[si];
-    const bool second = (p.second >> si) & 1u;
+__global__ __launch_bounds__(kAwThreads) void aw_state_kernel(const void* table, int64_t n, int64_t ntiles, int64_t tbase) {
+    const int lane = threadIdx.x;
+    const int64_t tile = tbase + blockIdx.x;
+    if (tile >= ntiles) return;
+    const int64_t* tile0 = (const int64_t*)table;
+    const int64_t si = find_segment(tile0, n, tile, lane);
+    const AwSegDev st = segments(table, n)[si];
+    uint8_t* codes = (uint8_t*)st.m;
+    const bool second = st.second != 0;
     constexpr bool SPLIT = K == kF32;
-    const int64_t t0 = (tile - p.tile0[si]) * kAwTile;
-    float x[8];
-    if constexpr (WRITE) {
+    constexpr int U = kAwStateTile / 512;
+    const int64_t t0 = (tile - tile0[si]) * kAwStateTile;
+    int64_t i0[U][2];
+    int valid[U][2];
+    float x[U][8];
+    uint32_t w[U][2], e[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int pc = 0; pc < 2; ++pc) {
-            const int64_t i0 = t0 + piece<SPLIT>(lane, pc);
-            load4<K>(st.values, i0, valid4(st.n, i0), x + 4 * pc);
+            i0[u][pc] = t0 + u * 512 + piece<SPLIT>(lane, pc);
+            valid[u][pc] = valid4(st.n, i0[u][pc]);
+            if (!WRITE) e[u][pc] = valid[u][pc] ? st.mexp[i0[u][pc] / BLOCK] : 0u;
         }
-        uint32_t top[2];
-        block_tops<BLOCK, SPLIT>(x, top);
+        if constexpr (WRITE) load8<K, SPLIT>(st.param, i0[u], valid[u], x[u]);
+        else load8b<SPLIT>(codes, i0[u], valid[u], w[u]);
+    }
 #pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            const int64_t i0 = t0 + piece<SPLIT>(lane, pc);
-            const int valid = valid4(st.n, i0);
-            const uint32_t e = second ? v_exp(top[pc]) : m_exp(top[pc]);
-            store4b(st.codes, i0, valid, second ? v_encode4(x + 4 * pc, e) : m_encode4(x + 4 * pc, e));
-            if (valid && i0 % BLOCK == 0) st.exps[i0 / BLOCK] = (uint8_t)e;
-        }
-    } else {
+    for (int u = 0; u < U; ++u) {
+        if constexpr (WRITE) {
+            uint32_t top[2];
+            block_tops<BLOCK, SPLIT>(x[u], top);
 #pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            const int64_t i0 = t0 + piece<SPLIT>(lane, pc);
-            const int valid = valid4(st.n, i0);
-            const uint32_t w = load4b(st.codes, i0, valid);
-            const uint32_t e = valid ? st.exps[i0 / BLOCK] : 0u;
-            if (second) v_decode4(w, e, x + 4 * pc);
-            else m_decode4(w, e, x + 4 * pc);
-        }
+            for (int pc = 0; pc < 2; ++pc) {
+                const uint32_t ex = second ? v_exp(top[pc]) : m_exp(top[pc]);
+                w[u][pc] = second ? v_encode4(x[u] + 4 * pc, ex) : m_encode4(x[u] + 4 * pc, ex);
+                if (valid[u][pc] && i0[u][pc] % BLOCK == 0) st.mexp[i0[u][pc] / BLOCK] = (uint8_t)ex;
+            }
+            store8b<SPLIT>(codes, i0[u], valid[u], w[u]);
+        } else {
 #pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            const int64_t i0 = t0 + piece<SPLIT>(lane, pc);
-            store4<K>(st.values, i0, valid4(st.n, i0), x + 4 * pc);
+            for (int pc = 0; pc < 2; ++pc) {
+                if (second) v_decode4(w[u][pc], e[u][pc], x[u] + 4 * pc);
+                else m_decode4(w[u][pc], e[u][pc], x[u] + 4 * pc);
+            }
+            store8<K, SPLIT>(st.param, i0[u], valid[u], x[u]);
         }
     }
 }
@@ -326,16 +440,13 @@ const void* pick_state(int block) {
     return nullptr;
 }
 
-// One wave per tile; launches of at most kMaxGrid workgroups.
-template <typename P>
-hipError_t launch_tiles(const void* k, const P& p, hipStream_t stream) {
+// One wave per tile; launches of at most kMaxGrid workgroups.  args[at] takes the first tile.
+hipError_t launch_tiles(const void* k, void** args, int at, int64_t ntiles, hipStream_t stream) {
     if (!k) return hipErrorInvalidValue;
-    constexpr int64_t waves = kAwThreads / 64;
-    for (int64_t tbase = 0; tbase < p.ntiles; tbase += kMaxGrid * waves) {
-        const int64_t tiles = p.ntiles - tbase < kMaxGrid * waves ? p.ntiles - tbase : kMaxGrid * waves;
-        void* args[] = {(void*)&p, (void*)&tbase};
-        const hipError_t err =
-            hipLaunchKernel(k, dim3((unsigned)((tiles + waves - 1) / waves)), dim3(kAwThreads), args, 0, stream);
+    for (int64_t tbase = 0; tbase < ntiles; tbase += kMaxGrid) {
+        const int64_t tiles = ntiles - tbase < kMaxGrid ? ntiles - tbase : kMaxGrid;
+        args[at] = (void*)&tbase;
+        const hipError_t err = hipLaunchKernel(k, dim3((unsigned)tiles), dim3(kAwThreads), args, 0, stream);
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
@@ -343,16 +454,24 @@ hipError_t launch_tiles(const void* k, const P& p, hipStream_t stream) {
 
 }  // namespace
 
+hipError_t launch_aw_fill(const AwFillParams& p, hipStream_t stream) {
+    void* args[] = {(void*)&p};
+    return hipLaunchKernel((const void*)&aw_fill_kernel, dim3(1), dim3(256), args, 0, stream);
+}
+
 hipError_t launch_aw(const AwParams& p, bool param_f32, bool grad_f32, int block, hipStream_t stream) {
     const void* k = param_f32 ? (grad_f32 ? pick_aw<kF32, kF32>(block) : pick_aw<kF32, kBF16>(block))
                               : (grad_f32 ? pick_aw<kBF16, kF32>(block) : pick_aw<kBF16, kBF16>(block));
-    return launch_tiles(k, p, stream);
+    void* args[] = {(void*)&p, nullptr};
+    return launch_tiles(k, args, 1, p.ntiles, stream);
 }
 
-hipError_t launch_aw_state(const AwStateParams& p, int block, bool f32, bool write, hipStream_t stream) {
+hipError_t launch_aw_state(const void* table, int64_t n, int64_t ntiles, int block, bool f32, bool write,
+                           hipStream_t stream) {
     const void* k = f32 ? (write ? pick_state<kF32, true>(block) : pick_state<kF32, false>(block))
                         : (write ? pick_state<kBF16, true>(block) : pick_state<kBF16, false>(block));
-    return launch_tiles(k, p, stream);
+    void* args[] = {(void*)&table, (void*)&n, (void*)&ntiles, nullptr};
+    return launch_tiles(k, args, 3, ntiles, stream);
 }
 
 }  // namespace loco

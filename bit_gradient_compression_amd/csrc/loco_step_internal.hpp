@@ -9,12 +9,13 @@ namespace loco {
 
 // ---- AdamW over many tensors ---------------------------------------------------------
 
-// Tensors per launch: their descriptions are kernel arguments, of which a launch takes 4 KB.
-constexpr int kAwMaxSeg = 48;
-constexpr int kAwTile = 512;  // elements per wave
+constexpr int kAwTile = 512;        // elements per wave of a step
+constexpr int kAwStateTile = 2048;  // elements per wave that reads or writes states, which moves 3 to 5 bytes of each
 
+// One tensor (or one 8-bit state with its values) as its table in device memory describes it.  A table of
+// n is n of AwSegDev after the n first tiles, each in the call's tile space.
 struct AwSegDev {
-    void* param;
+    void* param;  // or the values of a state
     const void* grad;
     void* m;  // fp32, or 8-bit codes with mexp
     void* v;
@@ -22,15 +23,27 @@ struct AwSegDev {
     uint8_t* vexp;
     uint16_t* copy;  // may be null
     int64_t n;
+    double weight_decay;
+    int64_t second;  // of a state: the second moment's
 };
+inline int64_t aw_table_bytes(int64_t n) { return ((n * 8 + 15) / 16 * 16) + n * (int64_t)sizeof(AwSegDev); }
+
+// Kernel arguments that carry descriptions into a table: a launch takes 4 KB of them.
+constexpr int kAwFill = 40;
+struct AwFillParams {
+    AwSegDev seg[kAwFill];
+    int64_t tile0[kAwFill];
+    void* table;
+    int64_t n, first;
+    int count;
+};
+hipError_t launch_aw_fill(const AwFillParams& p, hipStream_t stream);
 
 struct AwParams {
-    AwSegDev seg[kAwMaxSeg];
-    int64_t tile0[kAwMaxSeg];  // first tile of each tensor in the launch's tile space
-    float decay[kAwMaxSeg];    // 1 - lr * weight decay
-    int nseg;
-    int64_t ntiles;
+    const void* table;
+    int64_t n, ntiles;
     const float* grad_scale;  // may be null: 1
+    double lr;
     float beta1, omb1, beta2, omb2;
     float step_size;  // lr / (1 - beta1^step)
     float root;       // 1 / sqrt(1 - beta2^step)
@@ -38,22 +51,8 @@ struct AwParams {
 };
 // block: 0 for states in fp32, else the elements of one block of 8-bit states.
 hipError_t launch_aw(const AwParams& p, bool param_f32, bool grad_f32, int block, hipStream_t stream);
-
-struct AwStateDev {
-    uint8_t* codes;
-    uint8_t* exps;
-    void* values;
-    int64_t n;
-};
-constexpr int kAwMaxStates = 64;
-struct AwStateParams {
-    AwStateDev st[kAwMaxStates];
-    int64_t tile0[kAwMaxStates];
-    uint64_t second;  // bit i: state i is a second moment
-    int nst;
-    int64_t ntiles;
-};
-hipError_t launch_aw_state(const AwStateParams& p, int block, bool f32, bool write, hipStream_t stream);
+hipError_t launch_aw_state(const void* table, int64_t n, int64_t ntiles, int block, bool f32, bool write,
+                           hipStream_t stream);
 
 // ---- the norms around a block ----------------------------------------------------------
 

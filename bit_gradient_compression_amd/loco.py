@@ -39,7 +39,8 @@ SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequ
            "loco_version", "loco_layer_norm", "loco_layer_norm_backward", "loco_layer_norm_backward_workspace",
            "loco_checkpoint_write", "loco_checkpoint_read", "loco_linear", "loco_linear_workspace",
            "loco_linear_input_grad", "loco_linear_input_grad_workspace", "loco_linear_weight_grad",
-           "loco_linear_weight_grad_workspace", "loco_adamw", "loco_adamw_state_read", "loco_adamw_state_write",
+           "loco_linear_weight_grad_workspace", "loco_adamw_table_bytes", "loco_adamw_plan",
+           "loco_adamw", "loco_adamw_state_plan", "loco_adamw_state_read", "loco_adamw_state_write",
            "loco_residual_norm", "loco_residual_norm_backward", "loco_residual_norm_backward_workspace",
            "loco_token_logprobs", "loco_token_logprobs_workspace", "loco_token_logprobs_backward"]
 
@@ -92,6 +93,12 @@ class AdamwOptions(ctypes.Structure):
 class AdamwState(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p), ("values", ctypes.c_void_p),
                 ("n", ctypes.c_int64), ("moment", ctypes.c_int)]
+
+
+class AdamwPlan(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("ntensors", ctypes.c_int), ("live", ctypes.c_int64), ("tiles", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("tensors", ctypes.POINTER(AdamwTensor)), ("param_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int), ("block", ctypes.c_int)]
 
 
 _lib = None
@@ -157,10 +164,14 @@ def load(path: str | None = None):
             ("loco_token_logprobs", i32, [ptr, i32, i64, i64, i64, ptr, f32, ptr, ptr, ptr, i32, ptr, ptr, ptr, i64, ptr]),
             ("loco_token_logprobs_workspace", i64, [i64, i64, i32]),
             ("loco_token_logprobs_backward", i32, [ptr, i32, i64, i64, i64, ptr, f32, ptr, ptr, ptr, ptr, ptr, i64, ptr]),
-            ("loco_adamw", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ctypes.POINTER(AdamwOptions),
-                                 ptr, ptr]),
-            ("loco_adamw_state_read", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr]),
-            ("loco_adamw_state_write", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr])):
+            ("loco_adamw_table_bytes", i64, [i32]),
+            ("loco_adamw_plan", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ptr, i64,
+                                      ctypes.POINTER(AdamwPlan), ptr]),
+            ("loco_adamw", i32, [ctypes.POINTER(AdamwPlan), ctypes.POINTER(AdamwOptions), ptr, ptr]),
+            ("loco_adamw_state_plan", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr, i64,
+                                            ctypes.POINTER(AdamwPlan), ptr]),
+            ("loco_adamw_state_read", i32, [ctypes.POINTER(AdamwPlan), ptr]),
+            ("loco_adamw_state_write", i32, [ctypes.POINTER(AdamwPlan), ptr])):
         getattr(lib, fn).argtypes = args
         getattr(lib, fn).restype = res
     lib.loco_status_string.argtypes = [ctypes.c_int]
@@ -807,7 +818,7 @@ def _keep(t):
     return None if t is None else t.detach()
 
 
-def _state(state, n, nb, what, dev):
+def _state(state, n, nb, what):
     """(codes or values, exps or None), checked, and the bits of the state."""
     if isinstance(state, torch.Tensor):
         _sized(state, n, what, _F32)
@@ -818,6 +829,20 @@ def _state(state, n, nb, what, dev):
     return codes, exps, 8
 
 
+def _table(n, dev):
+    """Device memory for the table of n tensors."""
+    nbytes = load().loco_adamw_table_bytes(n)
+    return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}") if nbytes else None
+
+
+def _held_for(table, stream, dev):
+    """The stream to call on; the table's memory is not used again before that stream is past it."""
+    if stream is not None and table is not None:
+        table.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                            torch.cuda.ExternalStream(int(stream), device=dev))
+    return _stream(stream, dev)
+
+
 class AdamwTensors:
     """The tensors of loco_adamw, checked and described once; a training loop keeps it from step to
     step.  tensors: an iterable of (param, grad, m, v[, param_bf16[, weight_decay]]): param
@@ -825,22 +850,25 @@ class AdamwTensors:
     float8_e4m3fn, exps uint8), v: (codes uint8, exps uint8), one exps byte per block); every
     param, every grad and every state of one kind.  param_bf16 (or None) receives the bfloat16 copy
     of a float32 param.  weight_decay is that of the tensors that do not give one.  The memory of
-    the tensors is kept alive and must not be resized; later calls use it as it is now,
-    on the device that is current now."""
+    the tensors is kept alive and must not be resized; later calls use it as it is now, on the
+    device that is current now.  The description goes to the device on `stream` (the current one if
+    None): a call on another stream has to wait for that."""
 
-    def __init__(self, tensors, *, block: int = 256, weight_decay: float = 0.0):
+    def __init__(self, tensors, *, block: int = 256, weight_decay: float = 0.0, stream=None):
         self.device, self.block = _device(), block
         dev, rows, keep = self.device, [], []
         self.param_dtype = self.grad_dtype = self.bits = None
         for i, t in enumerate(tensors):
-            param, grad, m, v, copy, decay = (*t, None, None)[:6] if 4 <= len(t) <= 6 else _bad_tuple(i)
+            if not 4 <= len(t) <= 6:
+                raise ValueError(f"tensor {i}: expected (param, grad, m, v[, param_bf16[, weight_decay]])")
+            param, grad, m, v, copy, decay = (*t, None, None)[:6]
             if param.dtype not in _CODES or grad.dtype not in _CODES:
                 raise TypeError(f"tensor {i}: param and grad must be float32 or bfloat16")
             n = param.numel()
             nb = num_blocks(n, block) if block > 0 else 0
             _sized(grad, n, f"tensor {i}: grad", _FLOATS)
-            m, me, bits = _state(m, n, nb, "m", dev)
-            v, ve, vbits = _state(v, n, nb, "v", dev)
+            m, me, bits = _state(m, n, nb, "m")
+            v, ve, vbits = _state(v, n, nb, "v")
             kind = (param.dtype, grad.dtype, bits)
             if vbits != bits or (i and kind != (self.param_dtype, self.grad_dtype, self.bits)):
                 raise TypeError(f"tensor {i}: all params, grads and states must be of one kind")
@@ -851,12 +879,14 @@ class AdamwTensors:
             parts = (param, grad, m, v, me, ve, copy)
             rows.append((*(_ptr(x, dev) for x in parts), n, weight_decay if decay is None else decay))
             keep.append(tuple(_keep(x) for x in parts))
-        self._keep, self.count = keep, len(rows)
-        self.array = (AdamwTensor * max(1, len(rows)))(*(AdamwTensor(*r) for r in rows))
-
-
-def _bad_tuple(i):
-    raise ValueError(f"tensor {i}: expected (param, grad, m, v[, param_bf16[, weight_decay]])")
+        count = len(rows)
+        array = (AdamwTensor * max(1, count))(*(AdamwTensor(*r) for r in rows))
+        table = _table(count, dev)
+        self._keep, self._table, self.plan = (keep, array), table, AdamwPlan()
+        st = load().loco_adamw_plan(array, count, _CODES.get(self.param_dtype, LOCO_F32),
+                                    _CODES.get(self.grad_dtype, LOCO_F32), self.bits or 32, block, _ptr(table, dev),
+                                    _nbytes(table), ctypes.byref(self.plan), _held_for(table, stream, dev))
+        _check("loco_adamw_plan", st)
 
 
 def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -867,7 +897,8 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
     one element, or None.  lr, step and the others are read during the call: a captured graph
     repeats them."""
     if not isinstance(tensors, AdamwTensors):
-        tensors = AdamwTensors(tensors, block=256 if block is None else block, weight_decay=weight_decay or 0.0)
+        tensors = AdamwTensors(tensors, block=256 if block is None else block, weight_decay=weight_decay or 0.0,
+                               stream=stream)
     elif block is not None or weight_decay is not None:
         raise ValueError("an AdamwTensors has its own block and weight_decay")
     dev = _device()
@@ -875,19 +906,17 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
         raise ValueError(f"the tensors are on cuda:{tensors.device}; the call runs on the current device, cuda:{dev}")
     _sized(grad_scale, 1, "grad_scale", _F32)
     opt = AdamwOptions(lr, beta1, beta2, eps, step)
-    st = (_lib or load()).loco_adamw(
-        tensors.array, tensors.count, _CODES.get(tensors.param_dtype, LOCO_F32),
-        _CODES.get(tensors.grad_dtype, LOCO_F32), tensors.bits or 32, tensors.block, ctypes.byref(opt),
-        _ptr(grad_scale, dev), _stream(stream, dev))
+    st = (_lib or load()).loco_adamw(ctypes.byref(tensors.plan), ctypes.byref(opt), _ptr(grad_scale, dev),
+                                     _held_for(tensors._table, stream, dev))
     _check("loco_adamw", st)
 
 
 class AdamwStates:
     """8-bit states and the tensors of their values, checked and described once.  states: an
     iterable of ((codes, exps), values), values float32 or bfloat16, all alike; codes in
-    float8_e4m3fn are a first moment, in uint8 a second one.  Memory as in AdamwTensors."""
+    float8_e4m3fn are a first moment, in uint8 a second one.  Memory and stream as in AdamwTensors."""
 
-    def __init__(self, states, *, block: int = 256):
+    def __init__(self, states, *, block: int = 256, stream=None):
         self.device, self.block, self.dtype = _device(), block, None
         dev, rows, keep = self.device, [], []
         for i, ((codes, exps), values) in enumerate(states):
@@ -900,21 +929,24 @@ class AdamwStates:
             rows.append((_ptr(codes, dev), _ptr(exps, dev), _ptr(values, dev), n,
                          1 if codes.dtype == torch.float8_e4m3fn else 2))
             keep.append((_keep(codes), _keep(exps), _keep(values)))
-        self._keep, self.count = keep, len(rows)
-        self.array = (AdamwState * max(1, len(rows)))(*(AdamwState(*r) for r in rows))
+        count = len(rows)
+        array = (AdamwState * max(1, count))(*(AdamwState(*r) for r in rows))
+        table = _table(count, dev)
+        self._keep, self._table, self.plan = keep, table, AdamwPlan()
+        st = load().loco_adamw_state_plan(array, count, block, _CODES.get(self.dtype, LOCO_F32), _ptr(table, dev),
+                                          _nbytes(table), ctypes.byref(self.plan), _held_for(table, stream, dev))
+        _check("loco_adamw_state_plan", st)
 
 
 def _adamw_states(name, states, block, stream):
     if not isinstance(states, AdamwStates):
-        states = AdamwStates(states, block=256 if block is None else block)
+        states = AdamwStates(states, block=256 if block is None else block, stream=stream)
     elif block is not None:
         raise ValueError("an AdamwStates has its own block")
     dev = _device()
     if dev != states.device:
         raise ValueError(f"the states are on cuda:{states.device}; the call runs on the current device, cuda:{dev}")
-    st = getattr(_lib or load(), name)(states.array, states.count, states.block, _CODES.get(states.dtype, LOCO_F32),
-                                       _stream(stream, dev))
-    _check(name, st)
+    _check(name, getattr(_lib or load(), name)(ctypes.byref(states.plan), _held_for(states._table, stream, dev)))
 
 
 def loco_adamw_state_read(states, *, block: int | None = None, stream=None) -> None:

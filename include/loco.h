@@ -556,7 +556,7 @@ int loco_token_logprobs_backward(const void* logits, loco_dtype_t dtype, int64_t
  * the rounding: take beta2 0.95 or so with 8 bits.
  * ------------------------------------------------------------------------------ */
 
-/* One tensor (host struct, read during the call). */
+/* One tensor (host struct, read while planning and at each step). */
 typedef struct {
     void* param;          /* device, n elements of param_dtype, updated in place */
     const void* grad;     /* device, n elements of grad_dtype */
@@ -578,41 +578,67 @@ typedef struct {
 } loco_adamw_t;
 
 /*
- * loco_adamw - for every element, in IEEE fp32 operations in this order:
+ * A plan describes the tensors of many calls once: their addresses lie in a table in device memory, so
+ * that a step of any number of tensors is one launch that reads nothing but its arguments from the
+ * host.  The caller keeps this struct, the table and the host array of tensors as they are, and the tensors
+ * where they are, for as long as calls use the plan; its fields are the library's.
+ */
+typedef struct {
+    int kind, ntensors;
+    int64_t live, tiles;
+    const void* table;
+    const loco_adamw_tensor_t* tensors;
+    int param_dtype, grad_dtype, state_bits, block;
+} loco_adamw_plan_t;
+
+/* Bytes of the table of n tensors, or of n states. */
+int64_t loco_adamw_table_bytes(int n);
+
+/*
+ * loco_adamw_plan - checks ntensors (>= 0) tensors, fills their table on `stream` (calls on other
+ * streams have to wait for it) and *plan.
+ *   state_bits  32 or 8;  block  64, 128, 256 or 512 (ignored with 32)
+ *   table       device memory of table_bytes >= loco_adamw_table_bytes(ntensors)
+ * No buffer that a step writes may overlap another of its buffers, or the table.
+ */
+int loco_adamw_plan(const loco_adamw_tensor_t* tensors, int ntensors, loco_dtype_t param_dtype,
+                    loco_dtype_t grad_dtype, int state_bits, int block, void* table,
+                    int64_t table_bytes, loco_adamw_plan_t* plan, void* stream);
+
+/*
+ * loco_adamw - one step of a plan's tensors: for every element, in IEEE fp32 operations in this order:
  *   g     = grad * grad_scale[0]                      (grad_scale NULL: g = grad)
  *   m     = beta1 * m + (1 - beta1) * g
  *   v     = beta2 * v + (1 - beta2) * (g * g)
  *   param = param * (1 - lr * weight_decay)
  *           - lr / (1 - beta1^t) * (m / (sqrt(v) * (1 / sqrt(1 - beta2^t)) + eps))
- * with each host-side factor rounded to fp32 once.  With 8-bit states the parameter's update takes
- * m and v before they are rounded into their codes.
- *   tensors     host array of ntensors (>= 0); 48 of them take one launch
- *   state_bits  32 or 8;  block  64, 128, 256 or 512 (ignored with 32)
- *   grad_scale  device f32[1] (read), such as a clipping factor, or NULL
- * No buffer that the call writes may overlap another of its buffers.
+ * with each factor of the hyper-parameters formed in 64 bits and rounded to fp32 once.  With 8-bit states
+ * the parameter's update takes m and v before they are rounded into their codes.
+ *   grad_scale  device f32[1] (read), such as a clipping factor, or NULL; it must not lie in a buffer
+ *               that the step writes
  */
-int loco_adamw(const loco_adamw_tensor_t* tensors, int ntensors, loco_dtype_t param_dtype,
-               loco_dtype_t grad_dtype, int state_bits, int block, const loco_adamw_t* options,
-               const float* grad_scale, void* stream);
+int loco_adamw(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale,
+               void* stream);
 
-/* One 8-bit state and its values (host struct, read during the call). */
+/* One 8-bit state and its values (host struct, read while planning). */
 typedef struct {
     uint8_t* codes; /* device u8[n] */
     uint8_t* exps;  /* device u8[ceil(n/block)] */
-    void* values;   /* device, n elements */
+    void* values;   /* device, n elements of `dtype` */
     int64_t n;
     int moment;     /* 1 or 2 */
 } loco_adamw_state_t;
 
 /*
- * loco_adamw_state_read  - values = what the states stand for, in `dtype` (LOCO_F32 or LOCO_BF16,
- *                          both exact).
- * loco_adamw_state_write - the states of the values, as loco_adamw stores them.
+ * loco_adamw_state_plan  - as loco_adamw_plan, for states and their values, LOCO_F32 or LOCO_BF16; no buffer may
+ *                          overlap another.  The array of states is read during the call only.
+ * loco_adamw_state_read  - values = what the plan's states stand for (exact in either type).
+ * loco_adamw_state_write - the states of the plan's values, as loco_adamw stores them.
  */
-int loco_adamw_state_read(const loco_adamw_state_t* states, int nstates, int block,
-                          loco_dtype_t dtype, void* stream);
-int loco_adamw_state_write(const loco_adamw_state_t* states, int nstates, int block,
-                           loco_dtype_t dtype, void* stream);
+int loco_adamw_state_plan(const loco_adamw_state_t* states, int nstates, int block, loco_dtype_t dtype,
+                          void* table, int64_t table_bytes, loco_adamw_plan_t* plan, void* stream);
+int loco_adamw_state_read(const loco_adamw_plan_t* plan, void* stream);
+int loco_adamw_state_write(const loco_adamw_plan_t* plan, void* stream);
 
 /* A static, human-readable name for a status code. */
 const char* loco_status_string(int status);

@@ -28,30 +28,80 @@ def tensor(param=P[0], grad=P[1], m=P[2], v=P[3], me=P[4], ve=P[5], copy=P[6], n
     return loco.AdamwTensor(param, grad, m, v, me, ve, copy, n, wd)
 
 
-def adamw(lib, ts=None, nt=None, pd=F32, gd=BF16, bits=8, block=256, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, step=1,
-          scale=P[7], null=False):
+def plan_of(lib, ts=None, nt=None, pd=F32, gd=BF16, bits=8, block=256, table=P[15], nbytes=1 << 20, null=False):
+    """(status, plan, the array that it refers to) of loco_adamw_plan."""
     ts = [tensor()] if ts is None else ts
-    arr = (loco.AdamwTensor * max(1, len(ts)))(*ts)
-    opt = loco.AdamwOptions(lr, b1, b2, eps, step)
-    return lib.loco_adamw(arr if ts else None, len(ts) if nt is None else nt, pd, gd, bits, block,
-                          None if null else ctypes.byref(opt), scale, None)
+    arr, plan = (loco.AdamwTensor * max(1, len(ts)))(*ts), loco.AdamwPlan()
+    st = lib.loco_adamw_plan(arr if ts else None, len(ts) if nt is None else nt, pd, gd, bits, block, table, nbytes,
+                             None if null else ctypes.byref(plan), None)
+    return st, plan, arr
+
+
+def adamw(lib, ts=None, **kw):
+    return plan_of(lib, ts, **kw)[0]
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(nt=-1), INV), (dict(ts=[], nt=1), INV), (dict(ts=[]), OK), (dict(null=True), INV),
     (dict(pd=I8), INV), (dict(gd=I8), INV), (dict(pd=5), INV), (dict(bits=4), INV), (dict(bits=16), INV),
     (dict(block=0), INV), (dict(block=-64), INV), (dict(block=100), UNSUP), (dict(block=1024), UNSUP),
-    (dict(lr=NAN), INV), (dict(lr=INF), INV), (dict(lr=1e300), INV), (dict(b1=1.0), INV), (dict(b1=-0.1), INV),
-    (dict(b2=1.0), INV), (dict(b2=NAN), INV), (dict(eps=0.0), INV), (dict(eps=-1e-8), INV), (dict(eps=1e-60), INV),
-    (dict(eps=1e39), INV), (dict(eps=NAN), INV), (dict(step=0), INV), (dict(step=-3), INV), (dict(scale=P[7] + 4), ALIGN),
-    (dict(scale=P[0] + 16), INV), (dict(scale=P[5]), INV), (dict(scale=None, ts=[tensor(n=0)]), OK),
+    (dict(table=None), INV), (dict(nbytes=64), INV), (dict(nbytes=-1), INV), (dict(table=P[15] + 8), ALIGN),
+    (dict(table=P[1] + 16), INV), (dict(table=P[5]), INV), (dict(ts=[tensor(n=0)], table=None), OK),
 ])
-def test_adamw_arguments(lib, kw, want):
+def test_adamw_plan(lib, kw, want):
     assert adamw(lib, **kw) == want
 
 
+def test_adamw_table_bytes(lib):
+    w = lib.loco_adamw_table_bytes
+    assert w(0) == w(-5) == 0 and 0 < w(1) < w(2) < w(1000)
+    assert adamw(lib, nbytes=w(1) - 1) == INV
+
+
+def step(lib, plan, lr=1e-3, b1=0.9, b2=0.99, eps=1e-8, t=1, scale=None, null=False):
+    opt = loco.AdamwOptions(lr, b1, b2, eps, t)
+    return lib.loco_adamw(plan and ctypes.byref(plan), None if null else ctypes.byref(opt), scale, None)
+
+
 @pytest.mark.parametrize("kw,want", [
-    (dict(n=-1), INV), (dict(n=(1 << 52) + 1), INV), (dict(wd=NAN), INV), (dict(wd=INF), INV), (dict(wd=1e300), INV),
+    (dict(null=True), INV), (dict(lr=NAN), INV), (dict(lr=INF), INV), (dict(lr=1e300), INV), (dict(b1=1.0), INV),
+    (dict(b1=-0.1), INV), (dict(b2=1.0), INV), (dict(b2=NAN), INV), (dict(eps=0.0), INV), (dict(eps=-1e-8), INV),
+    (dict(eps=1e-60), INV), (dict(eps=1e39), INV), (dict(eps=NAN), INV), (dict(t=0), INV), (dict(t=-3), INV),
+    (dict(scale=P[7] + 4), ALIGN), (dict(), OK), (dict(scale=P[7]), OK),
+])
+def test_adamw_options(lib, kw, want):
+    """Of a plan without tensors, which launches nothing."""
+    st, plan, _ = plan_of(lib, [])
+    assert st == OK and step(lib, plan, **kw) == want
+
+
+def test_adamw_of_a_plan_that_is_none(lib):
+    assert step(lib, None) == INV
+    assert step(lib, loco.AdamwPlan()) == INV  # never filled
+    states = loco.AdamwPlan()
+    assert lib.loco_adamw_state_plan(None, 0, 256, BF16, None, 0, ctypes.byref(states), None) == OK
+    assert step(lib, states) == INV
+    _, plan, _ = plan_of(lib, [])
+    for fn in (lib.loco_adamw_state_read, lib.loco_adamw_state_write):
+        assert fn(None, None) == INV and fn(ctypes.byref(plan), None) == INV and fn(ctypes.byref(states), None) == OK
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(scale=P[0] + 16), INV), (dict(scale=P[2]), INV), (dict(scale=P[3] + 992), INV), (dict(scale=P[4]), INV),
+    (dict(scale=P[5]), INV), (dict(scale=P[6] + 16), INV), (dict(scale=P[7] + 4), ALIGN),
+])
+def test_adamw_grad_scale_of_a_plan(lib, kw, want):
+    """The plan's tensors are looked at before the launch (which no refused call reaches)."""
+    arr = (loco.AdamwTensor * 1)(tensor())
+    _, plan, _ = plan_of(lib, [])
+    plan.ntensors, plan.tensors = 1, arr
+    assert step(lib, plan, **kw) == want
+    arr[0].weight_decay = 1e300
+    assert step(lib, plan) == INV
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), INV), (dict(n=(1 << 52) + 1), INV), (dict(wd=NAN), INV), (dict(wd=INF), INV),
     (dict(param=None), INV), (dict(grad=None), INV), (dict(m=None), INV), (dict(v=None), INV), (dict(me=None), INV),
     (dict(ve=None), INV), (dict(param=P[0] + 4), ALIGN), (dict(grad=P[1] + 2), ALIGN), (dict(m=P[2] + 1), ALIGN),
     (dict(v=P[3] + 8), ALIGN), (dict(me=P[4] + 1), ALIGN), (dict(ve=P[5] + 2), ALIGN), (dict(copy=P[6] + 2), ALIGN),
@@ -63,7 +113,7 @@ def test_adamw_tensor(lib, kw, want):
     assert adamw(lib, [tensor(**kw)]) == want
     # the same with a good tensor before it, elsewhere
     far = tensor(*(p + (1 << 30) for p in P[8:15]))
-    if want != OK:
+    if want != OK:  # a plan that passes fills its table
         assert adamw(lib, [far, tensor(**kw)]) == want
 
 
@@ -93,21 +143,18 @@ def state(codes=P[0], exps=P[1], values=P[2], n=1000, moment=1):
     ([state(moment=0)], dict(), INV), ([state(moment=3)], dict(), INV), ([state(codes=None)], dict(), INV),
     ([state(exps=None)], dict(), INV), ([state(values=None)], dict(), INV), ([state(codes=P[0] + 1)], dict(), ALIGN),
     ([state(exps=P[1] + 4)], dict(), ALIGN), ([state(values=P[2] + 2)], dict(), ALIGN),
-    ([state(values=P[0] + 16)], dict(), INV), ([state(values=P[1])], dict(), INV), ([state(n=0)], dict(), OK),
+    ([state(values=P[0] + 16)], dict(), INV), ([state(values=P[1])], dict(), INV), ([state(n=0)], dict(table=None), OK),
+    ([state()], dict(table=None), INV), ([state()], dict(table=P[15] + 8), ALIGN), ([state()], dict(table=P[1]), INV),
+    ([state()], dict(nbytes=16), INV), ([state()], dict(null=True), INV),
+    ([state(), state(codes=P[3], exps=P[4])], dict(), INV), ([state(), state(exps=P[4], values=P[5])], dict(), INV),
+    ([state(), state(codes=P[3], values=P[5])], dict(), INV),
 ])
-def test_adamw_states(lib, s, kw, want):
-    a = dict(ns=len(s), block=256, dtype=BF16)
+def test_adamw_state_plan(lib, s, kw, want):
+    a = dict(ns=len(s), block=256, dtype=BF16, table=P[15], nbytes=1 << 20, null=False)
     a.update(kw)
-    arr = (loco.AdamwState * max(1, len(s)))(*s)
-    for fn in (lib.loco_adamw_state_read, lib.loco_adamw_state_write):
-        assert fn(arr if s else None, a["ns"], a["block"], a["dtype"], None) == want
-
-
-def test_adamw_states_that_share(lib):
-    """Read, values must not be written twice but codes may be read twice; written, the other way round."""
-    for shared, bad in ((dict(values=P[2]), lib.loco_adamw_state_read), (dict(codes=P[0]), lib.loco_adamw_state_write)):
-        arr = (loco.AdamwState * 2)(state(), state(**{**dict(codes=P[3], exps=P[4], values=P[5]), **shared}))
-        assert bad(arr, 2, 256, BF16, None) == INV
+    arr, plan = (loco.AdamwState * max(1, len(s)))(*s), loco.AdamwPlan()
+    assert lib.loco_adamw_state_plan(arr if s else None, a["ns"], a["block"], a["dtype"], a["table"], a["nbytes"],
+                                     None if a["null"] else ctypes.byref(plan), None) == want
 
 
 @pytest.fixture
@@ -151,9 +198,10 @@ def test_adamw_binding(no_device, make, err, match):
 
 def test_adamw_binding_kinds_and_plans(no_device, monkeypatch):
     monkeypatch.setattr(loco, "_ptr", lambda t, dev: None if t is None else t.data_ptr())
+    monkeypatch.setattr(loco, "_stream", lambda stream, dev: 0)
     with pytest.raises(TypeError, match="one kind"):
         loco.AdamwTensors([(t(8), t(8), t(8), t(8)), (t(8), t(8, BF), t(8), t(8))])
-    plan = loco.AdamwTensors([(t(8), t(8), t(8), t(8))])
+    plan = loco.AdamwTensors([])
     with pytest.raises(ValueError, match="its own"):
         loco.adamw(plan, step=1, lr=1e-3, weight_decay=0.1)
     with pytest.raises(ValueError, match="its own"):
