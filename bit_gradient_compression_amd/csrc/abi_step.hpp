@@ -343,10 +343,9 @@ int check_logits(int64_t rows, int64_t vocab, int64_t ld, int dtype, float scale
 }  // namespace
 
 LOCO_API int64_t loco_token_logprobs_workspace(int64_t rows, int64_t vocab, int top) {
-    (void)rows;
-    (void)vocab;
-    (void)top;
-    return 0;
+    if (rows < 0 || vocab < 1 || vocab > kLpMaxVocab || !sizes_ok(rows, vocab) || top < 0 || top > kLpMaxTop) return 0;
+    const int64_t splits = lp_splits(rows, vocab);
+    return splits > 1 ? rows * splits * (16 + top * 8) : 0;
 }
 
 LOCO_API int loco_token_logprobs(const void* logits, loco_dtype_t dtype, int64_t rows, int64_t vocab, int64_t ld,
@@ -370,8 +369,9 @@ LOCO_API int loco_token_logprobs(const void* logits, loco_dtype_t dtype, int64_t
                      {top_logprobs, rows * top * 4, true, true},
                      {workspace, need, true, true}});
     if (st != LOCO_OK) return st;
+    const int64_t parts = need > 0 ? rows * lp_splits(rows, vocab) : 0;
     const LpParams p = {logits, rows, ld, (int)vocab, targets, scale, logprob, entropy, stats, top_ids, top_logprobs, top,
-                        dtype == LOCO_F32};
+                        dtype == LOCO_F32, (f32x4_t*)workspace, (uint64_t*)((char*)workspace + parts * 16), 0, 0};
     return hip_status(launch_lp(p, (hipStream_t)stream));
 }
 

@@ -103,6 +103,7 @@ hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream);
 
 // ---- log probabilities of tokens ---------------------------------------------------------
 
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kLpMaxTop = 32;
 constexpr int64_t kLpMaxVocab = (int64_t)1 << 24;
 
@@ -119,7 +120,13 @@ struct LpParams {
     float* top_logprobs;
     int top;
     int f32;
+    f32x4_t* sums;   // [rows][splits] of a row's pieces: maximum and sums
+    uint64_t* keys;  // [rows][splits][top]: their best values
+    int splits, piece;  // set by launch_lp: pieces per row, chunks of eight per piece
 };
+// Pieces of a row that a call works on apart and joins in a second launch; 1: none.
+constexpr int kLpMaxSplits = 32;
+int lp_splits(int64_t rows, int64_t vocab);
 hipError_t launch_lp(const LpParams& p, hipStream_t stream);
 
 struct LpBwdParams {

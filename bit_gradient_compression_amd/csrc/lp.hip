@@ -70,15 +70,23 @@ __device__ __forceinline__ uint64_t group_max_u64(uint64_t v) {
     return (uint64_t)hi << 32 | lo;
 }
 
+// 16 bytes at any address.  Once: they leave the caches to what is read again.
+template <bool ONCE>
+__device__ __forceinline__ u32x4 load16_for(const void* p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load((const u32x4_any*)p);
+    else return load16(p);
+}
+
 // Values of a chunk, minus infinity past the row's end.
 template <typename T>
 struct LpChunk;
 template <>
 struct LpChunk<uint16_t> {
     u32x4 w;
+    template <bool ONCE>
     __device__ __forceinline__ void load(const uint16_t* p, int valid) {
         if (valid >= 8) {
-            w = load16(p);
+            w = load16_for<ONCE>(p);
         } else {
             w = u32x4{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
 #pragma unroll
@@ -94,9 +102,15 @@ struct LpChunk<uint16_t> {
 template <>
 struct LpChunk<float> {
     float w[8];
+    template <bool ONCE>
     __device__ __forceinline__ void load(const float* p, int valid) {
         if (valid >= 8) {
-            load_chunk(p, 8, w);
+            const u32x4 a = load16_for<ONCE>(p), b = load16_for<ONCE>(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = __uint_as_float(a[i]);
+                w[4 + i] = __uint_as_float(b[i]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = i < valid ? p[i] : -__builtin_huge_valf();
@@ -110,142 +124,172 @@ struct LpChunk<float> {
 
 // ---- forward --------------------------------------------------------------------------
 
-constexpr int kLpCand = 1024;  // candidates that are ranked at once
+// Candidates that are ranked at once, and slots (below) that are looked through once more.  A single wave's
+// bounds hold all that it can have where fewer lanes than k have a chunk, or where all values are equal.
+constexpr int lp_cand(int threads) { return threads == 64 ? 256 : 1024; }
+constexpr int lp_hits(int threads) { return threads == 64 ? 256 : 1024; }
+
+// A lane's batches of values, in order, over this many slots: each slot has the largest of its values.
+constexpr int lp_slots(int threads) { return threads == 256 ? 16 : threads == 64 ? 4 : 2; }
 
 template <int THREADS>
 struct LpShared {
     Sums wave[THREADS / 64];
+    uint64_t lane[THREADS];  // each lane's best
     uint64_t group[64];
-    uint64_t cand[kLpCand];
-    uint16_t hit[THREADS];
+    uint64_t cand[lp_cand(THREADS) + 8];
+    float slot[lp_slots(THREADS)][THREADS];
+    uint16_t hit[lp_hits(THREADS)];
     int nhit, ncand;
-    uint64_t best;
+    uint64_t bound, best;
 };
 
-// The row's best `top` values by THREADS threads, each of which has met the chunks of its own number
-// plus multiples of THREADS, the best of them `mine`.
-template <typename T, int THREADS>
-__device__ void lp_top(const LpParams& p, const T* x, int64_t row, uint64_t mine, float m, float log_s, bool lost,
-                       LpShared<THREADS>& sh) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    int32_t* ids = p.top_ids + row * p.top;
-    float* lps = p.top_logprobs + row * p.top;
-    if (lost) {
-        for (int i = tid; i < p.top; i += THREADS) {
-            ids[i] = -1;
-            lps[i] = __builtin_nanf("");
-        }
-        return;
+// The sums of all waves, in every lane.  sh.wave is free again after the next barrier.
+template <int THREADS>
+__device__ __forceinline__ Sums join_waves(Sums a, float c, LpShared<THREADS>& sh) {
+    constexpr int WAVES = THREADS / 64;
+    const int lane = threadIdx.x & 63;
+    a.move(wave_max(a.m), c);
+    a.s = wave_sum(a.s);
+    a.t = wave_sum(a.t);
+    if constexpr (WAVES > 1) {
+        if (lane == 0) sh.wave[threadIdx.x >> 6] = a;
+        __syncthreads();
+        const Sums none = {kLowest, 0.0f, 0.0f};
+        a = lane < WAVES ? sh.wave[lane] : none;
+        a.move(wave_max(a.m), c);
+        a.s = wave_sum(a.s);
+        a.t = wave_sum(a.t);
     }
-    const int nchunks = (p.vocab + 7) / 8;
-    const int k = p.top < p.vocab ? p.top : p.vocab;
-    // every wave ranks the groups' bests by itself
-    const uint64_t own = sh.group[lane];
-    int rank = 0;
+    return a;
+}
+
+// The k-th largest of the 64 groups' bests (1 if fewer groups than k have one), in every lane.  A group is every
+// 64th lane: where all values are equal and the first ones count, these are in as many groups.  Called by all
+// threads after the barrier that follows the writes of sh.lane; ends with one.
+template <int THREADS>
+__device__ __forceinline__ uint64_t kth_group(int k, LpShared<THREADS>& sh) {
+    constexpr int PER = THREADS / 64;  // lanes per group: each compares it with 64 / PER others
+    const int g = threadIdx.x / PER, part = threadIdx.x % PER;
+    const uint64_t own = group_max_u64<PER>(sh.lane[part * 64 + g]);
+    if (part == 0) sh.group[g] = own;
+    __syncthreads();
+    int above = 0;
 #pragma unroll 16
-    for (int i = 0; i < 64; ++i) rank += sh.group[i] > own;
-    const uint64_t at = ballot(rank == k - 1 && own != 0);
-    // fewer groups than k have a chunk at all: everything counts
-    uint64_t bound = 1;
-    if (at) {
-        const int src = __builtin_ctzll(at);
-        bound = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(own >> 32), src) << 32 |
-                (uint32_t)__builtin_amdgcn_readlane((uint32_t)own, src);
-    }
-    if (mine >= bound) sh.hit[atomicAdd(&sh.nhit, 1)] = (uint16_t)tid;
+    for (int i = 0; i < 64 / PER; ++i) above += sh.group[part * (64 / PER) + i] > own;
+    if constexpr (PER >= 2) above += (int)dpp<0xB1>((uint32_t)above);
+    if constexpr (PER >= 4) above += (int)dpp<0x4E>((uint32_t)above);
+    if constexpr (PER >= 8) above += (int)dpp<0x141>((uint32_t)above);
+    if constexpr (PER >= 16) above += (int)dpp<0x140>((uint32_t)above);
+    if (above == k - 1 && own != 0) sh.bound = own;  // one group's lanes: the keys differ
     __syncthreads();
-    const int turns = (nchunks + THREADS - 1) / THREADS, jobs = sh.nhit * turns;
-    for (int job = tid; job < jobs; job += THREADS) {
-        const int c = sh.hit[job / turns] + job % turns * THREADS;
-        if (c >= nchunks) continue;
-        const int left = p.vocab - c * 8, valid = left < 8 ? left : 8;
-        LpChunk<T> ch;
-        ch.load(x + (int64_t)c * 8, valid);
-        float v[8];
-        ch.get(v);
+    return sh.bound;
+}
+
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t u = (uint32_t)(key >> 32);
+    return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+template <int THREADS>
+__device__ __forceinline__ void add_candidate(uint64_t key, LpShared<THREADS>& sh) {
+    const int n = atomicAdd(&sh.ncand, 1);
+    if (n < lp_cand(THREADS)) sh.cand[n] = key;
+}
+
+// The first k of the n candidates in order: emit(rank, key).
+template <int THREADS, typename Emit>
+__device__ __forceinline__ void rank_candidates(int n, int k, LpShared<THREADS>& sh, Emit emit) {
+    if (threadIdx.x < 8) sh.cand[n + threadIdx.x] = 0;  // the last eight that are read together
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const uint64_t key = sh.cand[i];
+        int above = 0;
+        for (int j = 0; j < n; j += 8)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < valid && order_key(v[j], (uint32_t)c) >= bound) {
-                const int n = atomicAdd(&sh.ncand, 1);
-                if (n < kLpCand) sh.cand[n] = order_key(v[j], (uint32_t)(c * 8 + j));
-            }
-    }
-    __syncthreads();
-    const int n = sh.ncand;
-    auto write = [&](int i, uint64_t key) {
-        const uint32_t id = ~(uint32_t)key, u = (uint32_t)(key >> 32);
-        const float v = __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
-        ids[i] = (int32_t)id;
-        lps[i] = v == -__builtin_huge_valf() ? v : scaled_diff(v, m, p.scale) - log_s;
-    };
-    if (n <= kLpCand) {
-        for (int i = tid; i < n; i += THREADS) {
-            const uint64_t key = sh.cand[i];
-            int above = 0;
-            for (int j = 0; j < n; ++j) above += sh.cand[j] > key;
-            if (above < k) write(above, key);
-        }
-    } else {
-        // More values in the hit lanes than fit, as where few lanes hold all the large ones: one after
-        // the other, each the largest below the last.
-        uint64_t last = ~(uint64_t)0;
-        for (int i = 0; i < k; ++i) {
-            uint64_t best = 0;
-            for (int j = tid; j < p.vocab; j += THREADS) {
-                float v;
-                if constexpr (sizeof(T) == 2) v = __uint_as_float((uint32_t)x[j] << 16);
-                else v = x[j];
-                const uint64_t key = order_key(v, (uint32_t)j);
-                best = key < last && key > best ? key : best;
-            }
-            best = group_max_u64<64>(best);
-            if (tid == 0) sh.best = 0;
-            __syncthreads();
-            if (lane == 0) atomicMax((unsigned long long*)&sh.best, (unsigned long long)best);
-            __syncthreads();
-            last = sh.best;
-            if (tid == 0) write(i, last);
-            __syncthreads();
-        }
-    }
-    for (int i = k + tid; i < p.top; i += THREADS) {
-        ids[i] = -1;
-        lps[i] = -__builtin_huge_valf();
+            for (int q = 0; q < 8; ++q) above += sh.cand[j + q] > key;
+        if (above < k) emit(above, key);
     }
 }
 
-// One workgroup per row.
-template <typename T, int THREADS, bool ENTROPY, bool TOP>
+// One of a row's alternatives.
+__device__ __forceinline__ void write_top(const LpParams& p, int64_t row, int i, uint64_t key, float m, float log_s) {
+    const float v = key_value(key);
+    p.top_ids[row * p.top + i] = (int32_t) ~(uint32_t)key;
+    p.top_logprobs[row * p.top + i] = v == -__builtin_huge_valf() ? v : scaled_diff(v, m, p.scale) - log_s;
+}
+
+// Alternatives past the vocabulary, or all of them of a row without a distribution.
+__device__ __forceinline__ void write_no_top(const LpParams& p, int64_t row, int i, bool lost) {
+    p.top_ids[row * p.top + i] = -1;
+    p.top_logprobs[row * p.top + i] = lost ? __builtin_nanf("") : -__builtin_huge_valf();
+}
+
+// A row's numbers from its sums, by one thread.
+template <typename T>
+__device__ __forceinline__ void write_row(const LpParams& p, int64_t row, const Sums& a, float log_s) {
+    const bool lost = a.s != a.s, empty = a.s == 0.0f;
+    const float nan = __builtin_nanf(""), inf = __builtin_huge_valf();
+    if (p.stats) {
+        p.stats[2 * row] = lost ? nan : empty ? -inf : a.m;
+        p.stats[2 * row + 1] = a.s;
+    }
+    if (p.entropy) p.entropy[row] = empty ? 0.0f : log_s - p.scale * a.t / a.s;
+}
+template <typename T>
+__device__ __forceinline__ float target_logit(const LpParams& p, int64_t row, int64_t& target) {
+    target = p.targets[row];
+    if (target < 0 || target >= p.vocab) return 0.0f;
+    const T* x = (const T*)p.logits + row * p.ld + target;
+    if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)*x << 16);
+    else return *x;
+}
+__device__ __forceinline__ void write_logprob(const LpParams& p, int64_t row, const Sums& a, float log_s, int64_t target,
+                                              float xt) {
+    p.logprob[row] = target < 0                         ? 0.0f
+                     : a.s != a.s || target >= p.vocab ? __builtin_nanf("")
+                     : a.s == 0.0f                      ? -__builtin_huge_valf()
+                                                        : scaled_diff(xt, a.m, p.scale) - log_s;
+}
+
+// One workgroup per row, or (SPLIT) per piece of p.piece chunks of a row, whose sums and best values go to the
+// workspace for lp_join_kernel.
+template <typename T, int THREADS, bool ENTROPY, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(THREADS) void lp_kernel(const LpParams p, int64_t row0) {
-    constexpr int WAVES = THREADS / 64, U = sizeof(T) == 2 ? 4 : 2;  // 64 bytes per lane at once
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;  // 64 bytes per lane at once
     __shared__ LpShared<THREADS> sh;
-    const int64_t row = row0 + blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    int64_t row = row0 + blockIdx.x;
+    int first = 0, last = (p.vocab + 7) / 8;  // chunks
+    int64_t part = 0;
+    if constexpr (SPLIT) {
+        part = row0 + blockIdx.x;
+        row = part / p.splits;
+        first = (int)(part - row * p.splits) * p.piece;
+        last = min(last, first + p.piece);
+    }
+    const int tid = threadIdx.x;
     const T* x = (const T*)p.logits + row * p.ld;
     const float c = p.scale * kLog2e;
-    const int nchunks = (p.vocab + 7) / 8;
-    if (TOP && tid == 0) sh.nhit = sh.ncand = 0;
+    if constexpr (TOP) {
+        if (tid == 0) {
+            sh.nhit = sh.ncand = 0;
+            sh.bound = 1;
+        }
+    }
     // the given token's logit, on its way beside the row's
     int64_t target = -1;
     float xt = 0.0f;
-    if (tid == 0 && p.targets) {
-        target = p.targets[row];
-        if (target >= 0 && target < p.vocab) {
-            if constexpr (sizeof(T) == 2) xt = __uint_as_float((uint32_t)x[target] << 16);
-            else xt = x[target];
-        }
-    }
+    if (!SPLIT && tid == 0 && p.logprob) xt = target_logit<T>(p, row, target);
     Sums a = {kLowest, 0.0f, 0.0f};
     float best = -__builtin_huge_valf();
-    uint32_t best_chunk = tid;
-    for (int c0 = tid; c0 < nchunks; c0 += U * THREADS) {
-        LpChunk<T> ch[U];
+    uint32_t best_chunk = first + tid;
+    LpChunk<T> ch[U];
+    constexpr int SLOTS = lp_slots(THREADS);
+    int turn = 0;
+    auto valid_of = [&](int at) { return at < last ? min(p.vocab - at * 8, 8) : 0; };
+    for (int c0 = first + tid; c0 < last; c0 += U * THREADS, ++turn) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t at = (int64_t)(c0 + u * THREADS) * 8;
-            const int64_t left = p.vocab - at;
-            ch[u].load(x + at, left < 8 ? (left > 0 ? (int)left : 0) : 8);
-        }
+        for (int u = 0; u < U; ++u) ch[u].template load<!TOP>(x + (int64_t)(c0 + u * THREADS) * 8, valid_of(c0 + u * THREADS));
         float v[8], top = kLowest;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -256,6 +300,10 @@ __global__ __launch_bounds__(THREADS) void lp_kernel(const LpParams p, int64_t r
                 best_chunk = q > best ? (uint32_t)(c0 + u * THREADS) : best_chunk;
                 best = fmaxf(best, q);
             }
+        }
+        if constexpr (TOP) {
+            float& slot = sh.slot[turn % SLOTS][tid];
+            slot = turn < SLOTS ? top : fmaxf(slot, top);
         }
         a.move(fmaxf(a.m, top), c);
         float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
@@ -274,75 +322,200 @@ __global__ __launch_bounds__(THREADS) void lp_kernel(const LpParams p, int64_t r
         a.s += s[0] + s[1];
         a.t += t[0] + t[1];
     }
-    // the wave's and the row's sums
-    a.move(wave_max(a.m), c);
-    a.s = wave_sum(a.s);
-    if constexpr (ENTROPY) a.t = wave_sum(a.t);
     uint64_t mine = 0;
     if constexpr (TOP) {
-        mine = best_chunk < (uint32_t)nchunks ? order_key(best, best_chunk) : 0;
-        constexpr int G = THREADS / 64;  // lanes per group
-        const uint64_t g = group_max_u64<G>(mine);
-        if (tid % G == 0) sh.group[tid / G] = g;
+        mine = best_chunk < (uint32_t)last ? order_key(best, best_chunk) : 0;
+        sh.lane[tid] = mine;
     }
-    if constexpr (WAVES > 1) {
-        if (lane == 0) sh.wave[wave] = a;
-        __syncthreads();
-        a = sh.wave[0];
-#pragma unroll
-        for (int i = 1; i < WAVES; ++i) {
-            Sums b = sh.wave[i];
-            const float m = fmaxf(a.m, b.m);
-            a.move(m, c);
-            b.move(m, c);
-            a.s += b.s;
-            a.t += b.t;
-        }
-    } else if constexpr (TOP) {
-        __syncthreads();
-    }
-    const bool lost = a.s != a.s, empty = a.s == 0.0f;
-    const float log_s = logf(a.s);
+    a = join_waves<THREADS>(a, c, sh);
+    const float log_s = SPLIT ? 0.0f : logf(a.s);
+    const bool lost = a.s != a.s;
     if (tid == 0) {
-        const float nan = __builtin_nanf(""), inf = __builtin_huge_valf();
-        if (p.stats) {
-            p.stats[2 * row] = lost ? nan : empty ? -inf : a.m;
-            p.stats[2 * row + 1] = a.s;
+        if constexpr (SPLIT) {
+            p.sums[part] = f32x4{a.m, a.s, a.t, 0.0f};
+        } else {
+            write_row<T>(p, row, a, log_s);
+            if (p.logprob) write_logprob(p, row, a, log_s, target, xt);
         }
-        if (p.logprob)
-            p.logprob[row] = target < 0                   ? 0.0f
-                             : lost || target >= p.vocab ? nan
-                             : empty                      ? -inf
-                                                          : scaled_diff(xt, a.m, p.scale) - log_s;
-        if (p.entropy) p.entropy[row] = empty ? 0.0f : log_s - p.scale * a.t / a.s;
     }
-    if constexpr (TOP) lp_top<T, THREADS>(p, x, row, mine, a.m, log_s, lost, sh);
+    if constexpr (TOP) {
+        const int elems = min(p.vocab - first * 8, (last - first) * 8);
+        const int k = min(p.top, elems);
+        uint64_t* keys = SPLIT ? p.keys + part * p.top : nullptr;
+        auto emit = [&](int i, uint64_t key) {
+            if constexpr (SPLIT) keys[i] = key;
+            else write_top(p, row, i, key, a.m, log_s);
+        };
+        for (int i = tid; i < p.top; i += THREADS) {
+            if (i < k && !lost) continue;
+            if constexpr (SPLIT) keys[i] = 0;
+            else write_no_top(p, row, i, lost);
+        }
+        if (lost) return;  // the workgroup
+        if constexpr (THREADS == 64) __syncthreads();
+        const uint64_t bound = kth_group<THREADS>(k, sh);
+        // The values of the slots that reach the bound, once more, one per lane.  (Taken from the registers of
+        // the lanes that hold them, they need a branch each: code that runs once is fetched for as long as it
+        // runs.)
+        const int turns = (last - first + U * THREADS - 1) / (U * THREADS);
+        if (mine >= bound) {
+            const float least = bound == 1 ? kLowest : key_value(bound);  // minus infinity is in a slot as the lowest number
+            for (int i = 0; i < min(turns, SLOTS); ++i)
+                if (first + tid + i * U * THREADS < last && sh.slot[i][tid] >= least) {
+                    const int n = atomicAdd(&sh.nhit, 1);
+                    if (n < lp_hits(THREADS)) sh.hit[n] = (uint16_t)(tid * SLOTS + i);
+                }
+        }
+        __syncthreads();
+        const int each = min(U, (last - first + THREADS - 1) / THREADS);  // chunks of a batch
+        const int per = (turns + SLOTS - 1) / SLOTS * each * 8, nhit = sh.nhit;
+        if (nhit <= lp_hits(THREADS)) {
+            for (int job = tid; job < nhit * per; job += THREADS) {
+                const int h = job / per, r = job - h * per, lane_of = sh.hit[h] / SLOTS, slot = sh.hit[h] % SLOTS;
+                const int at = first + lane_of + ((slot + r / (each * 8) * SLOTS) * U + r / 8 % each) * THREADS;
+                const int i = at * 8 + r % 8;
+                if (at >= last || i >= p.vocab) continue;
+                float v;
+                if constexpr (sizeof(T) == 2) v = __uint_as_float((uint32_t)x[i] << 16);
+                else v = x[i];
+                if (order_key(v, (uint32_t)at) >= bound) add_candidate(order_key(v, (uint32_t)i), sh);
+            }
+        }
+        __syncthreads();
+        const int n = sh.ncand;
+        if (nhit <= lp_hits(THREADS) && n <= lp_cand(THREADS)) {
+            rank_candidates<THREADS>(n, k, sh, emit);
+            return;
+        }
+        // More slots or values than fit, as where few lanes hold all the large ones: one after the other, each
+        // the largest below the last.
+        uint64_t before = ~(uint64_t)0;
+        for (int i = 0; i < k; ++i) {
+            uint64_t most = 0;
+            for (int j = tid; j < elems; j += THREADS) {
+                float v;
+                if constexpr (sizeof(T) == 2) v = __uint_as_float((uint32_t)x[first * 8 + j] << 16);
+                else v = x[first * 8 + j];
+                const uint64_t key = order_key(v, (uint32_t)(first * 8 + j));
+                most = key < before && key > most ? key : most;
+            }
+            most = group_max_u64<64>(most);
+            if (tid == 0) sh.best = 0;
+            __syncthreads();
+            if ((tid & 63) == 0) atomicMax((unsigned long long*)&sh.best, (unsigned long long)most);
+            __syncthreads();
+            before = sh.best;
+            if (tid == 0) emit(i, before);
+            __syncthreads();
+        }
+    }
 }
 
-template <typename T, int THREADS>
+// A row's results from its pieces' sums and best values, in the pieces' order.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(256) void lp_join_kernel(const LpParams p, int64_t row0) {
+    constexpr int THREADS = 256, KEYS = kLpMaxSplits * kLpMaxTop / THREADS;
+    static_assert(kLpMaxSplits * kLpMaxTop <= lp_cand(THREADS));
+    __shared__ LpShared<THREADS> sh;
+    const int64_t row = row0 + blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const float c = p.scale * kLog2e;
+    if constexpr (TOP) {
+        if (tid == 0) {
+            sh.ncand = 0;
+            sh.bound = 1;
+        }
+    }
+    int64_t target = -1;
+    float xt = 0.0f;
+    if (tid == 0 && p.logprob) xt = target_logit<T>(p, row, target);
+    uint64_t key[KEYS], mine = 0;
+    if constexpr (TOP) {
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+            const int at = i * THREADS + tid;
+            key[i] = at < p.splits * p.top ? p.keys[row * p.splits * p.top + at] : 0;
+            mine = key[i] > mine ? key[i] : mine;
+        }
+    }
+    Sums a = {kLowest, 0.0f, 0.0f};
+    if (lane < p.splits) {
+        const f32x4 q = p.sums[row * p.splits + lane];
+        a = {q.x, q.y, q.z};
+    }
+    a.move(wave_max(a.m), c);
+    a.s = wave_sum(a.s);
+    a.t = wave_sum(a.t);
+    const float log_s = logf(a.s);
+    const bool lost = a.s != a.s;
+    if (tid == 0) {
+        write_row<T>(p, row, a, log_s);
+        if (p.logprob) write_logprob(p, row, a, log_s, target, xt);
+    }
+    if constexpr (TOP) {
+        const int k = min(p.top, p.vocab);
+        for (int i = tid; i < p.top; i += THREADS)
+            if (i >= k || lost) write_no_top(p, row, i, lost);
+        if (lost) return;
+        sh.lane[tid] = mine;
+        __syncthreads();
+        const uint64_t bound = kth_group<THREADS>(k, sh);
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i)
+            if (key[i] >= bound) add_candidate(key[i], sh);
+        __syncthreads();
+        rank_candidates<THREADS>(sh.ncand, k, sh, [&](int i, uint64_t q) { write_top(p, row, i, q, a.m, log_s); });
+    }
+}
+
+template <typename T, int THREADS, bool SPLIT>
 const void* pick_lp(bool entropy, bool top) {
-    return entropy ? (top ? (const void*)&lp_kernel<T, THREADS, true, true> : (const void*)&lp_kernel<T, THREADS, true, false>)
-                   : (top ? (const void*)&lp_kernel<T, THREADS, false, true>
-                          : (const void*)&lp_kernel<T, THREADS, false, false>);
+    return entropy ? (top ? (const void*)&lp_kernel<T, THREADS, true, true, SPLIT>
+                          : (const void*)&lp_kernel<T, THREADS, true, false, SPLIT>)
+                   : (top ? (const void*)&lp_kernel<T, THREADS, false, true, SPLIT>
+                          : (const void*)&lp_kernel<T, THREADS, false, false, SPLIT>);
 }
 template <typename T>
-const void* pick_lp(int threads, bool entropy, bool top) {
-    return threads == 64    ? pick_lp<T, 64>(entropy, top)
-           : threads == 256 ? pick_lp<T, 256>(entropy, top)
-                            : pick_lp<T, 1024>(entropy, top);
+const void* pick_lp(int threads, bool split, bool entropy, bool top) {
+    return split            ? pick_lp<T, 256, true>(entropy, top)
+           : threads == 64  ? pick_lp<T, 64, false>(entropy, top)
+           : threads == 256 ? pick_lp<T, 256, false>(entropy, top)
+                            : pick_lp<T, 1024, false>(entropy, top);
+}
+template <typename T>
+const void* pick_lp_join(bool top) {
+    return top ? (const void*)&lp_join_kernel<T, true> : (const void*)&lp_join_kernel<T, false>;
 }
 
 // ---- backward -------------------------------------------------------------------------
 
-constexpr int kLpBwdThreads = 256;
-constexpr int kLpBwdChunks = 4;  // per lane
+// One wave takes 1024 elements of a row; runs of 128 of them are on one XCD.  The stores stream past the
+// caches.  8192 x 32000 in bf16 / 333 x 50001 in fp32 (133 MB, whose half the caches hold), us: 169 / 25;
+// four waves of 2048 elements each in dispatch order 192 / 25, with streaming stores 184 / 27, with streaming
+// loads too 180 / 32; this with streaming loads too 165 / 29, with 1536 elements 175 / 26.
+constexpr int kLpBwdChunks = 2;  // per lane
+constexpr int kLpBwdTile = 64 * kLpBwdChunks * 8;
 
+__device__ __forceinline__ void store_once(uint16_t* p, int valid, const float (&v)[8]) {
+    if (valid >= 8) stream16(p, pack_bf16x8(v));
+    else store_chunk(p, valid, v);
+}
+__device__ __forceinline__ void store_once(float* p, int valid, const float (&v)[8]) {
+    if (valid >= 8) {
+        stream16(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+        stream16(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+    } else {
+        store_chunk(p, valid, v);
+    }
+}
+
+// segs: tiles per row.
 template <typename T, bool ENTROPY>
-__global__ __launch_bounds__(kLpBwdThreads) void lp_bwd_kernel(const LpBwdParams p, int64_t group0, int64_t segs) {
+__global__ __launch_bounds__(64) void lp_bwd_kernel(const LpBwdParams p, int64_t row0, uint32_t segs) {
     constexpr int U = kLpBwdChunks;
-    const int64_t g = group0 + blockIdx.x;
-    const int64_t row = g / segs;
-    const int base = (int)(g - row * segs) * (kLpBwdThreads * U * 8);
+    const uint32_t g = (uint32_t)xcd_remap<kXcds, 128>(blockIdx.x, gridDim.x), r = g / segs;
+    const int64_t row = row0 + r;
+    const int base = (int)(g - r * segs) * kLpBwdTile;
     const T* x = (const T*)p.logits + row * p.ld + base;
     T* dx = (T*)p.dlogits + row * p.dld + base;
     const int cols = p.vocab - base;  // of this segment and what follows
@@ -364,12 +537,12 @@ __global__ __launch_bounds__(kLpBwdThreads) void lp_bwd_kernel(const LpBwdParams
     LpChunk<T> ch[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int at = (u * kLpBwdThreads + (int)threadIdx.x) * 8;
-        if (!zero) ch[u].load(x + at, cols - at);
+        const int at = (u * 64 + (int)threadIdx.x) * 8;
+        if (!zero) ch[u].template load<false>(x + at, cols - at);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int at = (u * kLpBwdThreads + (int)threadIdx.x) * 8;
+        const int at = (u * 64 + (int)threadIdx.x) * 8;
         float v[8];
         if (zero) {
 #pragma unroll
@@ -385,37 +558,63 @@ __global__ __launch_bounds__(kLpBwdThreads) void lp_bwd_kernel(const LpBwdParams
                 v[j] += at + j == own ? p.scale * dlp : 0.0f;
             }
         }
-        store_chunk(dx + at, cols - at, v);
+        store_once(dx + at, cols - at, v);
     }
 }
 
 }  // namespace
 
-hipError_t launch_lp(const LpParams& p, hipStream_t stream) {
-    // At least 64 chunks for each of the groups' lanes, so that the groups bound the best values.
-    const int threads = p.vocab <= 2048 ? 64 : p.rows >= 512 || p.vocab < 8192 ? 256 : 1024;
+// Pieces of a row (1: one workgroup takes it whole).  With few rows a workgroup's arithmetic bounds it, a
+// batch of its lanes taking 1.5 us, so rows of more than one batch of 1024 lanes are cut into batches of 256
+// where four workgroups per compute unit are not there without; the second launch costs 2.5 us.  us without /
+// with 20 alternatives: 1 x 131071 4.9 / 9.9, whole 12.6 / 17.5; 1 x 32000 4.6 / 10.0, whole 4.2 / 6.8; 48 x
+// 131071 9.6 / 16.2, in pieces twice as large 10.3 / 16.6, in 5 of them 11.9 / 18.1, whole 16.7 / 21.9; 200 x
+// 131071 20 / 27, whole 20 / 23.
+int lp_splits(int64_t rows, int64_t vocab) {
+    if (rows <= 0 || rows >= 512 || vocab <= 32768) return 1;
+    const int64_t most = (vocab + 8191) / 8192, wanted = 1024 / rows;
+    const int64_t n = wanted < most ? wanted : most;
+    return (int)(n < 1 ? 1 : n < kLpMaxSplits ? n : kLpMaxSplits);
+}
+
+hipError_t launch_lp(const LpParams& params, hipStream_t stream) {
+    LpParams p = params;
     const bool entropy = p.entropy != nullptr, top = p.top > 0;
-    const void* k = p.f32 ? pick_lp<float>(threads, entropy, top) : pick_lp<uint16_t>(threads, entropy, top);
-    for (int64_t row0 = 0; row0 < p.rows; row0 += kMaxGrid) {
-        const int64_t rows = p.rows - row0 < kMaxGrid ? p.rows - row0 : kMaxGrid;
-        void* args[] = {(void*)&p, (void*)&row0};
-        const hipError_t err = hipLaunchKernel(k, dim3((unsigned)rows), dim3(threads), args, 0, stream);
+    p.splits = lp_splits(p.rows, p.vocab);
+    p.piece = ((p.vocab + 7) / 8 + p.splits - 1) / p.splits;
+    // At least one chunk for each of the groups' lanes, so that the groups bound the best values; few rows in
+    // large workgroups, many short ones in single waves (8192 x 2056: 15 us, 26 in four; 1024 x 4096 the
+    // same in both, with 20 alternatives 13 and 10).
+    const int threads = p.vocab <= 2048 || (p.rows >= 2048 && p.vocab <= 4096) ? 64
+                        : p.rows >= 512 || p.vocab < 8192                      ? 256
+                                                                               : 1024;
+    const bool split = p.splits > 1;
+    const void* k = p.f32 ? pick_lp<float>(threads, split, entropy, top) : pick_lp<uint16_t>(threads, split, entropy, top);
+    const int64_t groups = p.rows * p.splits;
+    for (int64_t g0 = 0; g0 < groups; g0 += kMaxGrid) {
+        const int64_t n = groups - g0 < kMaxGrid ? groups - g0 : kMaxGrid;
+        void* args[] = {(void*)&p, (void*)&g0};
+        const hipError_t err = hipLaunchKernel(k, dim3((unsigned)n), dim3(split ? 256 : threads), args, 0, stream);
         if (err != hipSuccess) return err;
     }
-    return hipSuccess;
+    if (!split) return hipSuccess;
+    int64_t row0 = 0;  // fewer rows than a grid holds are split
+    void* args[] = {(void*)&p, (void*)&row0};
+    return hipLaunchKernel(p.f32 ? pick_lp_join<float>(top) : pick_lp_join<uint16_t>(top), dim3((unsigned)p.rows), dim3(256),
+                           args, 0, stream);
 }
 
 hipError_t launch_lp_bwd(const LpBwdParams& p, hipStream_t stream) {
-    constexpr int64_t per = kLpBwdThreads * kLpBwdChunks * 8;
-    const int64_t segs = (p.vocab + per - 1) / per, groups = p.rows * segs;
+    const uint32_t segs = (uint32_t)((p.vocab + kLpBwdTile - 1) / kLpBwdTile);
+    const int64_t rows = kMaxGrid / segs;  // of one launch
     const bool entropy = p.dentropy != nullptr;
     const void* k = p.f32 ? (entropy ? (const void*)&lp_bwd_kernel<float, true> : (const void*)&lp_bwd_kernel<float, false>)
                           : (entropy ? (const void*)&lp_bwd_kernel<uint16_t, true>
                                      : (const void*)&lp_bwd_kernel<uint16_t, false>);
-    for (int64_t g0 = 0; g0 < groups; g0 += kMaxGrid) {
-        const int64_t n = groups - g0 < kMaxGrid ? groups - g0 : kMaxGrid;
-        void* args[] = {(void*)&p, (void*)&g0, (void*)&segs};
-        const hipError_t err = hipLaunchKernel(k, dim3((unsigned)n), dim3(kLpBwdThreads), args, 0, stream);
+    for (int64_t row0 = 0; row0 < p.rows; row0 += rows) {
+        const int64_t n = p.rows - row0 < rows ? p.rows - row0 : rows;
+        void* args[] = {(void*)&p, (void*)&row0, (void*)&segs};
+        const hipError_t err = hipLaunchKernel(k, dim3((unsigned)(n * segs)), dim3(64), args, 0, stream);
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
