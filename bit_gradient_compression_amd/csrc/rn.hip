@@ -292,13 +292,11 @@ struct RowPart {
     bool in;
 };
 
-// W columns of a row through the three phases of the pass.
+// What the pass reads of a row's W columns, as it lies in memory.
 template <typename T, int W, bool POST, int GATE>
-struct RnBwdPiece {
+struct RnRaw {
     using P = Piece<T, W>;
-    P h, dout, y, dh;
-    float dw[W];  // dweight's sum over the rows
-    float t[W];   // the gradient of the normed y
+    P h, dout, y, dh, gate;
 
     // A matrix that is not there is loaded as a span of no elements: values kept from the last row in
     // its place would need registers of their own.
@@ -313,14 +311,40 @@ struct RnBwdPiece {
     __device__ __forceinline__ void load_rest(const RnBwdParams& p, const RowPart& q) {
         load_y(p, q);
         dh.load(span_of<T>(p.dh, q.at, p.dh ? q.live : 0u), q.i);
+        if constexpr (GATE == kGateElement) gate.load(span_of<T>(p.gate, q.at, q.live), q.i);
+    }
+};
+
+// W columns of a row through the three phases of the pass.  KEEP: the parameters stay in registers.
+template <typename T, int W, bool POST, int GATE, bool KEEP>
+struct RnBwdPiece {
+    using P = Piece<T, W>;
+    using Raw = RnRaw<T, W, POST, GATE>;
+    float dw[W];  // dweight's sum over the rows
+    float t[W];   // the gradient of the normed y
+    float kept[3][KEEP ? W : 1];
+
+    __device__ __forceinline__ void keep(const RnBwdParams& p, const RowPart& q) {
+        get_param(p.dout ? p.weight : nullptr, p.param_f32, q.c0, q.count, q.i, kept[0]);
+        if constexpr (POST) get_param(p.post_weight, p.param_f32, q.c0, q.count, q.i, kept[1]);
+        if constexpr (GATE == kGateColumn) get_param(p.gate, p.param_f32, q.c0, q.count, q.i, kept[2]);
+    }
+    template <int WHICH>
+    __device__ __forceinline__ void param(const void* v, const RnBwdParams& p, const RowPart& q, float (&w)[W]) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j] = kept[WHICH][j];
+        } else {
+            get_param(v, p.param_f32, q.c0, q.count, q.i, w);
+        }
     }
     // The sum of dout weight xh.  Outside the row the values are 0, and so has to be r, which may be
     // infinite.
-    __device__ __forceinline__ void first(const RnBwdParams& p, const RowPart& q, float r, float& s) {
+    __device__ __forceinline__ void first(Raw& x, const RnBwdParams& p, const RowPart& q, float r, float& s) {
         float w[W], v[W], g[W];
-        get_param(p.weight, p.param_f32, q.c0, q.count, q.i, w);
-        h.get(v);
-        dout.get(g);
+        param<0>(p.weight, p, q, w);
+        x.h.get(v);
+        x.dout.get(g);
         const float rc = q.in ? r : 0.0f;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -328,21 +352,21 @@ struct RnBwdPiece {
             dw[j] += gx;
             s = __builtin_fmaf(gx, w[j], s);
         }
-        h.forget();
-        dout.forget();
+        x.h.forget();
+        x.dout.forget();
     }
     // dresidual and what follows from it; the sums over the rows of the gate's and the post-norm's
     // gradients are added by `add`.
     template <typename Add>
-    __device__ __forceinline__ void second(const RnBwdParams& p, const RowPart& q, float r, float s, float rp, float& s2,
-                                           Add add) {
+    __device__ __forceinline__ void second(Raw& x, const RnBwdParams& p, const RowPart& q, float r, float s, float rp,
+                                           float& s2, Add add) {
         float w[W], v[W], g[W];
-        get_param(p.dout ? p.weight : nullptr, p.param_f32, q.c0, q.count, q.i, w);
-        h.get(v);
-        dout.get(g);
+        param<0>(p.dout ? p.weight : nullptr, p, q, w);
+        x.h.get(v);
+        x.dout.get(g);
 #pragma unroll
         for (int j = 0; j < W; ++j) g[j] = (g[j] * w[j] - v[j] * r * s) * r;  // 0 without dout, whose r is 0
-        dh.get(v);
+        x.dh.get(v);
 #pragma unroll
         for (int j = 0; j < W; ++j) g[j] += v[j];
         if (p.dresidual) P::store(span_of<T>(p.dresidual, q.at, q.live), q.i, g);
@@ -350,20 +374,15 @@ struct RnBwdPiece {
         for (int j = 0; j < W; ++j) t[j] = q.in ? g[j] * p.scale : 0.0f;
         if constexpr (POST || GATE != kGateNone) {
             float yh[W];
-            y.get(yh);
+            x.y.get(yh);
             const float rc = q.in ? rp : 0.0f;
 #pragma unroll
             for (int j = 0; j < W; ++j) yh[j] *= rc;
-            if constexpr (POST) get_param(p.post_weight, p.param_f32, q.c0, q.count, q.i, w);
+            if constexpr (POST) param<1>(p.post_weight, p, q, w);
             if constexpr (GATE != kGateNone) {
                 float k[W];
-                if constexpr (GATE == kGateElement) {
-                    P gate;
-                    gate.load(span_of<T>(p.gate, q.at, q.live), q.i);
-                    gate.get(k);
-                } else {
-                    get_param(p.gate, p.param_f32, q.c0, q.count, q.i, k);
-                }
+                if constexpr (GATE == kGateElement) x.gate.get(k);
+                else param<2>(p.gate, p, q, k);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     v[j] = t[j] * (POST ? yh[j] * w[j] : yh[j]);
@@ -380,14 +399,14 @@ struct RnBwdPiece {
                     t[j] *= w[j];
                 }
                 add(0, v);
-                y.forget();
+                x.y.forget();
             }
         }
     }
-    __device__ __forceinline__ void third(const RnBwdParams& p, const RowPart& q, float rp, float s2) {
+    __device__ __forceinline__ void third(const Raw& x, const RnBwdParams& p, const RowPart& q, float rp, float s2) {
         if constexpr (POST) {
             float yh[W];
-            y.get(yh);
+            x.y.get(yh);
 #pragma unroll
             for (int j = 0; j < W; ++j) t[j] = (t[j] - yh[j] * rp * s2) * rp;
         }
@@ -396,6 +415,9 @@ struct RnBwdPiece {
 };
 
 // WPR waves per row, NP pieces of W columns per lane.
+//
+// In bf16 the next row is on its way while one is worked on.  Loads return in order, so none may follow
+// it: the parameters are kept in registers.  In fp32 those registers would cost a workgroup its place.
 template <typename T, int WPR, int W, int NP, int WAVES, bool POST, int GATE>
 __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p) {
     constexpr int TEAMS = WAVES / WPR;
@@ -404,6 +426,7 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
     constexpr int Q = W / 4;  // fours of columns per piece
     // Two chunks per lane do not fit: h, dout and y are read again for the phase that needs them, from the caches.
     constexpr bool ONCE = NP == 1;
+    constexpr bool AHEAD = ONCE && sizeof(T) == 2;
     constexpr int LSUMS = POST || GATE == kGateColumn ? 2 : 1;  // the join needs one
     __shared__ float red[2][2][WAVES];
     __shared__ float ltail[3][TEAMS][8];
@@ -415,8 +438,8 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
     const uint32_t cols = p.cols, whole = cols & ~(W - 1u);
     const float inv_cols = 1.0f / (float)p.cols;
     f32x4* mine = lsum + team * (COLS / 4) + lane;
-    RnBwdPiece<T, W, POST, GATE> pc[NP];
-    RnBwdPiece<T, 1, POST, GATE> tail;
+    RnBwdPiece<T, W, POST, GATE, AHEAD> pc[NP];
+    RnBwdPiece<T, 1, POST, GATE, AHEAD> tail;
     const bool tailed = (uint32_t)lane < cols - whole;
     float tsum[2] = {0.0f, 0.0f};
     tail.dw[0] = 0.0f;
@@ -442,48 +465,69 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
         }
         return v * inv_cols;
     };
-    const int64_t step = (int64_t)gridDim.x * TEAMS;
-    int64_t row = (int64_t)blockIdx.x * TEAMS + team;
-    // every team takes part in every turn's barriers, with or without a row
-    for (int flip = 0; row - team < p.rows; row += step, flip ^= 1) {
+    auto part = [&](int64_t row, int i) {
         const bool here = row < p.rows;
-        const int64_t at = row * cols;
-        const float r = here && p.dout ? p.rstd[row] : 0.0f;
-        const float rp = !POST ? 1.0f : here ? p.post_rstd[row] : 0.0f;
-        auto part = [&](int i) {
-            const uint32_t c = (uint32_t)(i * LANES + lane) * W;
-            return RowPart{at, 0, whole, here ? whole : 0u, c, here && c < whole};
-        };
-        const RowPart rest = {at + whole, whole, cols - whole, here ? cols - whole : 0u, (uint32_t)lane, here && tailed};
+        const uint32_t c = (uint32_t)(i * LANES + lane) * W;
+        return RowPart{row * cols, 0, whole, here ? whole : 0u, c, here && c < whole};
+    };
+    auto rest = [&](int64_t row) {
+        const bool here = row < p.rows;
+        return RowPart{row * cols + whole, whole, cols - whole, here ? cols - whole : 0u, (uint32_t)lane, here && tailed};
+    };
+    // What a row brings with it.
+    struct Row {
+        RnRaw<T, W, POST, GATE> x[NP];
+        RnRaw<T, 1, POST, GATE> tail;
+        float r, rp;
+    };
+    auto load_row = [&](Row& o, int64_t row) {
+        const bool here = row < p.rows;
+        o.r = here && p.dout ? p.rstd[row] : 0.0f;
+        o.rp = !POST ? 1.0f : here ? p.post_rstd[row] : 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            pc[i].load_first(p, part(i));
-            if (ONCE) pc[i].load_rest(p, part(i));
+            o.x[i].load_first(p, part(row, i));
+            if (ONCE) o.x[i].load_rest(p, part(row, i));
         }
         if (whole != cols) {
-            tail.load_first(p, rest);
-            tail.load_rest(p, rest);
+            o.tail.load_first(p, rest(row));
+            o.tail.load_rest(p, rest(row));
         }
+    };
+    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+    Row cur;
+    if constexpr (AHEAD) {
+        pc[0].keep(p, part(0, 0));
+        if (whole != cols) tail.keep(p, rest(0));
+        load_row(cur, row);
+    }
+    // every team takes part in every turn's barriers, with or without a row
+    for (int flip = 0; row - team < p.rows; row += step, flip ^= 1) {
+        Row next;
+        if constexpr (AHEAD) load_row(next, row + step);
+        else load_row(cur, row);
+        const float r = cur.r, rp = cur.rp;
         float s = 0.0f, s2 = 0.0f;
         if (p.dout) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 if (!ONCE) __builtin_amdgcn_sched_barrier(0);
-                pc[i].first(p, part(i), r, s);
+                pc[i].first(cur.x[i], p, part(row, i), r, s);
             }
-            if (whole != cols) tail.first(p, rest, r, s);
+            if (whole != cols) tail.first(cur.tail, p, rest(row), r, s);
             s = team_sum(s, flip, 0);
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            RowPart q = part(i);
+            RowPart q = part(row, i);
             if (!ONCE) {
                 __builtin_amdgcn_sched_barrier(0);  // one chunk after the other
                 asm volatile("" : "+v"(q.i));       // loads of their own, not the first phase's kept
-                pc[i].load_first(p, q);
-                pc[i].load_rest(p, q);
+                cur.x[i].load_first(p, q);
+                cur.x[i].load_rest(p, q);
             }
-            pc[i].second(p, q, r, s, rp, s2, [&](int which, const float(&v)[W]) {
+            pc[i].second(cur.x[i], p, q, r, s, rp, s2, [&](int which, const float(&v)[W]) {
 #pragma unroll
                 for (int k = 0; k < Q; ++k)
                     mine[which * (TEAMS * COLS / 4) + (Q * i + k) * LANES] +=
@@ -491,20 +535,22 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
             });
         }
         if (whole != cols)
-            tail.second(p, rest, r, s, rp, s2, [&](int which, const float(&v)[1]) { tsum[which] += v[0]; });
+            tail.second(cur.tail, p, rest(row), r, s, rp, s2, [&](int which, const float(&v)[1]) { tsum[which] += v[0]; });
         if constexpr (POST) s2 = team_sum(s2, flip, 1);
-        if (!p.dy) continue;
+        if (p.dy) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            RowPart q = part(i);
-            if (!ONCE) {
-                __builtin_amdgcn_sched_barrier(0);
-                asm volatile("" : "+v"(q.i));
-                pc[i].load_y(p, q);
+            for (int i = 0; i < NP; ++i) {
+                RowPart q = part(row, i);
+                if (!ONCE) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    asm volatile("" : "+v"(q.i));
+                    cur.x[i].load_y(p, q);
+                }
+                pc[i].third(cur.x[i], p, q, rp, s2);
             }
-            pc[i].third(p, q, rp, s2);
+            if (whole != cols) tail.third(cur.tail, p, rest(row), rp, s2);
         }
-        if (whole != cols) tail.third(p, rest, rp, s2);
+        if constexpr (AHEAD) cur = next;
     }
     if (!p.part) return;
     if (tailed) {
@@ -514,7 +560,7 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
     }
     // What LDS holds first, then dweight's sums through the first's place.
     auto join = [&](int which, const f32x4* teams) {
-        float* part = p.part + ((int64_t)blockIdx.x * 3 + which) * cols;
+        float* out = p.part + ((int64_t)blockIdx.x * 3 + which) * cols;
         __syncthreads();
         for (uint32_t q = threadIdx.x; q < COLS / 4; q += WAVES * 64) {
             const uint32_t c = (q / (Q * LANES) * LANES + q % LANES) * W + q / LANES % Q * 4;
@@ -523,13 +569,13 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
 #pragma unroll
             for (int k = 0; k < TEAMS; ++k) v += teams[k * (COLS / 4) + q];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[c + j] = v[j];
+            for (int j = 0; j < 4; ++j) out[c + j] = v[j];
         }
         if (threadIdx.x < cols - whole) {
             float v = 0.0f;
 #pragma unroll
             for (int k = 0; k < TEAMS; ++k) v += ltail[which][k][threadIdx.x];
-            part[whole + threadIdx.x] = v;
+            out[whole + threadIdx.x] = v;
         }
     };
     if constexpr (LSUMS == 2) {
