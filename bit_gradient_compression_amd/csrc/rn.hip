@@ -18,12 +18,31 @@ namespace {
 
 __device__ __forceinline__ int chunk_valid(int cols, int c) { return cols - c < 8 ? cols - c : 8; }
 
-// Sum over the WPR waves of a row; every lane gets it.  `slot` alternates between calls so that one
+// Sum over aligned groups of LANES (16, 32 or 64) lanes; every lane gets its group's.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    v += __uint_as_float(dpp<0xB1>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<0x4E>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<0x141>(__float_as_uint(v)));
+    v += __uint_as_float(dpp<0x140>(__float_as_uint(v)));
+    if constexpr (LANES >= 32) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    if constexpr (LANES >= 64) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    return v;
+}
+
+// Sum over the LPT lanes of a row; every lane gets it.  `slot` alternates between calls so that one
 // barrier per call is enough.
-template <int WPR>
+template <int LPT>
 __device__ __forceinline__ float row_sum(float v, float* red, int slot) {
-    v = wave_sum(v);
-    if constexpr (WPR > 1) {
+    v = lanes_sum<LPT < 64 ? LPT : 64>(v);
+    if constexpr (LPT > 64) {
+        constexpr int WPR = LPT / 64;
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) red[slot * WPR + wave] = v;
         __syncthreads();
@@ -41,22 +60,26 @@ __device__ __forceinline__ void fill(float (&v)[8], float x) {
 
 // ---- forward --------------------------------------------------------------------------
 
-// WPR waves per row, NP chunks of eight per lane.
-template <typename T, int WPR, int NP>
-__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void rn_kernel(const RnParams p, int64_t row0) {
-    __shared__ float red[2 * WPR];
-    constexpr int RPW = WPR == 1 ? 4 : 1;  // rows per workgroup
-    constexpr int LANES = WPR * 64;
-    const int64_t row = row0 + (int64_t)blockIdx.x * RPW + (WPR == 1 ? uniform(threadIdx.x >> 6) : 0);
-    if (row >= p.rows) return;  // whole waves (WPR == 1: no barrier follows)
-    const int lane = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
+// LPT lanes per row, NP chunks of eight per lane.
+template <typename T, int LPT, int NP>
+__global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParams p, int64_t row0) {
+    __shared__ float red[LPT <= 64 ? 1 : 2 * LPT / 64];
+    constexpr int LANES = LPT;
+    constexpr int RPW = LPT <= 64 ? 256 / LPT : 1;  // rows per workgroup
+    int64_t row = row0 + (int64_t)blockIdx.x * RPW;
+    if constexpr (LPT == 64) row += uniform(threadIdx.x >> 6);
+    else row += threadIdx.x / LPT;
+    if (LPT >= 64 && row >= p.rows) return;  // whole waves (LPT == 64: no barrier follows)
+    // rows of part of a wave: the others go on, with nothing to read or write
+    const bool here = row < p.rows;
+    const int lane = threadIdx.x % LPT;
     const int cols = p.cols;
     const float inv_cols = 1.0f / (float)cols;
     RawChunk<T> y[NP], res[NP], gate[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = (i * LANES + lane) * 8;
-        const int valid = chunk_valid(cols, c);
+        const int valid = here ? chunk_valid(cols, c) : 0;
         if (p.y) y[i].load((const T*)p.y + row * cols + c, valid);
         if (p.residual) res[i].load((const T*)p.residual + row * cols + c, valid);
         if (p.gate_kind == kGateElement) gate[i].load((const T*)p.gate + row * cols + c, valid);
@@ -71,14 +94,14 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void rn_kernel(const RnP
 #pragma unroll
             for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[j], v[j], sq);
         }
-        rp = 1.0f / __builtin_sqrtf(row_sum<WPR>(sq, red, 0) * inv_cols + p.eps);
-        if (lane == 0) p.post_rstd[row] = rp;
+        rp = 1.0f / __builtin_sqrtf(row_sum<LPT>(sq, red, 0) * inv_cols + p.eps);
+        if (lane == 0 && here) p.post_rstd[row] = rp;
     }
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = (i * LANES + lane) * 8;
-        const int valid = chunk_valid(cols, c);
+        const int valid = here ? chunk_valid(cols, c) : 0;
         fill(h[i], 0.0f);
         if (p.residual) res[i].get(h[i]);
         if (p.y) {
@@ -108,12 +131,12 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void rn_kernel(const RnP
         }
     }
     if (!p.out) return;  // the whole grid
-    const float r = 1.0f / __builtin_sqrtf(row_sum<WPR>(sq, red, 1) * inv_cols + p.eps);
-    if (lane == 0) p.rstd[row] = r;
+    const float r = 1.0f / __builtin_sqrtf(row_sum<LPT>(sq, red, 1) * inv_cols + p.eps);
+    if (lane == 0 && here) p.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = (i * LANES + lane) * 8;
-        const int valid = chunk_valid(cols, c);
+        const int valid = here ? chunk_valid(cols, c) : 0;
         float w[8];
         fill(w, 1.0f);
         if (p.weight) load_chunk_any(p.weight, p.param_f32, c, valid, w);
@@ -132,26 +155,38 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void rn_kernel(const RnP
 }
 
 struct RnShape {
-    int wpr, np;
+    int lpt, np;
 };
-RnShape rn_shape(int64_t cols) {
-    if (cols <= 512) return {1, 1};
-    if (cols <= 1024) return {1, 2};
-    if (cols <= 2048) return {4, 1};
-    if (cols <= 4096) return {4, 2};
-    if (cols <= 8192) return {8, 2};
-    return {8, 4};
+// 16 to 32 bytes of each matrix per lane.  The shape does not depend on the rows, so that a token's bits do
+// not depend on what else is in its batch.  us: 16384 x 4096 in bf16 from y and residual / of the residual
+// alone 98 / 53 with 512 lanes, 99 / 44 with 256, 110 / 51 with 128; one row 3.7, 4.7, 6.6; 8192 x 4096 in fp32
+// 100, 108, 114; 8192 x 8192 in bf16 102 with 1024, 99 with 512, 107 with 256; 4096 x 8192 in fp32 102, 106, 113.
+RnShape rn_shape(int64_t cols, bool f32, bool alone) {
+    if (cols <= 128) return {16, 1};
+    if (cols <= 256) return {32, 1};
+    if (cols <= 512) return {64, 1};
+    if (cols <= 1024) return {64, 2};
+    if (cols <= 2048) return {256, 1};
+    if (cols <= 4096) return f32 || !alone ? RnShape{512, 1} : RnShape{256, 2};
+    if (cols <= 8192) return f32 ? RnShape{1024, 1} : RnShape{512, 2};
+    return {512, 4};
 }
 template <typename T>
 const void* pick_rn(RnShape s) {
-    switch (s.wpr * 16 + s.np) {
-        case 16 + 1: return (const void*)&rn_kernel<T, 1, 1>;
-        case 16 + 2: return (const void*)&rn_kernel<T, 1, 2>;
-        case 64 + 1: return (const void*)&rn_kernel<T, 4, 1>;
-        case 64 + 2: return (const void*)&rn_kernel<T, 4, 2>;
-        case 128 + 2: return (const void*)&rn_kernel<T, 8, 2>;
+    switch (s.lpt * 8 + s.np) {
+        case 16 * 8 + 1: return (const void*)&rn_kernel<T, 16, 1>;
+        case 32 * 8 + 1: return (const void*)&rn_kernel<T, 32, 1>;
+        case 64 * 8 + 1: return (const void*)&rn_kernel<T, 64, 1>;
+        case 64 * 8 + 2: return (const void*)&rn_kernel<T, 64, 2>;
+        case 256 * 8 + 1: return (const void*)&rn_kernel<T, 256, 1>;
+        case 512 * 8 + 1: return (const void*)&rn_kernel<T, 512, 1>;
     }
-    return (const void*)&rn_kernel<T, 8, 4>;
+    if constexpr (sizeof(T) == 4) {
+        if (s.lpt == 1024) return (const void*)&rn_kernel<T, 1024, 1>;
+    } else {
+        if (s.np == 2) return s.lpt == 256 ? (const void*)&rn_kernel<T, 256, 2> : (const void*)&rn_kernel<T, 512, 2>;
+    }
+    return (const void*)&rn_kernel<T, 512, 4>;
 }
 
 // ---- backward -------------------------------------------------------------------------
@@ -218,35 +253,6 @@ struct Piece<float, 8> {
     }
 };
 template <>
-struct Piece<uint16_t, 4> {
-    u32x2 w;
-    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b64(r, i * 2, 0, 0); }
-    __device__ __forceinline__ void get(float (&v)[4]) const {
-        v[0] = bf16_lo(w.x);
-        v[1] = bf16_hi(w.x);
-        v[2] = bf16_lo(w.y);
-        v[3] = bf16_hi(w.y);
-    }
-    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(w)); }
-    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[4]) {
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])}, r, i * 2, 0, 0);
-    }
-};
-template <>
-struct Piece<float, 4> {
-    u32x4 a;
-    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, 0); }
-    __device__ __forceinline__ void get(float (&v)[4]) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(a[j]);
-    }
-    __device__ __forceinline__ void forget() {}
-    static __device__ __forceinline__ void store(Rsrc r, uint32_t i, const float (&v)[4]) {
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                     __float_as_uint(v[3])}, r, i * 4, 0, 0);
-    }
-};
-template <>
 struct Piece<uint16_t, 1> {
     uint32_t w;
     __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b16(r, i * 2, 0, 0); }
@@ -284,13 +290,15 @@ __device__ __forceinline__ void get_param(const void* p, bool f32, uint32_t c0, 
     }
 }
 
-// The part of one row that a lane's piece belongs to: elements at .. at + count of each matrix, columns
-// c0 .. of the parameters.  in: whether the piece, the span's element i on, lies inside.
+// Where a lane's piece lies: element i of a span of `live` elements from `at` on in each matrix (past its
+// end if the piece is not there), element ip of `count` from column c0 on in the parameters.
 struct RowPart {
     int64_t at;
-    uint32_t c0, count, live, i;  // live: count, or 0 for a team without a row
+    uint32_t live, i;
+    uint32_t c0, count, ip;
     bool in;
 };
+constexpr uint32_t kNowhere = 1u << 28;  // past the end of any span
 
 // What the pass reads of a row's W columns, as it lies in memory.
 template <typename T, int W, bool POST, int GATE>
@@ -325,9 +333,9 @@ struct RnBwdPiece {
     float kept[3][KEEP ? W : 1];
 
     __device__ __forceinline__ void keep(const RnBwdParams& p, const RowPart& q) {
-        get_param(p.dout ? p.weight : nullptr, p.param_f32, q.c0, q.count, q.i, kept[0]);
-        if constexpr (POST) get_param(p.post_weight, p.param_f32, q.c0, q.count, q.i, kept[1]);
-        if constexpr (GATE == kGateColumn) get_param(p.gate, p.param_f32, q.c0, q.count, q.i, kept[2]);
+        get_param(p.dout ? p.weight : nullptr, p.param_f32, q.c0, q.count, q.ip, kept[0]);
+        if constexpr (POST) get_param(p.post_weight, p.param_f32, q.c0, q.count, q.ip, kept[1]);
+        if constexpr (GATE == kGateColumn) get_param(p.gate, p.param_f32, q.c0, q.count, q.ip, kept[2]);
     }
     template <int WHICH>
     __device__ __forceinline__ void param(const void* v, const RnBwdParams& p, const RowPart& q, float (&w)[W]) {
@@ -335,7 +343,7 @@ struct RnBwdPiece {
 #pragma unroll
             for (int j = 0; j < W; ++j) w[j] = kept[WHICH][j];
         } else {
-            get_param(v, p.param_f32, q.c0, q.count, q.i, w);
+            get_param(v, p.param_f32, q.c0, q.count, q.ip, w);
         }
     }
     // The sum of dout weight xh.  Outside the row the values are 0, and so has to be r, which may be
@@ -414,26 +422,33 @@ struct RnBwdPiece {
     }
 };
 
-// WPR waves per row, NP pieces of W columns per lane.
+// LPT lanes per row (a team), NP pieces of W columns per lane.  Teams smaller than a wave have consecutive
+// rows, which are one span.
 //
 // In bf16 the next row is on its way while one is worked on.  Loads return in order, so none may follow
 // it: the parameters are kept in registers.  In fp32 those registers would cost a workgroup its place.
-template <typename T, int WPR, int W, int NP, int WAVES, bool POST, int GATE>
-__global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p) {
-    constexpr int TEAMS = WAVES / WPR;
-    constexpr int LANES = WPR * 64;
+template <typename T, int LPT, int W, int NP, int WAVES, bool POST, int GATE>
+__global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(const RnBwdParams p) {
+    constexpr int TEAMS = WAVES * 64 / LPT;
+    constexpr int LANES = LPT;
+    constexpr int SUB = LPT < 64 ? 64 / LPT : 1;   // teams of a wave
+    constexpr int WPR = LPT < 64 ? 1 : LPT / 64;   // waves of a team
     constexpr int COLS = NP * LANES * W;
     constexpr int Q = W / 4;  // fours of columns per piece
-    // Two chunks per lane do not fit: h, dout and y are read again for the phase that needs them, from the caches.
-    constexpr bool ONCE = NP == 1;
-    constexpr bool AHEAD = ONCE && sizeof(T) == 2;
+    // Two pieces of fp32 per lane do not fit: h, dout and y are read again for the phase that needs them, from
+    // the caches.
+    constexpr bool ONCE = NP == 1 || sizeof(T) == 2;
+    constexpr bool AHEAD = NP == 1 && sizeof(T) == 2;
     constexpr int LSUMS = POST || GATE == kGateColumn ? 2 : 1;  // the join needs one
     __shared__ float red[2][2][WAVES];
     __shared__ float ltail[3][TEAMS][8];
     // [which][team][COLS], a lane's four columns together: column W (i LANES + lane) + 4 q + j at
     // ((Q i + q) LANES + lane) 4 + j, free of bank conflicts
     __shared__ f32x4 lsum[LSUMS * TEAMS * COLS / 4];
-    const int wave = uniform(threadIdx.x >> 6), team = wave / WPR;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int first_team = wave * SUB / WPR;  // of the wave
+    const uint32_t sub = SUB > 1 ? (threadIdx.x & 63) / LPT : 0;
+    const int team = first_team + (int)sub;
     const int lane = threadIdx.x - team * LANES;
     const uint32_t cols = p.cols, whole = cols & ~(W - 1u);
     const float inv_cols = 1.0f / (float)p.cols;
@@ -455,7 +470,7 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
     }
     // Sum over the row's waves; the two slots of a turn and the turns' flip keep one barrier enough.
     auto team_sum = [&](float v, int flip, int slot) {
-        v = wave_sum(v);
+        v = lanes_sum<LPT < 64 ? LPT : 64>(v);
         if constexpr (WPR > 1) {
             if ((threadIdx.x & 63) == 0) red[flip][slot][wave] = v;
             __syncthreads();
@@ -465,14 +480,23 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
         }
         return v * inv_cols;
     };
+    // Of the wave's first row `row`.
+    auto rows_here = [&](int64_t row) {
+        const int64_t left = p.rows - row;
+        return left <= 0 ? 0u : left < SUB ? (uint32_t)left : (uint32_t)SUB;
+    };
     auto part = [&](int64_t row, int i) {
-        const bool here = row < p.rows;
-        const uint32_t c = (uint32_t)(i * LANES + lane) * W;
-        return RowPart{row * cols, 0, whole, here ? whole : 0u, c, here && c < whole};
+        const uint32_t n = rows_here(row), c = (uint32_t)(i * LANES + lane) * W;
+        const bool in = sub < n && c < whole;
+        if constexpr (SUB > 1) return RowPart{row * cols, n * cols, in ? sub * cols + c : kNowhere, 0, whole, c, in};
+        else return RowPart{row * cols, n * whole, c, 0, whole, c, in};
     };
     auto rest = [&](int64_t row) {
-        const bool here = row < p.rows;
-        return RowPart{row * cols + whole, whole, cols - whole, here ? cols - whole : 0u, (uint32_t)lane, here && tailed};
+        const uint32_t n = rows_here(row), tail_cols = cols - whole;
+        const bool in = sub < n && tailed;
+        if constexpr (SUB > 1)
+            return RowPart{row * cols, n * cols, in ? sub * cols + whole + lane : kNowhere, whole, tail_cols, (uint32_t)lane, in};
+        else return RowPart{row * cols + whole, n * tail_cols, (uint32_t)lane, whole, tail_cols, (uint32_t)lane, in};
     };
     // What a row brings with it.
     struct Row {
@@ -481,9 +505,9 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
         float r, rp;
     };
     auto load_row = [&](Row& o, int64_t row) {
-        const bool here = row < p.rows;
-        o.r = here && p.dout ? p.rstd[row] : 0.0f;
-        o.rp = !POST ? 1.0f : here ? p.post_rstd[row] : 0.0f;
+        const bool here = sub < rows_here(row);
+        o.r = here && p.dout ? p.rstd[row + sub] : 0.0f;
+        o.rp = !POST ? 1.0f : here ? p.post_rstd[row + sub] : 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             o.x[i].load_first(p, part(row, i));
@@ -495,7 +519,7 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
         }
     };
     const int64_t step = (int64_t)gridDim.x * TEAMS;
-    int64_t row = (int64_t)blockIdx.x * TEAMS + team;
+    int64_t row = (int64_t)blockIdx.x * TEAMS + first_team;
     Row cur;
     if constexpr (AHEAD) {
         pc[0].keep(p, part(0, 0));
@@ -503,7 +527,7 @@ __global__ __launch_bounds__(WAVES * 64) void rn_bwd_kernel(const RnBwdParams p)
         load_row(cur, row);
     }
     // every team takes part in every turn's barriers, with or without a row
-    for (int flip = 0; row - team < p.rows; row += step, flip ^= 1) {
+    for (int flip = 0; row - first_team < p.rows; row += step, flip ^= 1) {
         Row next;
         if constexpr (AHEAD) load_row(next, row + step);
         else load_row(cur, row);
@@ -623,43 +647,46 @@ __global__ __launch_bounds__(1024) void rn_bwd_join_kernel(const RnBwdParams p, 
 }
 
 struct RnBwdShape {
-    int wpr, np, waves, groups;  // groups: the workgroups that are at work at once
+    int lpt, waves, groups;  // groups: the workgroups that are at work at once
 };
 RnBwdShape rn_bwd_shape(int64_t cols) {
-    if (cols <= 512) return {1, 1, 8, 512};
-    if (cols <= 1024) return {2, 1, 8, 512};
-    if (cols <= 2048) return {4, 1, 8, 512};
-    if (cols <= 4096) return {8, 1, 8, 512};
-    if (cols <= 8192) return {16, 1, 16, 256};
-    return {8, 8, 8, 256};
+    if (cols <= 128) return {16, 4, 768};
+    if (cols <= 256) return {32, 4, 768};
+    if (cols <= 512) return {64, 8, 512};
+    if (cols <= 1024) return {128, 8, 512};
+    if (cols <= 2048) return {256, 8, 512};
+    if (cols <= 4096) return {512, 8, 512};
+    return {1024, 16, 256};
 }
 template <typename T, bool POST, int GATE>
-const void* pick_rn_bwd_shape(RnBwdShape s) {
-    switch (s.wpr * 16 + s.np) {
-        case 16 + 1: return (const void*)&rn_bwd_kernel<T, 1, 8, 1, 8, POST, GATE>;
-        case 32 + 1: return (const void*)&rn_bwd_kernel<T, 2, 8, 1, 8, POST, GATE>;
-        case 64 + 1: return (const void*)&rn_bwd_kernel<T, 4, 8, 1, 8, POST, GATE>;
-        case 128 + 1: return (const void*)&rn_bwd_kernel<T, 8, 8, 1, 8, POST, GATE>;
-        case 256 + 1: return (const void*)&rn_bwd_kernel<T, 16, 8, 1, 16, POST, GATE>;
+const void* pick_rn_bwd_shape(int64_t cols) {
+    switch (rn_bwd_shape(cols).lpt) {
+        case 16: return (const void*)&rn_bwd_kernel<T, 16, 8, 1, 4, POST, GATE>;
+        case 32: return (const void*)&rn_bwd_kernel<T, 32, 8, 1, 4, POST, GATE>;
+        case 64: return (const void*)&rn_bwd_kernel<T, 64, 8, 1, 8, POST, GATE>;
+        case 128: return (const void*)&rn_bwd_kernel<T, 128, 8, 1, 8, POST, GATE>;
+        case 256: return (const void*)&rn_bwd_kernel<T, 256, 8, 1, 8, POST, GATE>;
+        case 512: return (const void*)&rn_bwd_kernel<T, 512, 8, 1, 8, POST, GATE>;
     }
-    return (const void*)&rn_bwd_kernel<T, 8, 4, 8, 8, POST, GATE>;
+    return cols <= 8192 ? (const void*)&rn_bwd_kernel<T, 1024, 8, 1, 16, POST, GATE>
+                        : (const void*)&rn_bwd_kernel<T, 1024, 8, 2, 16, POST, GATE>;
 }
 template <typename T, bool POST>
-const void* pick_rn_bwd_gate(RnBwdShape s, int gate) {
+const void* pick_rn_bwd_gate(int64_t s, int gate) {
     return gate == kGateNone     ? pick_rn_bwd_shape<T, POST, kGateNone>(s)
            : gate == kGateColumn ? pick_rn_bwd_shape<T, POST, kGateColumn>(s)
                                  : pick_rn_bwd_shape<T, POST, kGateElement>(s);
 }
 template <typename T>
-const void* pick_rn_bwd(RnBwdShape s, bool post, int gate) {
+const void* pick_rn_bwd(int64_t s, bool post, int gate) {
     return post ? pick_rn_bwd_gate<T, true>(s, gate) : pick_rn_bwd_gate<T, false>(s, gate);
 }
 
 }  // namespace
 
 hipError_t launch_rn(const RnParams& p, hipStream_t stream) {
-    const RnShape s = rn_shape(p.cols);
-    const int rpw = s.wpr == 1 ? 4 : 1, threads = s.wpr == 1 ? 256 : s.wpr * 64;
+    const RnShape s = rn_shape(p.cols, p.f32, !p.y);
+    const int rpw = s.lpt <= 64 ? 256 / s.lpt : 1, threads = s.lpt <= 64 ? 256 : s.lpt;
     const void* k = p.f32 ? pick_rn<float>(s) : pick_rn<uint16_t>(s);
     for (int64_t row0 = 0; row0 < p.rows; row0 += kMaxGrid * rpw) {
         const int64_t rows = p.rows - row0 < kMaxGrid * rpw ? p.rows - row0 : kMaxGrid * rpw;
@@ -673,7 +700,7 @@ hipError_t launch_rn(const RnParams& p, hipStream_t stream) {
 
 int64_t rn_bwd_groups(int64_t rows, int64_t cols) {
     const RnBwdShape s = rn_bwd_shape(cols);
-    const int64_t teams = s.waves / s.wpr, wanted = (rows + teams - 1) / teams;
+    const int64_t teams = s.waves * 64 / s.lpt, wanted = (rows + teams - 1) / teams;
     return wanted < 1 ? 1 : wanted < s.groups ? wanted : s.groups;
 }
 
@@ -681,7 +708,7 @@ hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream) {
     const RnBwdShape s = rn_bwd_shape(p.cols);
     const int64_t groups = rn_bwd_groups(p.rows, p.cols);
     const bool post = p.post_rstd != nullptr;
-    const void* k = p.f32 ? pick_rn_bwd<float>(s, post, p.gate_kind) : pick_rn_bwd<uint16_t>(s, post, p.gate_kind);
+    const void* k = p.f32 ? pick_rn_bwd<float>(p.cols, post, p.gate_kind) : pick_rn_bwd<uint16_t>(p.cols, post, p.gate_kind);
     void* args[] = {(void*)&p};
     hipError_t err = hipLaunchKernel(k, dim3((unsigned)groups), dim3(s.waves * 64), args, 0, stream);
     if (err != hipSuccess || !p.part) return err;
