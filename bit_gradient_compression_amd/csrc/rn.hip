@@ -364,59 +364,60 @@ struct RnBwdPiece {
         x.dout.forget();
     }
     // dresidual and what follows from it; the sums over the rows of the gate's and the post-norm's
-    // gradients are added by `add`.
+    // gradients are added by `add`.  Outside the row all values are 0, and the row's factors are made so.
     template <typename Add>
     __device__ __forceinline__ void second(Raw& x, const RnBwdParams& p, const RowPart& q, float r, float s, float rp,
                                            float& s2, Add add) {
         float w[W], v[W], g[W];
+        const float rc = q.in ? r : 0.0f, rs = q.in ? r * s : 0.0f;
         param<0>(p.dout ? p.weight : nullptr, p, q, w);
         x.h.get(v);
         x.dout.get(g);
 #pragma unroll
-        for (int j = 0; j < W; ++j) g[j] = (g[j] * w[j] - v[j] * r * s) * r;  // 0 without dout, whose r is 0
+        for (int j = 0; j < W; ++j) g[j] = __builtin_fmaf(-v[j], rs, g[j] * w[j]);
         x.dh.get(v);
 #pragma unroll
-        for (int j = 0; j < W; ++j) g[j] += v[j];
+        for (int j = 0; j < W; ++j) g[j] = __builtin_fmaf(g[j], rc, v[j]);  // dh without dout, whose r is 0
         if (p.dresidual) P::store(span_of<T>(p.dresidual, q.at, q.live), q.i, g);
 #pragma unroll
-        for (int j = 0; j < W; ++j) t[j] = q.in ? g[j] * p.scale : 0.0f;
+        for (int j = 0; j < W; ++j) t[j] = g[j] * p.scale;
         if constexpr (POST || GATE != kGateNone) {
-            float yh[W];
-            x.y.get(yh);
-            const float rc = q.in ? rp : 0.0f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) yh[j] *= rc;
+            float k[W];
+            if constexpr (GATE == kGateElement) x.gate.get(k);
+            if constexpr (GATE == kGateColumn) param<2>(p.gate, p, q, k);
             if constexpr (POST) param<1>(p.post_weight, p, q, w);
+            x.y.get(v);
+            const float yc = q.in ? rp : 0.0f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) g[j] = t[j] * (v[j] * yc);  // times yh
             if constexpr (GATE != kGateNone) {
-                float k[W];
-                if constexpr (GATE == kGateElement) x.gate.get(k);
-                else param<2>(p.gate, p, q, k);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    v[j] = t[j] * (POST ? yh[j] * w[j] : yh[j]);
+                    v[j] = POST ? g[j] * w[j] : g[j];
                     t[j] *= k[j];
+                    g[j] *= k[j];
                 }
                 if constexpr (GATE == kGateColumn) add(1, v);
                 else if (p.dgate_rows) P::store(span_of<T>(p.dgate_rows, q.at, q.live), q.i, v);
             }
             if constexpr (POST) {
+                add(0, g);
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
-                    v[j] = t[j] * yh[j];
-                    s2 = __builtin_fmaf(v[j], w[j], s2);
+                    s2 = __builtin_fmaf(g[j], w[j], s2);
                     t[j] *= w[j];
                 }
-                add(0, v);
                 x.y.forget();
             }
         }
     }
     __device__ __forceinline__ void third(const Raw& x, const RnBwdParams& p, const RowPart& q, float rp, float s2) {
         if constexpr (POST) {
-            float yh[W];
-            x.y.get(yh);
+            float y[W];
+            x.y.get(y);
+            const float ys = rp * s2;
 #pragma unroll
-            for (int j = 0; j < W; ++j) t[j] = (t[j] - yh[j] * rp * s2) * rp;
+            for (int j = 0; j < W; ++j) t[j] = __builtin_fmaf(-y[j], ys, t[j]) * rp;
         }
         P::store(span_of<T>(p.dy, q.at, q.live), q.i, t);
     }
@@ -515,7 +516,7 @@ __global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(co
         }
         if (whole != cols) {
             o.tail.load_first(p, rest(row));
-            o.tail.load_rest(p, rest(row));
+            if (ONCE) o.tail.load_rest(p, rest(row));
         }
     };
     const int64_t step = (int64_t)gridDim.x * TEAMS;
@@ -558,8 +559,16 @@ __global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(co
                         f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
             });
         }
-        if (whole != cols)
-            tail.second(cur.tail, p, rest(row), r, s, rp, s2, [&](int which, const float(&v)[1]) { tsum[which] += v[0]; });
+        if (whole != cols) {
+            RowPart q = rest(row);
+            if (!ONCE) {
+                __builtin_amdgcn_sched_barrier(0);
+                asm volatile("" : "+v"(q.i));
+                cur.tail.load_first(p, q);
+                cur.tail.load_rest(p, q);
+            }
+            tail.second(cur.tail, p, q, r, s, rp, s2, [&](int which, const float(&v)[1]) { tsum[which] += v[0]; });
+        }
         if constexpr (POST) s2 = team_sum(s2, flip, 1);
         if (p.dy) {
 #pragma unroll
@@ -572,7 +581,14 @@ __global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(co
                 }
                 pc[i].third(cur.x[i], p, q, rp, s2);
             }
-            if (whole != cols) tail.third(cur.tail, p, rest(row), rp, s2);
+            if (whole != cols) {
+                RowPart q = rest(row);
+                if (!ONCE) {
+                    asm volatile("" : "+v"(q.i));
+                    cur.tail.load_y(p, q);
+                }
+                tail.third(cur.tail, p, q, rp, s2);
+            }
         }
         if constexpr (AHEAD) cur = next;
     }
@@ -655,7 +671,7 @@ RnBwdShape rn_bwd_shape(int64_t cols) {
     if (cols <= 512) return {64, 8, 512};
     if (cols <= 1024) return {128, 8, 512};
     if (cols <= 2048) return {256, 8, 512};
-    if (cols <= 4096) return {512, 8, 512};
+    if (cols <= 4096) return {512, 16, 256};
     return {1024, 16, 256};
 }
 template <typename T, bool POST, int GATE>
@@ -666,7 +682,7 @@ const void* pick_rn_bwd_shape(int64_t cols) {
         case 64: return (const void*)&rn_bwd_kernel<T, 64, 8, 1, 8, POST, GATE>;
         case 128: return (const void*)&rn_bwd_kernel<T, 128, 8, 1, 8, POST, GATE>;
         case 256: return (const void*)&rn_bwd_kernel<T, 256, 8, 1, 8, POST, GATE>;
-        case 512: return (const void*)&rn_bwd_kernel<T, 512, 8, 1, 8, POST, GATE>;
+        case 512: return (const void*)&rn_bwd_kernel<T, 512, 8, 1, 16, POST, GATE>;
     }
     return cols <= 8192 ? (const void*)&rn_bwd_kernel<T, 1024, 8, 1, 16, POST, GATE>
                         : (const void*)&rn_bwd_kernel<T, 1024, 8, 2, 16, POST, GATE>;
