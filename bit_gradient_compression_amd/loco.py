@@ -835,6 +835,19 @@ def _table(n, dev):
     return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}") if nbytes else None
 
 
+def _described(table, stream, dev):
+    """Waits until the description is in the table: a step on another stream may follow at once, and would
+    take what it read before for addresses."""
+    if table is None:
+        return
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("describe the tensors before a graph is captured: the table is filled on the device")
+    if stream is None:
+        torch.cuda.current_stream(dev).synchronize()
+    else:
+        (stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)).synchronize()
+
+
 def _held_for(table, stream, dev):
     """The stream to call on; the table's memory is not used again before that stream is past it."""
     if stream is not None and table is not None:
@@ -851,10 +864,10 @@ class AdamwTensors:
     param, every grad and every state of one kind.  param_bf16 (or None) receives the bfloat16 copy
     of a float32 param.  weight_decay is that of the tensors that do not give one.  The memory of
     the tensors is kept alive and must not be resized; later calls use it as it is now, on the
-    device that is current now.  The description goes to the device on `stream` (the current one if
-    None): a call on another stream has to wait for that."""
+    device that is current now.  The description is on the device when the constructor returns; it
+    cannot be made while a graph is captured."""
 
-    def __init__(self, tensors, *, block: int = 256, weight_decay: float = 0.0, stream=None):
+    def __init__(self, tensors, *, block: int = 256, weight_decay: float = 0.0, stream=None, _wait: bool = True):
         self.device, self.block = _device(), block
         dev, rows, keep = self.device, [], []
         self.param_dtype = self.grad_dtype = self.bits = None
@@ -887,6 +900,8 @@ class AdamwTensors:
                                     _CODES.get(self.grad_dtype, LOCO_F32), self.bits or 32, block, _ptr(table, dev),
                                     _nbytes(table), ctypes.byref(self.plan), _held_for(table, stream, dev))
         _check("loco_adamw_plan", st)
+        if _wait:
+            _described(table, stream, dev)
 
 
 def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -898,7 +913,7 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
     repeats them."""
     if not isinstance(tensors, AdamwTensors):
         tensors = AdamwTensors(tensors, block=256 if block is None else block, weight_decay=weight_decay or 0.0,
-                               stream=stream)
+                               stream=stream, _wait=False)
     elif block is not None or weight_decay is not None:
         raise ValueError("an AdamwTensors has its own block and weight_decay")
     dev = _device()
@@ -914,9 +929,9 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
 class AdamwStates:
     """8-bit states and the tensors of their values, checked and described once.  states: an
     iterable of ((codes, exps), values), values float32 or bfloat16, all alike; codes in
-    float8_e4m3fn are a first moment, in uint8 a second one.  Memory and stream as in AdamwTensors."""
+    float8_e4m3fn are a first moment, in uint8 a second one.  Memory and device as in AdamwTensors."""
 
-    def __init__(self, states, *, block: int = 256, stream=None):
+    def __init__(self, states, *, block: int = 256, stream=None, _wait: bool = True):
         self.device, self.block, self.dtype = _device(), block, None
         dev, rows, keep = self.device, [], []
         for i, ((codes, exps), values) in enumerate(states):
@@ -936,11 +951,13 @@ class AdamwStates:
         st = load().loco_adamw_state_plan(array, count, block, _CODES.get(self.dtype, LOCO_F32), _ptr(table, dev),
                                           _nbytes(table), ctypes.byref(self.plan), _held_for(table, stream, dev))
         _check("loco_adamw_state_plan", st)
+        if _wait:
+            _described(table, stream, dev)
 
 
 def _adamw_states(name, states, block, stream):
     if not isinstance(states, AdamwStates):
-        states = AdamwStates(states, block=256 if block is None else block, stream=stream)
+        states = AdamwStates(states, block=256 if block is None else block, stream=stream, _wait=False)
     elif block is not None:
         raise ValueError("an AdamwStates has its own block")
     dev = _device()

@@ -292,3 +292,33 @@ def test_memory_is_kept_by_the_description(gpu_lib):
     assert other.data_ptr() != where
     gpu_lib.adamw(kept, **HP)
     assert bool((m != 0).all())
+
+
+def test_description_and_streams(gpu_lib):
+    """A description made on one stream is there for a step on another that waits for nothing else; it
+    cannot be made while a graph is captured, but a plain list can be stepped there."""
+    a, b = (Tensor(12, 3000, BF, BF, 8, 64, False) for _ in range(2))
+    torch.cuda.synchronize()
+    busy, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(busy):
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            big = big @ big * 1e-2
+        ta = gpu_lib.AdamwTensors([a.args(0.1)], block=64)
+    gpu_lib.adamw(ta, stream=side, **HP)
+    gpu_lib.adamw([b.args(0.1)], block=64, stream=side.cuda_stream, **HP)
+    side.synchronize()
+    for x, y in zip((a.p, a.m, a.v, a.me), (b.p, b.m, b.v, b.me)):
+        assert np.array_equal(bits(x.t), bits(y.t))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gpu_lib.adamw([a.args(0.1)], block=64, **HP)
+        with pytest.raises(RuntimeError, match="captured"):
+            gpu_lib.AdamwTensors([b.args(0.1)], block=64)
+    for _ in range(3):
+        graph.replay()
+        gpu_lib.adamw([b.args(0.1)], block=64, **HP)
+        torch.cuda.synchronize()
+        for x, y in zip((a.p, a.m, a.v), (b.p, b.m, b.v)):
+            assert np.array_equal(bits(x.t), bits(y.t))
