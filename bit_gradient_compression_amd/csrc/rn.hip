@@ -60,8 +60,16 @@ __device__ __forceinline__ void fill(float (&v)[8], float x) {
 
 // ---- forward --------------------------------------------------------------------------
 
-// LPT lanes per row, NP chunks of eight per lane.
-template <typename T, int LPT, int NP>
+// 1 / sqrt(x), within an ulp as the hardware's is.  That takes normal numbers only.
+__device__ __forceinline__ float inv_root(float x) {
+    const bool small = x < 0x1p-96f;
+    return __builtin_amdgcn_rsqf(small ? x * 0x1p64f : x) * (small ? 0x1p32f : 1.0f);
+}
+
+// LPT lanes per row, NP chunks of eight per lane.  WHOLE: rows are whole chunks, and a lane has all of a
+// chunk or nothing.  Past a row's end every value is 0 and stays it: a norm's factor, which may be infinite,
+// is made 0 there.
+template <typename T, int LPT, int NP, bool WHOLE>
 __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParams p, int64_t row0) {
     __shared__ float red[LPT <= 64 ? 1 : 2 * LPT / 64];
     constexpr int LANES = LPT;
@@ -75,11 +83,12 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
     const int lane = threadIdx.x % LPT;
     const int cols = p.cols;
     const float inv_cols = 1.0f / (float)cols;
+    const auto valid_at = [&](int c) { return !here ? 0 : !WHOLE ? chunk_valid(cols, c) : c < cols ? 8 : 0; };
     RawChunk<T> y[NP], res[NP], gate[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = (i * LANES + lane) * 8;
-        const int valid = here ? chunk_valid(cols, c) : 0;
+        const int valid = valid_at(c);
         if (p.y) y[i].load((const T*)p.y + row * cols + c, valid);
         if (p.residual) res[i].load((const T*)p.residual + row * cols + c, valid);
         if (p.gate_kind == kGateElement) gate[i].load((const T*)p.gate + row * cols + c, valid);
@@ -94,14 +103,14 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
 #pragma unroll
             for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[j], v[j], sq);
         }
-        rp = 1.0f / __builtin_sqrtf(row_sum<LPT>(sq, red, 0) * inv_cols + p.eps);
+        rp = inv_root(row_sum<LPT>(sq, red, 0) * inv_cols + p.eps);
         if (lane == 0 && here) p.post_rstd[row] = rp;
     }
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = (i * LANES + lane) * 8;
-        const int valid = here ? chunk_valid(cols, c) : 0;
+        const int valid = valid_at(c);
         fill(h[i], 0.0f);
         if (p.residual) res[i].get(h[i]);
         if (p.y) {
@@ -118,30 +127,27 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
                 fill(w, 1.0f);
                 if (p.post_weight) load_chunk_any(p.post_weight, p.param_f32, c, valid, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * rp * w[j];
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * (WHOLE ? valid ? rp : 0.0f : j < valid ? rp : 0.0f) * w[j];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[i][j] = __builtin_fmaf(k[j], v[j], h[i][j]);
         }
         if (p.h) store_chunk((T*)p.h + row * cols + c, valid, h[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            h[i][j] = j < valid ? h[i][j] : 0.0f;  // past the end 0 * rp may be a NaN
-            sq = __builtin_fmaf(h[i][j], h[i][j], sq);
-        }
+        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(h[i][j], h[i][j], sq);
     }
     if (!p.out) return;  // the whole grid
-    const float r = 1.0f / __builtin_sqrtf(row_sum<LPT>(sq, red, 1) * inv_cols + p.eps);
+    const float r = inv_root(row_sum<LPT>(sq, red, 1) * inv_cols + p.eps);
     if (lane == 0 && here) p.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int c = (i * LANES + lane) * 8;
-        const int valid = here ? chunk_valid(cols, c) : 0;
+        const int valid = valid_at(c);
         float w[8];
         fill(w, 1.0f);
         if (p.weight) load_chunk_any(p.weight, p.param_f32, c, valid, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < valid ? h[i][j] * r * w[j] : 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = h[i][j] * (WHOLE ? valid ? r : 0.0f : j < valid ? r : 0.0f) * w[j];
         store_chunk((T*)p.out + row * cols + c, valid, v);
         if (p.ckpt.codes) {
             // of the fp32 values, before their rounding to the output's type
@@ -171,22 +177,22 @@ RnShape rn_shape(int64_t cols, bool f32, bool alone) {
     if (cols <= 8192) return f32 ? RnShape{1024, 1} : RnShape{512, 2};
     return {512, 4};
 }
-template <typename T>
+template <typename T, bool WHOLE>
 const void* pick_rn(RnShape s) {
     switch (s.lpt * 8 + s.np) {
-        case 16 * 8 + 1: return (const void*)&rn_kernel<T, 16, 1>;
-        case 32 * 8 + 1: return (const void*)&rn_kernel<T, 32, 1>;
-        case 64 * 8 + 1: return (const void*)&rn_kernel<T, 64, 1>;
-        case 64 * 8 + 2: return (const void*)&rn_kernel<T, 64, 2>;
-        case 256 * 8 + 1: return (const void*)&rn_kernel<T, 256, 1>;
-        case 512 * 8 + 1: return (const void*)&rn_kernel<T, 512, 1>;
+        case 16 * 8 + 1: return (const void*)&rn_kernel<T, 16, 1, WHOLE>;
+        case 32 * 8 + 1: return (const void*)&rn_kernel<T, 32, 1, WHOLE>;
+        case 64 * 8 + 1: return (const void*)&rn_kernel<T, 64, 1, WHOLE>;
+        case 64 * 8 + 2: return (const void*)&rn_kernel<T, 64, 2, WHOLE>;
+        case 256 * 8 + 1: return (const void*)&rn_kernel<T, 256, 1, WHOLE>;
+        case 512 * 8 + 1: return (const void*)&rn_kernel<T, 512, 1, WHOLE>;
     }
     if constexpr (sizeof(T) == 4) {
-        if (s.lpt == 1024) return (const void*)&rn_kernel<T, 1024, 1>;
+        if (s.lpt == 1024) return (const void*)&rn_kernel<T, 1024, 1, WHOLE>;
     } else {
-        if (s.np == 2) return s.lpt == 256 ? (const void*)&rn_kernel<T, 256, 2> : (const void*)&rn_kernel<T, 512, 2>;
+        if (s.np == 2) return s.lpt == 256 ? (const void*)&rn_kernel<T, 256, 2, WHOLE> : (const void*)&rn_kernel<T, 512, 2, WHOLE>;
     }
-    return (const void*)&rn_kernel<T, 512, 4>;
+    return (const void*)&rn_kernel<T, 512, 4, WHOLE>;
 }
 
 // ---- backward -------------------------------------------------------------------------
@@ -703,7 +709,8 @@ const void* pick_rn_bwd(int64_t s, bool post, int gate) {
 hipError_t launch_rn(const RnParams& p, hipStream_t stream) {
     const RnShape s = rn_shape(p.cols, p.f32, !p.y);
     const int rpw = s.lpt <= 64 ? 256 / s.lpt : 1, threads = s.lpt <= 64 ? 256 : s.lpt;
-    const void* k = p.f32 ? pick_rn<float>(s) : pick_rn<uint16_t>(s);
+    const void* k = p.cols % 8 == 0 ? (p.f32 ? pick_rn<float, true>(s) : pick_rn<uint16_t, true>(s))
+                                    : (p.f32 ? pick_rn<float, false>(s) : pick_rn<uint16_t, false>(s));
     for (int64_t row0 = 0; row0 < p.rows; row0 += kMaxGrid * rpw) {
         const int64_t rows = p.rows - row0 < kMaxGrid * rpw ? p.rows - row0 : kMaxGrid * rpw;
         void* args[] = {(void*)&p, (void*)&row0};
