@@ -16,8 +16,6 @@ namespace loco {
 
 namespace {
 
-__device__ __forceinline__ int chunk_valid(int cols, int c) { return cols - c < 8 ? cols - c : 8; }
-
 // Sum over aligned groups of LANES (16, 32 or 64) lanes; every lane gets its group's.
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -60,6 +58,152 @@ __device__ __forceinline__ void fill(float (&v)[8], float x) {
 
 // ---- forward --------------------------------------------------------------------------
 
+// Where a lane's chunk lies in a row: `valid` elements, 0 to 8, from column c on.  WHOLE: all of a chunk or
+// nothing.  Else a chunk of which less than all exists is read as the row's last eight elements (`at`), of which
+// `shift` are dropped when they are there: element by element, or in parts that are put together where they are
+// loaded, one matrix waited for the one before it (16384 x 4095 in bf16 with a checkpoint 236 and 176 us, so
+// 149; 8192 x 4095 in fp32 109, 114 and 107; only a last chunk alone in its wave is slower, 4097 in fp32 116, 117
+// and 136).  What is dropped another lane may be writing, where a call works in place.
+struct Place {
+    int c, at, valid, shift;
+};
+template <bool WHOLE>
+__device__ __forceinline__ Place place_of(int c, int cols, bool here) {
+    const int valid = !here || c >= cols ? 0 : WHOLE || cols - c >= 8 ? 8 : cols - c;
+    const int at = WHOLE || valid == 8 || cols < 8 ? c : cols - 8;
+    return {c, at, valid, WHOLE || valid == 0 ? 0 : c - at};
+}
+
+// A chunk as it lies in memory; elements that do not exist are 0 after `fix`.
+template <typename T, bool WHOLE>
+struct RowChunk;
+template <bool WHOLE>
+struct RowChunk<uint16_t, WHOLE> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t* row, int cols, const Place& q) {
+        w = u32x4{0u, 0u, 0u, 0u};
+        if (!WHOLE && cols < 8) {
+            if (q.valid)
+                for (int j = 0; j < cols; ++j) {
+                    const uint32_t x = (uint32_t)row[j] << (16 * (j & 1));
+                    w.x |= j < 2 ? x : 0u;
+                    w.y |= j >> 1 == 1 ? x : 0u;
+                    w.z |= j >> 1 == 2 ? x : 0u;
+                    w.w |= j >> 1 == 3 ? x : 0u;
+                }
+        } else if (q.valid) {
+            w = load16(row + q.at);
+        }
+    }
+    __device__ __forceinline__ void fix(const Place& q) {
+        if (!WHOLE && q.shift) {
+            if (q.shift & 4) w = u32x4{w.z, w.w, 0u, 0u};
+            if (q.shift & 2) w = u32x4{w.y, w.z, w.w, 0u};
+            if (q.shift & 1)
+                w = u32x4{w.x >> 16 | w.y << 16, w.y >> 16 | w.z << 16, w.z >> 16 | w.w << 16, w.w >> 16};
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(w, v); }
+    static __device__ __forceinline__ void store(uint16_t* row, const Place& q, const float (&v)[8]) {
+        uint16_t* p = row + q.c;
+        const u32x4 x = pack_bf16x8(v);
+        if (q.valid == 8) {
+            store16(p, x);
+        } else if (!WHOLE && q.valid > 0) {
+            const uint32_t r0 = q.valid & 4 ? x[2] : x[0], r1 = q.valid & 4 ? x[3] : x[1];
+            const u32x2 four = {x[0], x[1]};
+            if (q.valid & 4) __builtin_memcpy(p, &four, 8);
+            if (q.valid & 2) __builtin_memcpy(p + (q.valid & 4), &r0, 4);
+            if (q.valid & 1) p[q.valid & 6] = (uint16_t)(q.valid & 2 ? r1 : r0);
+        }
+    }
+};
+template <bool WHOLE>
+struct RowChunk<float, WHOLE> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float* row, int cols, const Place& q) {
+        a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!WHOLE && cols < 8) {
+            if (q.valid)
+                for (int j = 0; j < cols; ++j) {
+                    const float x = row[j];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        a[k] = j == k ? x : a[k];
+                        b[k] = j == 4 + k ? x : b[k];
+                    }
+                }
+        } else if (q.valid) {
+            __builtin_memcpy(&a, row + q.at, 16);
+            __builtin_memcpy(&b, row + q.at + 4, 16);
+        }
+    }
+    __device__ __forceinline__ void fix(const Place& q) {
+        if (!WHOLE && q.shift) {
+            if (q.shift & 4) {
+                a = b;
+                b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            if (q.shift & 2) {
+                a = f32x4{a[2], a[3], b[0], b[1]};
+                b = f32x4{b[2], b[3], 0.0f, 0.0f};
+            }
+            if (q.shift & 1) {
+                a = f32x4{a[1], a[2], a[3], b[0]};
+                b = f32x4{b[1], b[2], b[3], 0.0f};
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    }
+    static __device__ __forceinline__ void store(float* row, const Place& q, const float (&v)[8]) {
+        float* p = row + q.c;
+        const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        if (q.valid == 8) {
+            __builtin_memcpy(p, &a, 16);
+            __builtin_memcpy(p + 4, &b, 16);
+        } else if (!WHOLE && q.valid > 0) {
+            const f32x4 r = q.valid & 4 ? b : a;
+            const float two[2] = {r[0], r[1]};
+            if (q.valid & 4) __builtin_memcpy(p, &a, 16);
+            if (q.valid & 2) __builtin_memcpy(p + (q.valid & 4), two, 8);
+            if (q.valid & 1) p[q.valid & 6] = q.valid & 2 ? r[2] : r[0];
+        }
+    }
+};
+// The same of a parameter vector, whose type is known at run time only.
+template <bool WHOLE>
+__device__ __forceinline__ void get_chunk(const void* base, bool f32, int cols, const Place& q, float (&v)[8]) {
+    if (f32) {
+        RowChunk<float, WHOLE> x;
+        x.load((const float*)base, cols, q);
+        x.fix(q);
+        x.get(v);
+    } else {
+        RowChunk<uint16_t, WHOLE> x;
+        x.load((const uint16_t*)base, cols, q);
+        x.fix(q);
+        x.get(v);
+    }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store_row_codes(int8_t* p, int valid, u32x2 w) {
+    if (valid == 8) {
+        stream8(p, w);
+    } else if (!WHOLE && valid > 0) {
+        const uint32_t four = w.x, r = valid & 4 ? w.y : w.x;
+        const uint16_t two = (uint16_t)r;
+        if (valid & 4) __builtin_memcpy(p, &four, 4);
+        if (valid & 2) __builtin_memcpy(p + (valid & 4), &two, 2);
+        if (valid & 1) p[valid & 6] = (int8_t)(valid & 2 ? r >> 16 : r);
+    }
+}
+
 // 1 / sqrt(x), within an ulp as the hardware's is.  That takes normal numbers only.
 __device__ __forceinline__ float inv_root(float x) {
     const bool small = x < 0x1p-96f;
@@ -83,15 +227,22 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
     const int lane = threadIdx.x % LPT;
     const int cols = p.cols;
     const float inv_cols = 1.0f / (float)cols;
-    const auto valid_at = [&](int c) { return !here ? 0 : !WHOLE ? chunk_valid(cols, c) : c < cols ? 8 : 0; };
-    RawChunk<T> y[NP], res[NP], gate[NP];
+    const auto place = [&](int i) { return place_of<WHOLE>((i * LANES + lane) * 8, cols, here); };
+    using Chunk = RowChunk<T, WHOLE>;
+    Chunk y[NP], res[NP], gate[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int c = (i * LANES + lane) * 8;
-        const int valid = valid_at(c);
-        if (p.y) y[i].load((const T*)p.y + row * cols + c, valid);
-        if (p.residual) res[i].load((const T*)p.residual + row * cols + c, valid);
-        if (p.gate_kind == kGateElement) gate[i].load((const T*)p.gate + row * cols + c, valid);
+        const Place q = place(i);
+        if (p.y) y[i].load((const T*)p.y + row * cols, cols, q);
+        if (p.residual) res[i].load((const T*)p.residual + row * cols, cols, q);
+        if (p.gate_kind == kGateElement) gate[i].load((const T*)p.gate + row * cols, cols, q);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const Place q = place(i);
+        if (p.y) y[i].fix(q);
+        if (p.residual) res[i].fix(q);
+        if (p.gate_kind == kGateElement) gate[i].fix(q);
     }
     float v[8], h[NP][8];
     float rp = 1.0f;
@@ -109,8 +260,7 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int c = (i * LANES + lane) * 8;
-        const int valid = valid_at(c);
+        const Place q = place(i);
         fill(h[i], 0.0f);
         if (p.residual) res[i].get(h[i]);
         if (p.y) {
@@ -118,21 +268,21 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
             fill(k, p.scale);
             if (p.gate_kind != kGateNone) {
                 if (p.gate_kind == kGateElement) gate[i].get(w);
-                else load_chunk_any(p.gate, p.param_f32, c, valid, w);
+                else get_chunk<WHOLE>(p.gate, p.param_f32, cols, q, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) k[j] *= w[j];
             }
             y[i].get(v);
             if (p.post_rstd) {
                 fill(w, 1.0f);
-                if (p.post_weight) load_chunk_any(p.post_weight, p.param_f32, c, valid, w);
+                if (p.post_weight) get_chunk<WHOLE>(p.post_weight, p.param_f32, cols, q, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * (WHOLE ? valid ? rp : 0.0f : j < valid ? rp : 0.0f) * w[j];
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * (WHOLE ? q.valid ? rp : 0.0f : j < q.valid ? rp : 0.0f) * w[j];
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[i][j] = __builtin_fmaf(k[j], v[j], h[i][j]);
         }
-        if (p.h) store_chunk((T*)p.h + row * cols + c, valid, h[i]);
+        if (p.h) Chunk::store((T*)p.h + row * cols, q, h[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(h[i][j], h[i][j], sq);
     }
@@ -141,21 +291,20 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
     if (lane == 0 && here) p.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int c = (i * LANES + lane) * 8;
-        const int valid = valid_at(c);
+        const Place q = place(i);
         float w[8];
         fill(w, 1.0f);
-        if (p.weight) load_chunk_any(p.weight, p.param_f32, c, valid, w);
+        if (p.weight) get_chunk<WHOLE>(p.weight, p.param_f32, cols, q, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = h[i][j] * (WHOLE ? valid ? r : 0.0f : j < valid ? r : 0.0f) * w[j];
-        store_chunk((T*)p.out + row * cols + c, valid, v);
+        for (int j = 0; j < 8; ++j) v[j] = h[i][j] * (WHOLE ? q.valid ? r : 0.0f : j < q.valid ? r : 0.0f) * w[j];
+        Chunk::store((T*)p.out + row * cols, q, v);
         if (p.ckpt.codes) {
             // of the fp32 values, before their rounding to the output's type
             const uint32_t e = ckpt_exp(block_top(v, p.ckpt.block64));
-            store_codes(p.ckpt.codes + row * cols + c, valid, ckpt_codes(v, e));
+            store_row_codes<WHOLE>(p.ckpt.codes + row * cols + q.c, q.valid, ckpt_codes(v, e));
             const int per = p.ckpt.block64 ? 8 : 4;
-            if ((lane & (per - 1)) == 0 && valid > 0)
-                p.ckpt.exps[row * p.ckpt.nblocks + c / (8 * per)] = (uint8_t)e;
+            if ((lane & (per - 1)) == 0 && q.valid > 0)
+                p.ckpt.exps[row * p.ckpt.nblocks + q.c / (8 * per)] = (uint8_t)e;
         }
     }
 }
