@@ -829,31 +829,42 @@ def _state(state, n, nb, what):
     return codes, exps, 8
 
 
-def _table(n, dev):
-    """Device memory for the table of n tensors."""
-    nbytes = load().loco_adamw_table_bytes(n)
-    return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}") if nbytes else None
+def _stream_of(stream, dev):
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
 
 
-def _described(table, stream, dev):
-    """Waits until the description is in the table: a step on another stream may follow at once, and would
-    take what it read before for addresses."""
-    if table is None:
-        return
+class _Table:
+    """Device memory for a table of n tensors, of the stream that fills it: memory that another stream freed may
+    still be written by the kernels before."""
+
+    def __init__(self, n, stream, dev):
+        nbytes = load().loco_adamw_table_bytes(n)
+        self.tensor = self.home = None
+        if nbytes:
+            s = _stream_of(stream, dev)
+            self.home = s.cuda_stream
+            with torch.cuda.stream(s):
+                self.tensor = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+
+    def stream(self, stream, dev):
+        """The stream to call on; the memory is not used again before that stream is past the call."""
+        handle = _stream(stream, dev)
+        if self.tensor is not None and handle != self.home:
+            self.tensor.record_stream(_stream_of(stream, dev))
+        return handle
+
+    def described(self, stream, dev):
+        """Waits until the description is in the table: a step on another stream may follow at once, and would
+        take what it read before for addresses."""
+        if self.tensor is not None:
+            _stream_of(stream, dev).synchronize()
+
+
+def _not_captured():
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("describe the tensors before a graph is captured: the table is filled on the device")
-    if stream is None:
-        torch.cuda.current_stream(dev).synchronize()
-    else:
-        (stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)).synchronize()
-
-
-def _held_for(table, stream, dev):
-    """The stream to call on; the table's memory is not used again before that stream is past it."""
-    if stream is not None and table is not None:
-        table.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                            torch.cuda.ExternalStream(int(stream), device=dev))
-    return _stream(stream, dev)
 
 
 class AdamwTensors:
@@ -893,15 +904,17 @@ class AdamwTensors:
             rows.append((*(_ptr(x, dev) for x in parts), n, weight_decay if decay is None else decay))
             keep.append(tuple(_keep(x) for x in parts))
         count = len(rows)
+        if _wait and count:
+            _not_captured()
         array = (AdamwTensor * max(1, count))(*(AdamwTensor(*r) for r in rows))
-        table = _table(count, dev)
+        table = _Table(count, stream, dev)
         self._keep, self._table, self.plan = (keep, array), table, AdamwPlan()
         st = load().loco_adamw_plan(array, count, _CODES.get(self.param_dtype, LOCO_F32),
-                                    _CODES.get(self.grad_dtype, LOCO_F32), self.bits or 32, block, _ptr(table, dev),
-                                    _nbytes(table), ctypes.byref(self.plan), _held_for(table, stream, dev))
+                                    _CODES.get(self.grad_dtype, LOCO_F32), self.bits or 32, block, _ptr(table.tensor, dev),
+                                    _nbytes(table.tensor), ctypes.byref(self.plan), table.stream(stream, dev))
         _check("loco_adamw_plan", st)
         if _wait:
-            _described(table, stream, dev)
+            table.described(stream, dev)
 
 
 def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -922,7 +935,7 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
     _sized(grad_scale, 1, "grad_scale", _F32)
     opt = AdamwOptions(lr, beta1, beta2, eps, step)
     st = (_lib or load()).loco_adamw(ctypes.byref(tensors.plan), ctypes.byref(opt), _ptr(grad_scale, dev),
-                                     _held_for(tensors._table, stream, dev))
+                                     tensors._table.stream(stream, dev))
     _check("loco_adamw", st)
 
 
@@ -945,14 +958,16 @@ class AdamwStates:
                          1 if codes.dtype == torch.float8_e4m3fn else 2))
             keep.append((_keep(codes), _keep(exps), _keep(values)))
         count = len(rows)
+        if _wait and count:
+            _not_captured()
         array = (AdamwState * max(1, count))(*(AdamwState(*r) for r in rows))
-        table = _table(count, dev)
+        table = _Table(count, stream, dev)
         self._keep, self._table, self.plan = keep, table, AdamwPlan()
-        st = load().loco_adamw_state_plan(array, count, block, _CODES.get(self.dtype, LOCO_F32), _ptr(table, dev),
-                                          _nbytes(table), ctypes.byref(self.plan), _held_for(table, stream, dev))
+        st = load().loco_adamw_state_plan(array, count, block, _CODES.get(self.dtype, LOCO_F32), _ptr(table.tensor, dev),
+                                          _nbytes(table.tensor), ctypes.byref(self.plan), table.stream(stream, dev))
         _check("loco_adamw_state_plan", st)
         if _wait:
-            _described(table, stream, dev)
+            table.described(stream, dev)
 
 
 def _adamw_states(name, states, block, stream):
@@ -963,7 +978,7 @@ def _adamw_states(name, states, block, stream):
     dev = _device()
     if dev != states.device:
         raise ValueError(f"the states are on cuda:{states.device}; the call runs on the current device, cuda:{dev}")
-    _check(name, getattr(_lib or load(), name)(ctypes.byref(states.plan), _held_for(states._table, stream, dev)))
+    _check(name, getattr(_lib or load(), name)(ctypes.byref(states.plan), states._table.stream(stream, dev)))
 
 
 def loco_adamw_state_read(states, *, block: int | None = None, stream=None) -> None:

@@ -322,3 +322,21 @@ def test_description_and_streams(gpu_lib):
         torch.cuda.synchronize()
         for x, y in zip((a.p, a.m, a.v), (b.p, b.m, b.v)):
             assert np.array_equal(bits(x.t), bits(y.t))
+
+
+def test_a_list_on_a_stream_of_its_own(gpu_lib):
+    """The table of a plain list is not memory that the current stream has freed and is still to write."""
+    a, b = (Tensor(13, 5000, BF, BF, 8, 64, False) for _ in range(2))
+    gpu_lib.adamw([b.args(0.1)], block=64, **HP)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    big = torch.randn(4096, 4096, device="cuda")
+    for _ in range(20):
+        big = big @ big * 1e-2
+    for n in (256, 512, 1024):
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    gpu_lib.adamw([a.args(0.1)], block=64, stream=side, **HP)
+    side.synchronize()
+    torch.cuda.synchronize()
+    for x, y in zip((a.p, a.m, a.v), (b.p, b.m, b.v)):
+        assert np.array_equal(bits(x.t), bits(y.t))
