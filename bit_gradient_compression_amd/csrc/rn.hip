@@ -63,7 +63,7 @@ __device__ __forceinline__ void fill(float (&v)[8], float x) {
 // `shift` are dropped when they are there: element by element, or in parts that are put together where they are
 // loaded, one matrix waited for the one before it (16384 x 4095 in bf16 with a checkpoint 236 and 176 us, so
 // 149; 8192 x 4095 in fp32 109, 114 and 107; only a last chunk alone in its wave is slower, 4097 in fp32 116, 117
-// and 136).  What is dropped another lane may be writing, where a call works in place.
+// and 136).
 struct Place {
     int c, at, valid, shift;
 };
@@ -879,7 +879,7 @@ int64_t rn_bwd_groups(int64_t rows, int64_t cols) {
 hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream) {
     const RnBwdShape s = rn_bwd_shape(p.cols);
     const int64_t groups = rn_bwd_groups(p.rows, p.cols);
-    const bool post = p.post_rstd != nullptr;
+    const bool post = p.post_rstd || p.sums[1];  // without rows the sum is there without rstd
     const void* k = p.f32 ? pick_rn_bwd<float>(p.cols, post, p.gate_kind) : pick_rn_bwd<uint16_t>(p.cols, post, p.gate_kind);
     void* args[] = {(void*)&p};
     hipError_t err = hipLaunchKernel(k, dim3((unsigned)groups), dim3(s.waves * 64), args, 0, stream);

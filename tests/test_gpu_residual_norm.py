@@ -269,6 +269,19 @@ def test_backward_without_rows(gpu_lib):
     assert all(bool((s == 0).all()) for s in sums)
 
 
+@pytest.mark.parametrize("gate", [None, "column", "element"])
+def test_backward_without_rows_or_statistics(gpu_lib, gate):
+    """Without rows post_rstd is not needed, and the sums are 0, whatever the workspace held."""
+    e = lambda *s, dtype=BF: torch.empty(*s, dtype=dtype, device="cuda")
+    for cols in (96, 300, 1000, 4096, 9001):
+        sums = [torch.full((cols,), 7.0, device="cuda") for _ in range(3)]
+        ws = torch.full((gpu_lib.residual_norm_backward_workspace(0, cols),), 0x41, dtype=torch.uint8, device="cuda")
+        g = {None: None, "column": torch.ones(cols, device="cuda"), "element": e(0, cols)}[gate]
+        gpu_lib.residual_norm_backward(e(0, cols), gate=g, dgate=sums[0] if gate == "column" else None, dweight=sums[1],
+                                       dpost_weight=sums[2], workspace=ws)
+        assert all(bool((s == 0).all()) for s in sums[gate != "column":]), cols
+
+
 def test_gradient_is_that_of_the_forward_pass(gpu_lib):
     """In fp32, the change of a random linear functional of h and out between two nearby inputs is what
     the gradients say.  Central differences: the step's square times third derivatives, and 2^-24 of the
