@@ -12,6 +12,11 @@
 // m reaches 2^-17 of the block's largest, v 2^-31, and a v that is not 0 never becomes 0: under
 // it m would be divided by eps alone.  The weights' update takes the new m and v before they are
 // rounded.
+//
+// Bound by HBM: every byte is moved once, 28 per element with fp32 weights and states, bf16 gradients and a bf16
+// copy, 16 with 8-bit states.  One LLaMA-7B layer (202 million elements) takes 904 - 974 us
+// (6.3 - 5.8 TB/s, from one card to the next) and 530 us (6.1 TB/s, at 89 instructions per element).  200 tensors
+// of 100 to 40000 elements take 9 us.
 
 #include "loco_device.hpp"
 #include "loco_step_internal.hpp"

@@ -12,6 +12,11 @@
 // that holds it.  Ordered by value and chunk, the k-th of the groups' best bounds the row's k best
 // values from below, each of which is then in a lane whose own best is not below that bound.  Those
 // lanes' values, some k of them at or above it, are collected and ranked by value and index.
+//
+// Forward, a large call is bound by HBM and nearly as much by its 11 instructions per value: 8192 x 32000 in
+// bf16 84 us, 6.2 TB/s, with the vector units busy for 75 of them.  A few rows are bound by latency: a row of
+// 32000 with 8 alternatives takes 6.8 us, 3.5 more than nothing at all, 48 of 131071 with 20 take 12.8 and 3.9
+// for the join.  The gradient reads and writes each value once: 167 us for 8192 x 32000, 6.3 TB/s.
 
 #include "loco_layer.hpp"
 #include "loco_step_internal.hpp"
@@ -226,7 +231,6 @@ __device__ __forceinline__ void write_no_top(const LpParams& p, int64_t row, int
 }
 
 // A row's numbers from its sums, by one thread.
-template <typename T>
 __device__ __forceinline__ void write_row(const LpParams& p, int64_t row, const Sums& a, float log_s) {
     const bool lost = a.s != a.s, empty = a.s == 0.0f;
     const float nan = __builtin_nanf(""), inf = __builtin_huge_valf();
@@ -334,7 +338,7 @@ __global__ __launch_bounds__(THREADS) void lp_kernel(const LpParams p, int64_t r
         if constexpr (SPLIT) {
             p.sums[part] = f32x4{a.m, a.s, a.t, 0.0f};
         } else {
-            write_row<T>(p, row, a, log_s);
+            write_row(p, row, a, log_s);
             if (p.logprob) write_logprob(p, row, a, log_s, target, xt);
         }
     }
@@ -449,7 +453,7 @@ __global__ __launch_bounds__(256) void lp_join_kernel(const LpParams p, int64_t 
     const float log_s = logf(a.s);
     const bool lost = a.s != a.s;
     if (tid == 0) {
-        write_row<T>(p, row, a, log_s);
+        write_row(p, row, a, log_s);
         if (p.logprob) write_logprob(p, row, a, log_s, target, xt);
     }
     if constexpr (TOP) {
