@@ -106,11 +106,12 @@ struct RowChunk<uint16_t, WHOLE> {
         }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(w, v); }
-    static __device__ __forceinline__ void store(uint16_t* row, const Place& q, const float (&v)[8]) {
+    static __device__ __forceinline__ void store(uint16_t* row, const Place& q, const float (&v)[8], bool once) {
         uint16_t* p = row + q.c;
         const u32x4 x = pack_bf16x8(v);
         if (q.valid == 8) {
-            store16(p, x);
+            if (once) stream16(p, x);
+            else store16(p, x);
         } else if (!WHOLE && q.valid > 0) {
             const uint32_t r0 = q.valid & 4 ? x[2] : x[0], r1 = q.valid & 4 ? x[3] : x[1];
             const u32x2 four = {x[0], x[1]};
@@ -163,12 +164,17 @@ struct RowChunk<float, WHOLE> {
             v[4 + j] = b[j];
         }
     }
-    static __device__ __forceinline__ void store(float* row, const Place& q, const float (&v)[8]) {
+    static __device__ __forceinline__ void store(float* row, const Place& q, const float (&v)[8], bool once) {
         float* p = row + q.c;
         const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
         if (q.valid == 8) {
-            __builtin_memcpy(p, &a, 16);
-            __builtin_memcpy(p + 4, &b, 16);
+            if (once) {
+                stream16(p, __builtin_bit_cast(u32x4, a));
+                stream16(p + 4, __builtin_bit_cast(u32x4, b));
+            } else {
+                __builtin_memcpy(p, &a, 16);
+                __builtin_memcpy(p + 4, &b, 16);
+            }
         } else if (!WHOLE && q.valid > 0) {
             const f32x4 r = q.valid & 4 ? b : a;
             const float two[2] = {r[0], r[1]};
@@ -216,7 +222,7 @@ __device__ __forceinline__ float inv_root(float x) {
 // chunk or nothing.  Past a row's end every value is 0 and stays it: a norm's factor, which may be infinite,
 // is made 0 there.
 template <typename T, int LPT, int NP, bool WHOLE>
-__global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParams p, int64_t row0) {
+__global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParams p, int64_t row0, bool once) {
     __shared__ float red[LPT <= 64 ? 1 : 2 * LPT / 64];
     constexpr int LANES = LPT;
     constexpr int RPW = LPT <= 64 ? 256 / LPT : 1;  // rows per workgroup
@@ -284,7 +290,7 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[i][j] = __builtin_fmaf(k[j], v[j], h[i][j]);
         }
-        if (p.h) Chunk::store((T*)p.h + row * cols, q, h[i]);
+        if (p.h) Chunk::store((T*)p.h + row * cols, q, h[i], once);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(h[i][j], h[i][j], sq);
     }
@@ -299,7 +305,7 @@ __global__ __launch_bounds__(LPT <= 64 ? 256 : LPT) void rn_kernel(const RnParam
         if (p.weight) get_chunk<WHOLE>(p.weight, p.param_f32, cols, q, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = h[i][j] * (WHOLE ? q.valid ? r : 0.0f : j < q.valid ? r : 0.0f) * w[j];
-        Chunk::store((T*)p.out + row * cols, q, v);
+        Chunk::store((T*)p.out + row * cols, q, v, once);
         if (p.ckpt.codes) {
             // of the fp32 values, before their rounding to the output's type
             const uint32_t e = ckpt_exp(block_top(v, p.ckpt.block64));
@@ -368,13 +374,18 @@ __device__ __forceinline__ Rsrc span_of(const void* p, int64_t at, uint32_t coun
     return buffer_rsrc((const T*)p + at, count * (uint32_t)sizeof(T));
 }
 
+constexpr int kStream = 2;  // a buffer access's nt bit
+
 // W consecutive elements, the first of them element i of a span, as they lie in memory.
 template <typename T, int W>
 struct Piece;
 template <>
 struct Piece<uint16_t, 8> {
     u32x4 w;
-    __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b128(r, i * 2, 0, 0); }
+    template <bool ONCE = false>
+    __device__ __forceinline__ void load(Rsrc r, uint32_t i) {
+        w = __builtin_amdgcn_raw_buffer_load_b128(r, i * 2, 0, ONCE ? kStream : 0);
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(w, v); }
     // Makes the compiler unpack the values again, instead of keeping them from one phase of a row to the
     // next in registers of their own.
@@ -386,9 +397,10 @@ struct Piece<uint16_t, 8> {
 template <>
 struct Piece<float, 8> {
     u32x4 a, b;
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(Rsrc r, uint32_t i) {
-        a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, 0);
-        b = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4 + 16, 0, 0);
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, ONCE ? kStream : 0);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4 + 16, 0, ONCE ? kStream : 0);
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
@@ -412,6 +424,7 @@ struct Piece<float, 8> {
 template <>
 struct Piece<uint16_t, 1> {
     uint32_t w;
+    template <bool = false>
     __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b16(r, i * 2, 0, 0); }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float(w << 16); }
     __device__ __forceinline__ void forget() {}
@@ -422,6 +435,7 @@ struct Piece<uint16_t, 1> {
 template <>
 struct Piece<float, 1> {
     uint32_t w;
+    template <bool = false>
     __device__ __forceinline__ void load(Rsrc r, uint32_t i) { w = __builtin_amdgcn_raw_buffer_load_b32(r, i * 4, 0, 0); }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float(w); }
     __device__ __forceinline__ void forget() {}
@@ -458,7 +472,7 @@ struct RowPart {
 constexpr uint32_t kNowhere = 1u << 28;  // past the end of any span
 
 // What the pass reads of a row's W columns, as it lies in memory.
-template <typename T, int W, bool POST, int GATE>
+template <typename T, int W, bool POST, int GATE, bool STREAM>
 struct RnRaw {
     using P = Piece<T, W>;
     P h, dout, y, dh, gate;
@@ -467,24 +481,24 @@ struct RnRaw {
     // its place would need registers of their own.
     __device__ __forceinline__ void load_first(const RnBwdParams& p, const RowPart& q) {
         const uint32_t live = p.dout ? q.live : 0u;
-        h.load(span_of<T>(p.h, q.at, live), q.i);
-        dout.load(span_of<T>(p.dout, q.at, live), q.i);
+        h.template load<STREAM>(span_of<T>(p.h, q.at, live), q.i);
+        dout.template load<STREAM>(span_of<T>(p.dout, q.at, live), q.i);
     }
     __device__ __forceinline__ void load_y(const RnBwdParams& p, const RowPart& q) {
-        if constexpr (POST || GATE != kGateNone) y.load(span_of<T>(p.y, q.at, q.live), q.i);
+        if constexpr (POST || GATE != kGateNone) y.template load<STREAM>(span_of<T>(p.y, q.at, q.live), q.i);
     }
     __device__ __forceinline__ void load_rest(const RnBwdParams& p, const RowPart& q) {
         load_y(p, q);
-        dh.load(span_of<T>(p.dh, q.at, p.dh ? q.live : 0u), q.i);
-        if constexpr (GATE == kGateElement) gate.load(span_of<T>(p.gate, q.at, q.live), q.i);
+        dh.template load<STREAM>(span_of<T>(p.dh, q.at, p.dh ? q.live : 0u), q.i);
+        if constexpr (GATE == kGateElement) gate.template load<STREAM>(span_of<T>(p.gate, q.at, q.live), q.i);
     }
 };
 
 // W columns of a row through the three phases of the pass.  KEEP: the parameters stay in registers.
-template <typename T, int W, bool POST, int GATE, bool KEEP>
+template <typename T, int W, bool POST, int GATE, bool STREAM, bool KEEP>
 struct RnBwdPiece {
     using P = Piece<T, W>;
-    using Raw = RnRaw<T, W, POST, GATE>;
+    using Raw = RnRaw<T, W, POST, GATE, STREAM>;
     float dw[W];  // dweight's sum over the rows
     float t[W];   // the gradient of the normed y
     float kept[3][KEEP ? W : 1];
@@ -585,7 +599,7 @@ struct RnBwdPiece {
 //
 // In bf16 the next row is on its way while one is worked on.  Loads return in order, so none may follow
 // it: the parameters are kept in registers.  In fp32 those registers would cost a workgroup its place.
-template <typename T, int LPT, int W, int NP, int WAVES, bool POST, int GATE>
+template <typename T, int LPT, int W, int NP, int WAVES, bool POST, int GATE, bool STREAM>
 __global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(const RnBwdParams p) {
     constexpr int TEAMS = WAVES * 64 / LPT;
     constexpr int LANES = LPT;
@@ -611,8 +625,8 @@ __global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(co
     const uint32_t cols = p.cols, whole = cols & ~(W - 1u);
     const float inv_cols = 1.0f / (float)p.cols;
     f32x4* mine = lsum + team * (COLS / 4) + lane;
-    RnBwdPiece<T, W, POST, GATE, AHEAD> pc[NP];
-    RnBwdPiece<T, 1, POST, GATE, AHEAD> tail;
+    RnBwdPiece<T, W, POST, GATE, STREAM, AHEAD> pc[NP];
+    RnBwdPiece<T, 1, POST, GATE, STREAM, AHEAD> tail;
     const bool tailed = (uint32_t)lane < cols - whole;
     float tsum[2] = {0.0f, 0.0f};
     tail.dw[0] = 0.0f;
@@ -658,8 +672,8 @@ __global__ __launch_bounds__(WAVES * 64, LPT < 64 ? 3 : 4) void rn_bwd_kernel(co
     };
     // What a row brings with it.
     struct Row {
-        RnRaw<T, W, POST, GATE> x[NP];
-        RnRaw<T, 1, POST, GATE> tail;
+        RnRaw<T, W, POST, GATE, STREAM> x[NP];
+        RnRaw<T, 1, POST, GATE, STREAM> tail;
         float r, rp;
     };
     auto load_row = [&](Row& o, int64_t row) {
@@ -834,29 +848,36 @@ RnBwdShape rn_bwd_shape(int64_t cols) {
     if (cols <= 4096) return {512, 16, 256};
     return {1024, 16, 256};
 }
-template <typename T, bool POST, int GATE>
+template <typename T, bool POST, int GATE, bool STREAM>
 const void* pick_rn_bwd_shape(int64_t cols) {
     switch (rn_bwd_shape(cols).lpt) {
-        case 16: return (const void*)&rn_bwd_kernel<T, 16, 8, 1, 4, POST, GATE>;
-        case 32: return (const void*)&rn_bwd_kernel<T, 32, 8, 1, 4, POST, GATE>;
-        case 64: return (const void*)&rn_bwd_kernel<T, 64, 8, 1, 8, POST, GATE>;
-        case 128: return (const void*)&rn_bwd_kernel<T, 128, 8, 1, 8, POST, GATE>;
-        case 256: return (const void*)&rn_bwd_kernel<T, 256, 8, 1, 8, POST, GATE>;
-        case 512: return (const void*)&rn_bwd_kernel<T, 512, 8, 1, 16, POST, GATE>;
+        case 16: return (const void*)&rn_bwd_kernel<T, 16, 8, 1, 4, POST, GATE, STREAM>;
+        case 32: return (const void*)&rn_bwd_kernel<T, 32, 8, 1, 4, POST, GATE, STREAM>;
+        case 64: return (const void*)&rn_bwd_kernel<T, 64, 8, 1, 8, POST, GATE, STREAM>;
+        case 128: return (const void*)&rn_bwd_kernel<T, 128, 8, 1, 8, POST, GATE, STREAM>;
+        case 256: return (const void*)&rn_bwd_kernel<T, 256, 8, 1, 8, POST, GATE, STREAM>;
+        case 512: return (const void*)&rn_bwd_kernel<T, 512, 8, 1, 16, POST, GATE, STREAM>;
     }
-    return cols <= 8192 ? (const void*)&rn_bwd_kernel<T, 1024, 8, 1, 16, POST, GATE>
-                        : (const void*)&rn_bwd_kernel<T, 1024, 8, 2, 16, POST, GATE>;
+    return cols <= 8192 ? (const void*)&rn_bwd_kernel<T, 1024, 8, 1, 16, POST, GATE, STREAM>
+                        : (const void*)&rn_bwd_kernel<T, 1024, 8, 2, 16, POST, GATE, STREAM>;
 }
-template <typename T, bool POST>
+template <typename T, bool POST, bool STREAM>
 const void* pick_rn_bwd_gate(int64_t s, int gate) {
-    return gate == kGateNone     ? pick_rn_bwd_shape<T, POST, kGateNone>(s)
-           : gate == kGateColumn ? pick_rn_bwd_shape<T, POST, kGateColumn>(s)
-                                 : pick_rn_bwd_shape<T, POST, kGateElement>(s);
+    return gate == kGateNone     ? pick_rn_bwd_shape<T, POST, kGateNone, STREAM>(s)
+           : gate == kGateColumn ? pick_rn_bwd_shape<T, POST, kGateColumn, STREAM>(s)
+                                 : pick_rn_bwd_shape<T, POST, kGateElement, STREAM>(s);
 }
 template <typename T>
-const void* pick_rn_bwd(int64_t s, bool post, int gate) {
-    return post ? pick_rn_bwd_gate<T, true>(s, gate) : pick_rn_bwd_gate<T, false>(s, gate);
+const void* pick_rn_bwd(int64_t s, bool post, int gate, bool stream) {
+    if constexpr (sizeof(T) == 2) {
+        if (stream) return post ? pick_rn_bwd_gate<T, true, true>(s, gate) : pick_rn_bwd_gate<T, false, true>(s, gate);
+    }
+    return post ? pick_rn_bwd_gate<T, true, false>(s, gate) : pick_rn_bwd_gate<T, false, false>(s, gate);
 }
+
+// What the matrices of one pass have to come to for it to stream them past the caches: the last-level cache's
+// bytes, past which nothing of the last pass is left in it, nor anything of this one for the next.
+constexpr int64_t kStreamBytes = 256 << 20;
 
 }  // namespace
 
@@ -865,9 +886,12 @@ hipError_t launch_rn(const RnParams& p, hipStream_t stream) {
     const int rpw = s.lpt <= 64 ? 256 / s.lpt : 1, threads = s.lpt <= 64 ? 256 : s.lpt;
     const void* k = p.cols % 8 == 0 ? (p.f32 ? pick_rn<float, true>(s) : pick_rn<uint16_t, true>(s))
                                     : (p.f32 ? pick_rn<float, false>(s) : pick_rn<uint16_t, false>(s));
+    // What is written.  us without / with, both norms and a gate of columns in bf16: 16384 x 4096 96 / 94, with the
+    // checkpoint 117 / 114, 8192 x 8192 110 / 106.  Smaller outputs the caches hold for what reads them next.
+    const bool once = p.rows * p.cols * ((p.h ? 1 : 0) + (p.out ? 1 : 0)) * (p.f32 ? 4 : 2) >= kStreamBytes;
     for (int64_t row0 = 0; row0 < p.rows; row0 += kMaxGrid * rpw) {
         const int64_t rows = p.rows - row0 < kMaxGrid * rpw ? p.rows - row0 : kMaxGrid * rpw;
-        void* args[] = {(void*)&p, (void*)&row0};
+        void* args[] = {(void*)&p, (void*)&row0, (void*)&once};
         const hipError_t err =
             hipLaunchKernel(k, dim3((unsigned)((rows + rpw - 1) / rpw)), dim3(threads), args, 0, stream);
         if (err != hipSuccess) return err;
@@ -885,7 +909,14 @@ hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream) {
     const RnBwdShape s = rn_bwd_shape(p.cols);
     const int64_t groups = rn_bwd_groups(p.rows, p.cols);
     const bool post = p.post_rstd || p.sums[1];  // without rows the sum is there without rstd
-    const void* k = p.f32 ? pick_rn_bwd<float>(p.cols, post, p.gate_kind) : pick_rn_bwd<uint16_t>(p.cols, post, p.gate_kind);
+    // What is read, in bf16.  Rows of 4096, again and again, us without / with: 4096 rows with a gate of columns
+    // 40 / 49, without one 37 / 43; 6144 62 / 64, 57 / 57; 8192 86 / 79, 85 / 71; 16384 154 / 143, 152 / 129.  In
+    // fp32, which reads each row when it is its turn, 8192 rows 165 / 174.
+    const int matrices = (p.dout ? 2 : 0) + (p.dh ? 1 : 0) + (post || p.gate_kind != kGateNone ? 1 : 0) +
+                         (p.gate_kind == kGateElement ? 1 : 0);
+    const bool once = !p.f32 && p.rows * p.cols * matrices * 2 >= kStreamBytes;
+    const void* k = p.f32 ? pick_rn_bwd<float>(p.cols, post, p.gate_kind, once)
+                          : pick_rn_bwd<uint16_t>(p.cols, post, p.gate_kind, once);
     void* args[] = {(void*)&p};
     hipError_t err = hipLaunchKernel(k, dim3((unsigned)groups), dim3(s.waves * 64), args, 0, stream);
     if (err != hipSuccess || !p.part) return err;

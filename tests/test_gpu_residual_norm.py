@@ -361,3 +361,64 @@ def test_streams_and_graphs(gpu_lib):
         torch.cuda.synchronize()
         for o in outs:
             assert all(torch.equal(o[k], want[k]) for k in want), i
+
+
+@pytest.mark.parametrize("cols, rows", [(4096, 16500), (4095, 16500), (200, 340000)])
+@pytest.mark.parametrize("post, gate", [(True, "column"), (True, None), (False, "column"), (True, "element"),
+                                        (False, "element"), (False, None)])
+def test_calls_past_the_caches(gpu_lib, cols, rows, post, gate):
+    """Matrices that no cache holds are streamed: the rows of such a call have the bits that a call of
+    few rows gives them, and its sums are those of the formula.  160 fp32 additions at most lie between a
+    term and its sum over the rows (rows per team, 56 at most here, teams, groups per thread of the join, its 32
+    threads), each off by half a step of at most the sum of the terms' sizes.  A term is a product of up to five
+    roundings with dh', whose own are of its parts' sizes, at most 30 of them in the row's sum."""
+    g = torch.Generator("cuda").manual_seed(7)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+    y, res, dout, dh = (randn(rows, cols) for _ in range(4))
+    w, wp = (1 + 0.1 * randn(cols) for _ in range(2))
+    gt = None if gate is None else randn(cols) if gate == "column" else randn(rows, cols)
+    rows_of = lambda t, s: t if s == slice(None) else t[s].clone()  # a buffer starts on 16 bytes
+
+    def call(s, sums=True):
+        e = lambda *shape, dtype=BF: torch.empty(*shape, dtype=dtype, device="cuda")
+        ys, rs, ds, dhs = (rows_of(t, s) for t in (y, res, dout, dh))
+        gs, n = rows_of(gt, s) if gate == "element" else gt, ys.shape[0]
+        o = {"h": e(n, cols), "out": e(n, cols), "rstd": e(n, dtype=F32), "dres": e(n, cols), "dy": e(n, cols),
+             "rp": e(n, dtype=F32) if post else None}
+        gpu_lib.residual_norm(ys, rs, h=o["h"], out=o["out"], rstd=o["rstd"], weight=w, post_rstd=o["rp"],
+                              post_weight=wp if post else None, gate=gs, scale=0.5)
+        if gate == "element":
+            o["dgate"] = e(n, cols)
+        elif gate and sums:
+            o["dgate"] = e(cols, dtype=F32)
+        if sums:
+            o["dw"] = e(cols, dtype=F32)
+            o["dwp"] = e(cols, dtype=F32) if post else None
+        ws = e(gpu_lib.residual_norm_backward_workspace(n, cols), dtype=torch.uint8)
+        gpu_lib.residual_norm_backward(ds, o["h"], rstd=o["rstd"], weight=w, dh=dhs, y=ys, post_rstd=o["rp"],
+                                       post_weight=wp if post else None, gate=gs, scale=0.5, dresidual=o["dres"],
+                                       dy=o["dy"], dgate=o.get("dgate"), dweight=o.get("dw"), dpost_weight=o.get("dwp"),
+                                       workspace=ws)
+        return o
+
+    whole = call(slice(None))
+    for s in (slice(0, 300), slice(rows // 2, rows // 2 + 301), slice(rows - 77, rows)):
+        few = call(s, sums=False)
+        for k, t in few.items():
+            assert t is None or torch.equal(whole[k][s], t), k
+    d64 = lambda t: t.double()
+
+    def near(got, term, size=None):
+        return bool(((d64(got) - term.sum(0)).abs() <= 200 * 2.0 ** -24 * (term if size is None else size).abs().sum(0)).all())
+
+    r = d64(whole["rstd"])[:, None]
+    xh, gw = d64(whole["h"]) * r, d64(dout) * d64(w)
+    assert near(whole["dw"], d64(dout) * xh)
+    f = 0.5 * d64(y) * (d64(whole["rp"])[:, None] if post else 1.0)
+    d = (d64(dh) + r * (gw - xh * (gw * xh).mean(1, keepdim=True))) * f
+    size = (d64(dh).abs() + r * (gw.abs() + xh.abs() * (gw * xh).abs().mean(1, keepdim=True))) * f
+    if post:
+        k = 1.0 if gt is None else d64(gt)
+        assert near(whole["dwp"], d * k, size * k)
+    if gate == "column":
+        assert near(whole["dgate"], d * (d64(wp) if post else 1.0), size * (d64(wp) if post else 1.0))
