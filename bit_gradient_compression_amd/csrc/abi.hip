@@ -6,7 +6,7 @@
 
 using namespace loco;
 
-LOCO_API int loco_version(void) { return 10300; }
+LOCO_API int loco_version(void) { return 10400; }
 
 LOCO_API const char* loco_status_string(int status) {
     switch (status) {

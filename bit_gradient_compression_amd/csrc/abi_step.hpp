@@ -121,12 +121,14 @@ LOCO_API int loco_adamw_plan(const loco_adamw_tensor_t* tensors, int ntensors, l
     return LOCO_OK;
 }
 
-LOCO_API int loco_adamw(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale, void* stream) {
+LOCO_API int loco_adamw_ex(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale,
+                           const loco_adamw_rounding_t* rounding, void* stream) {
     if (!plan || plan->kind != kAdamwPlan || !options) return LOCO_ERR_INVALID;
     const loco_adamw_t& o = *options;
     if (!isfinite(o.lr) || !isfinite(o.eps) || !((float)o.eps > 0.0f) || !isfinite((float)o.eps)) return LOCO_ERR_INVALID;
     if (!(o.beta1 >= 0.0 && o.beta1 < 1.0 && o.beta2 >= 0.0 && o.beta2 < 1.0) || o.step < 1) return LOCO_ERR_INVALID;
     const double bias1 = 1.0 - pow(o.beta1, (double)o.step), bias2 = 1.0 - pow(o.beta2, (double)o.step);
+    const int64_t* counter = rounding ? rounding->counter : nullptr;
     AwParams p;
     memset(&p, 0, sizeof(p));
     p.table = plan->table;
@@ -141,23 +143,30 @@ LOCO_API int loco_adamw(const loco_adamw_plan_t* plan, const loco_adamw_t* optio
     p.step_size = (float)(o.lr / bias1);
     p.root = (float)(1.0 / sqrt(bias2));
     p.eps = (float)o.eps;
+    if (rounding) p.key = aw_mix(rounding->seed + (uint64_t)o.step * 0x9E3779B97F4A7C15u);
+    p.counter = counter;
     if (!isfinite(p.step_size)) return LOCO_ERR_INVALID;
     const int ps = dtype_size(plan->param_dtype), ss = plan->state_bits == 8 ? 1 : 4;
-    const Range scale = range_of(grad_scale, grad_scale ? 4 : 0);
+    const Range scalars[2] = {range_of(grad_scale, grad_scale ? 4 : 0), range_of(counter, counter ? 8 : 0)};
     for (int i = 0; i < plan->ntensors; ++i) {
         const loco_adamw_tensor_t& t = plan->tensors[i];
         if (!isfinite((float)(1.0 - o.lr * t.weight_decay))) return LOCO_ERR_INVALID;
-        if (!grad_scale || t.n == 0) continue;
+        if ((!grad_scale && !counter) || t.n == 0) continue;
         const int64_t nb = plan->state_bits == 8 ? nblocks(t.n, plan->block) : 0;
-        if (overlap(scale, range_of(t.param, t.n * ps)) || overlap(scale, range_of(t.m, t.n * ss)) ||
-            overlap(scale, range_of(t.v, t.n * ss)) || overlap(scale, range_of(t.m_exps, nb)) ||
-            overlap(scale, range_of(t.v_exps, nb)) || overlap(scale, range_of(t.param_bf16, t.param_bf16 ? t.n * 2 : 0)))
-            return LOCO_ERR_INVALID;
+        for (const Range& r : scalars)
+            if (overlap(r, range_of(t.param, t.n * ps)) || overlap(r, range_of(t.m, t.n * ss)) ||
+                overlap(r, range_of(t.v, t.n * ss)) || overlap(r, range_of(t.m_exps, nb)) ||
+                overlap(r, range_of(t.v_exps, nb)) || overlap(r, range_of(t.param_bf16, t.param_bf16 ? t.n * 2 : 0)))
+                return LOCO_ERR_INVALID;
     }
-    if (grad_scale && !aligned16(grad_scale)) return LOCO_ERR_ALIGN;
+    if ((grad_scale && !aligned16(grad_scale)) || (counter && !aligned16(counter))) return LOCO_ERR_ALIGN;
     if (p.ntiles == 0) return LOCO_OK;
     return hip_status(launch_aw(p, plan->param_dtype == LOCO_F32, plan->grad_dtype == LOCO_F32,
-                                plan->state_bits == 8 ? plan->block : 0, (hipStream_t)stream));
+                                plan->state_bits == 8 ? plan->block : 0, rounding != nullptr, (hipStream_t)stream));
+}
+
+LOCO_API int loco_adamw(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale, void* stream) {
+    return loco_adamw_ex(plan, options, grad_scale, nullptr, stream);
 }
 
 LOCO_API int loco_adamw_state_plan(const loco_adamw_state_t* states, int nstates, int block, loco_dtype_t dtype,

@@ -13,10 +13,15 @@
 // it m would be divided by eps alone.  The weights' update takes the new m and v before they are
 // rounded.
 //
+// A step changes v by (1 - b2) of itself or so, which is less than half a step of its code as soon as
+// 1 - b2 is below 1/18: rounded to nearest, v stays where it is for good, and so does a small m beside a large
+// one.  Rounded up with the probability of the dropped part (RANDOM), a state is its average in the mean at
+// any b1 and b2.  The random bits are a hash of the call's key and the element's position.
+//
 // Bound by HBM: every byte is moved once, 28 per element with fp32 weights and states, bf16 gradients and a bf16
 // copy, 16 with 8-bit states.  One LLaMA-7B layer (202 million elements) takes 904 - 974 us
-// (6.3 - 5.8 TB/s, from one card to the next) and 530 us (6.1 TB/s, at 89 instructions per element).  200 tensors
-// of 100 to 40000 elements take 9 us.
+// (6.3 - 5.8 TB/s, from one card to the next) and 523 us (6.2 TB/s, at 89 instructions per element), 547 with random
+// rounding.  200 tensors of 100 to 40000 elements take 9 us in either.
 
 #include "loco_device.hpp"
 #include "loco_step_internal.hpp"
@@ -58,6 +63,8 @@ __device__ __forceinline__ uint32_t m_encode4(const float* x, uint32_t e) {
 // v: the byte of the block's exponent, that of its largest value rounded to four significant bits.
 // At least 32: the smallest exponent, 31 below it, is a normal number's.
 __device__ __forceinline__ uint32_t v_exp(uint32_t top) { return min(max((top + 0x80000u) >> 23, 32u), 255u); }
+// Where values may be rounded up: that of the largest rounded up, so that the largest code is not a limit.
+__device__ __forceinline__ uint32_t v_exp_up(uint32_t top) { return min(max((top + 0xfffffu) >> 23, 32u), 255u); }
 
 __device__ __forceinline__ void v_decode4(uint32_t w, uint32_t e, float* x) {
     const uint32_t base = (max(e, 32u) - 31u) << 3;
@@ -75,6 +82,47 @@ __device__ __forceinline__ uint32_t v_encode4(const float* x, uint32_t e) {
     for (int j = 0; j < 4; ++j) {
         const uint32_t b = __float_as_uint(x[j]);
         const int r = (int)((b + 0x7ffffu + ((b >> 20) & 1u)) >> 20);  // four significant bits, ties to even
+        const uint32_t c = x[j] > 0.0f ? (uint32_t)min(max(r - base, 1), 255) : 0u;
+        w |= c << (8 * j);
+    }
+    return e == 255u ? 0u : w;
+}
+
+// ---- random rounding ----------------------------------------------------------------------
+//
+// A code keeps the upper bits of a pattern; 20 random bits are added to the 20 that it drops, and carry with
+// the probability that these are of a step.  What is a code's value already drops zeros and stays.
+
+// 32 random bits of an element: two rounds of shifts and products, each half of the key before one.  All bits
+// depend on all of the position's and the key's (the tests count them).
+__device__ __forceinline__ uint32_t element_bits(uint32_t pos, uint32_t k0, uint32_t k1) {
+    uint32_t x = pos ^ k0;
+    x = (x ^ (x >> 16)) * 0x9E3779B9u;
+    x = x ^ k1;
+    x = (x ^ (x >> 15)) * 0xB504F335u;
+    return x ^ (x >> 16);
+}
+// m takes the upper 20 of them, v the lower 20 in reverse: what they share are the lowest bits of both.
+__device__ __forceinline__ uint32_t m_encode4_random(const float* x, uint32_t e, const uint32_t* bits) {
+    const float inv = m_inv(e);
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float y = __builtin_fabsf(x[j] * inv);
+        // below 2^-6 codes are equidistant, as the values from 2^-6 to 2^-5 are
+        const bool small = y < 0x1p-6f;
+        const uint32_t b = __float_as_uint(small ? y + 0x1p-6f : y);
+        const uint32_t c = ((b + (bits[j] >> 12)) >> 20) - (small ? 121u << 3 : 120u << 3);
+        w |= (c | (__float_as_uint(x[j]) >> 24 & 128u)) << (8 * j);
+    }
+    return e == 255u ? 0u : w;
+}
+__device__ __forceinline__ uint32_t v_encode4_random(const float* x, uint32_t e, const uint32_t* bits) {
+    const int base = (int)(e - 31u) << 3;
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = (int)((__float_as_uint(x[j]) + (__builtin_bitreverse32(bits[j]) >> 12)) >> 20);
         const uint32_t c = x[j] > 0.0f ? (uint32_t)min(max(r - base, 1), 255) : 0u;
         w |= c << (8 * j);
     }
@@ -258,8 +306,8 @@ __global__ __launch_bounds__(256) void aw_fill_kernel(const AwFillParams p) {
 constexpr int kAwThreads = 64;
 constexpr int kAwXcdRun = 128;
 
-// A sub-tile of 512 elements of a tensor.  FULL: all of them exist.
-template <int PK, int GK, int BLOCK, bool FULL>
+// A sub-tile of 512 elements of a tensor.  FULL: all of them exist.  RANDOM: the states are rounded so.
+template <int PK, int GK, int BLOCK, bool RANDOM, bool FULL>
 struct AwSub {
     static constexpr bool SPLIT = PK == kF32 || GK == kF32 || BLOCK == 0;
     int64_t i0[2];
@@ -288,7 +336,9 @@ struct AwSub {
             }
         }
     }
-    __device__ __forceinline__ void step(const AwSegDev& sg, const AwParams& p, float gs, float decay) {
+    // pos, key: of the sub-tile's first element, where RANDOM.
+    __device__ __forceinline__ void step(const AwSegDev& sg, const AwParams& p, float gs, float decay, uint64_t pos,
+                                         uint64_t key, int lane) {
         if constexpr (BLOCK != 0) {
 #pragma unroll
             for (int pc = 0; pc < 2; ++pc) {
@@ -324,9 +374,19 @@ struct AwSub {
 #pragma unroll
             for (int pc = 0; pc < 2; ++pc) {
                 me[pc] = m_exp(mt[pc]);
-                ve[pc] = v_exp(vt[pc]);
-                mw[pc] = m_encode4(m + 4 * pc, me[pc]);
-                vw[pc] = v_encode4(v + 4 * pc, ve[pc]);
+                if constexpr (RANDOM) {
+                    const uint32_t k0 = (uint32_t)key ^ (uint32_t)(pos >> 32) * 0x9E3779B9u, k1 = (uint32_t)(key >> 32);
+                    uint32_t bits[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) bits[j] = element_bits((uint32_t)pos + piece<SPLIT>(lane, pc) + j, k0, k1);
+                    ve[pc] = v_exp_up(vt[pc]);
+                    mw[pc] = m_encode4_random(m + 4 * pc, me[pc], bits);
+                    vw[pc] = v_encode4_random(v + 4 * pc, ve[pc], bits);
+                } else {
+                    ve[pc] = v_exp(vt[pc]);
+                    mw[pc] = m_encode4(m + 4 * pc, me[pc]);
+                    vw[pc] = v_encode4(v + 4 * pc, ve[pc]);
+                }
                 if (valid[pc] && i0[pc] % BLOCK == 0) {
                     sg.mexp[i0[pc] / BLOCK] = (uint8_t)me[pc];
                     sg.vexp[i0[pc] / BLOCK] = (uint8_t)ve[pc];
@@ -339,9 +399,9 @@ struct AwSub {
 };
 
 // One wave per tile of kAwTile elements.  BLOCK: 0 for states in fp32.
-template <int PK, int GK, int BLOCK>
+template <int PK, int GK, int BLOCK, bool RANDOM>
 __global__ __launch_bounds__(kAwThreads) void aw_kernel(const AwParams p, int64_t tbase) {
-    constexpr int U = kAwTile / 512;
+    static_assert(kAwTile == 512, "a tile is a sub-tile");
     const int lane = threadIdx.x;
     const int64_t group = xcd_remap<kXcds, kAwXcdRun>(blockIdx.x, gridDim.x);
     const int64_t tile = tbase + group;
@@ -352,31 +412,34 @@ __global__ __launch_bounds__(kAwThreads) void aw_kernel(const AwParams p, int64_
     const float decay = (float)(1.0 - p.lr * sg.weight_decay);
     const int64_t t0 = (tile - tile0[si]) * kAwTile;
     const float gs = p.grad_scale ? *p.grad_scale : 1.0f;
+    uint64_t key = 0;
+    if constexpr (RANDOM) key = p.counter ? aw_mix(p.key + (uint64_t)*p.counter) : aw_mix(p.key);
+    const uint64_t pos = (uint64_t)tile * kAwTile;
     if (t0 + kAwTile <= sg.n) {
-        AwSub<PK, GK, BLOCK, true> s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) s[u].load(sg, t0 + u * 512, lane);
-#pragma unroll
-        for (int u = 0; u < U; ++u) s[u].step(sg, p, gs, decay);
+        AwSub<PK, GK, BLOCK, RANDOM, true> s;
+        s.load(sg, t0, lane);
+        s.step(sg, p, gs, decay, pos, key, lane);
     } else {
-        for (int64_t t = t0; t < sg.n; t += 512) {
-            AwSub<PK, GK, BLOCK, false> s;
-            s.load(sg, t, lane);
-            s.step(sg, p, gs, decay);
-        }
+        AwSub<PK, GK, BLOCK, RANDOM, false> s;
+        s.load(sg, t0, lane);
+        s.step(sg, p, gs, decay, pos, key, lane);
     }
 }
 
-template <int PK, int GK>
+template <int PK, int GK, bool RANDOM>
 const void* pick_aw(int block) {
     switch (block) {
-        case 0: return (const void*)&aw_kernel<PK, GK, 0>;
-        case 64: return (const void*)&aw_kernel<PK, GK, 64>;
-        case 128: return (const void*)&aw_kernel<PK, GK, 128>;
-        case 256: return (const void*)&aw_kernel<PK, GK, 256>;
-        case 512: return (const void*)&aw_kernel<PK, GK, 512>;
+        case 64: return (const void*)&aw_kernel<PK, GK, 64, RANDOM>;
+        case 128: return (const void*)&aw_kernel<PK, GK, 128, RANDOM>;
+        case 256: return (const void*)&aw_kernel<PK, GK, 256, RANDOM>;
+        case 512: return (const void*)&aw_kernel<PK, GK, 512, RANDOM>;
     }
     return nullptr;
+}
+template <int PK, int GK>
+const void* pick_aw(int block, bool random) {
+    if (block == 0) return (const void*)&aw_kernel<PK, GK, 0, false>;
+    return random ? pick_aw<PK, GK, true>(block) : pick_aw<PK, GK, false>(block);
 }
 
 // ---- 8-bit states to and from values ------------------------------------------------------
@@ -464,9 +527,9 @@ hipError_t launch_aw_fill(const AwFillParams& p, hipStream_t stream) {
     return hipLaunchKernel((const void*)&aw_fill_kernel, dim3(1), dim3(256), args, 0, stream);
 }
 
-hipError_t launch_aw(const AwParams& p, bool param_f32, bool grad_f32, int block, hipStream_t stream) {
-    const void* k = param_f32 ? (grad_f32 ? pick_aw<kF32, kF32>(block) : pick_aw<kF32, kBF16>(block))
-                              : (grad_f32 ? pick_aw<kBF16, kF32>(block) : pick_aw<kBF16, kBF16>(block));
+hipError_t launch_aw(const AwParams& p, bool param_f32, bool grad_f32, int block, bool random, hipStream_t stream) {
+    const void* k = param_f32 ? (grad_f32 ? pick_aw<kF32, kF32>(block, random) : pick_aw<kF32, kBF16>(block, random))
+                              : (grad_f32 ? pick_aw<kBF16, kF32>(block, random) : pick_aw<kBF16, kBF16>(block, random));
     void* args[] = {(void*)&p, nullptr};
     return launch_tiles(k, args, 1, p.ntiles, stream);
 }

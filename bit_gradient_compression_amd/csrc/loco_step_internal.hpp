@@ -48,9 +48,17 @@ struct AwParams {
     float step_size;  // lr / (1 - beta1^step)
     float root;       // 1 / sqrt(1 - beta2^step)
     float eps;
+    uint64_t key;            // of random rounding: aw_mix(key + *counter) is the call's
+    const int64_t* counter;  // may be null: 0
 };
-// block: 0 for states in fp32, else the elements of one block of 8-bit states.
-hipError_t launch_aw(const AwParams& p, bool param_f32, bool grad_f32, int block, hipStream_t stream);
+// 64 bits of which each depends on all of x's.
+__host__ __device__ inline uint64_t aw_mix(uint64_t x) {
+    x = (x ^ (x >> 32)) * 0x9E3779B97F4A7C15u;
+    x = (x ^ (x >> 29)) * 0xB504F333F9DE6485u;
+    return x ^ (x >> 32);
+}
+// block: 0 for states in fp32, else the elements of one block of 8-bit states, rounded at random or to nearest.
+hipError_t launch_aw(const AwParams& p, bool param_f32, bool grad_f32, int block, bool random, hipStream_t stream);
 hipError_t launch_aw_state(const void* table, int64_t n, int64_t ntiles, int block, bool f32, bool write,
                            hipStream_t stream);
 

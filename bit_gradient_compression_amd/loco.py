@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import warnings
 
 import torch
 
@@ -40,7 +41,7 @@ SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequ
            "loco_checkpoint_write", "loco_checkpoint_read", "loco_linear", "loco_linear_workspace",
            "loco_linear_input_grad", "loco_linear_input_grad_workspace", "loco_linear_weight_grad",
            "loco_linear_weight_grad_workspace", "loco_adamw_table_bytes", "loco_adamw_plan",
-           "loco_adamw", "loco_adamw_state_plan", "loco_adamw_state_read", "loco_adamw_state_write",
+           "loco_adamw", "loco_adamw_ex", "loco_adamw_state_plan", "loco_adamw_state_read", "loco_adamw_state_write",
            "loco_residual_norm", "loco_residual_norm_backward", "loco_residual_norm_backward_workspace",
            "loco_token_logprobs", "loco_token_logprobs_workspace", "loco_token_logprobs_backward"]
 
@@ -88,6 +89,10 @@ class AdamwTensor(ctypes.Structure):
 class AdamwOptions(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
+class AdamwRounding(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("counter", ctypes.c_void_p)]
 
 
 class AdamwState(ctypes.Structure):
@@ -168,6 +173,8 @@ def load(path: str | None = None):
             ("loco_adamw_plan", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ptr, i64,
                                       ctypes.POINTER(AdamwPlan), ptr]),
             ("loco_adamw", i32, [ctypes.POINTER(AdamwPlan), ctypes.POINTER(AdamwOptions), ptr, ptr]),
+            ("loco_adamw_ex", i32, [ctypes.POINTER(AdamwPlan), ctypes.POINTER(AdamwOptions), ptr,
+                                    ctypes.POINTER(AdamwRounding), ptr]),
             ("loco_adamw_state_plan", i32, [ctypes.POINTER(AdamwState), i32, i32, i32, ptr, i64,
                                             ctypes.POINTER(AdamwPlan), ptr]),
             ("loco_adamw_state_read", i32, [ctypes.POINTER(AdamwPlan), ptr]),
@@ -882,6 +889,7 @@ class AdamwTensors:
         self.device, self.block = _device(), block
         dev, rows, keep = self.device, [], []
         self.param_dtype = self.grad_dtype = self.bits = None
+        self.told = False  # that 8-bit states want a seed
         for i, t in enumerate(tensors):
             if not 4 <= len(t) <= 6:
                 raise ValueError(f"tensor {i}: expected (param, grad, m, v[, param_bf16[, weight_decay]])")
@@ -917,13 +925,20 @@ class AdamwTensors:
             table.described(stream, dev)
 
 
-def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-               weight_decay: float | None = None, block: int | None = None, grad_scale=None, stream=None) -> None:
+def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: float | None = None, eps: float = 1e-8,
+               weight_decay: float | None = None, block: int | None = None, grad_scale=None, seed=None,
+               stream=None) -> None:
     """One AdamW step (decoupled weight decay, bias correction) of all tensors.  tensors: an
     AdamwTensors, which has its own block and weight_decay, or what its constructor takes.  beta1
-    and beta2 are the weights of the old moments; step counts from 1; grad_scale is a float32 tensor of
-    one element, or None.  lr, step and the others are read during the call: a captured graph
-    repeats them."""
+    and beta2 (None: 0.999) are the weights of the old moments; step counts from 1; grad_scale is a
+    float32 tensor of one element, or None.  lr, step and the others are read during the call: a
+    captured graph repeats them.
+
+    seed: an int, or an int64 tensor of one element.  With it, 8-bit states are rounded at random, by bits
+    that seed, step and the element's place decide, and follow their averages over a run.  A captured graph,
+    which repeats step, needs a tensor that the graph raises at each replay.  Without it they are rounded to
+    nearest, for a single step: over many, a state that changes by less than half a step at once stays where
+    it is.  Then beta2 has no default, and the first such step of a description warns."""
     if not isinstance(tensors, AdamwTensors):
         tensors = AdamwTensors(tensors, block=256 if block is None else block, weight_decay=weight_decay or 0.0,
                                stream=stream, _wait=False)
@@ -933,9 +948,24 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
     if dev != tensors.device:
         raise ValueError(f"the tensors are on cuda:{tensors.device}; the call runs on the current device, cuda:{dev}")
     _sized(grad_scale, 1, "grad_scale", _F32)
-    opt = AdamwOptions(lr, beta1, beta2, eps, step)
-    st = (_lib or load()).loco_adamw(ctypes.byref(tensors.plan), ctypes.byref(opt), _ptr(grad_scale, dev),
-                                     tensors._table.stream(stream, dev))
+    rounding = None
+    if seed is None:
+        if tensors.bits == 8:
+            if beta2 is None:
+                raise ValueError("8-bit states need a seed: rounded to nearest they do not follow their averages "
+                                 "(for a single step without one, give beta2)")
+            if not tensors.told:
+                tensors.told = True
+                warnings.warn("8-bit states are rounded to nearest without a seed: over many steps they do not follow "
+                              "their averages", RuntimeWarning, stacklevel=2)
+    elif isinstance(seed, torch.Tensor):
+        _sized(seed, 1, "seed", _I64)
+        rounding = ctypes.byref(AdamwRounding(0, _ptr(seed, dev)))
+    else:
+        rounding = ctypes.byref(AdamwRounding(int(seed) & 0xFFFFFFFFFFFFFFFF, None))
+    opt = AdamwOptions(lr, beta1, 0.999 if beta2 is None else beta2, eps, step)
+    st = (_lib or load()).loco_adamw_ex(ctypes.byref(tensors.plan), ctypes.byref(opt), _ptr(grad_scale, dev), rounding,
+                                        tensors._table.stream(stream, dev))
     _check("loco_adamw", st)
 
 

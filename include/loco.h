@@ -548,12 +548,15 @@ int loco_token_logprobs_backward(const void* logits, loco_dtype_t dtype, int64_t
  *                  largest value rounded to 4 significant bits.  Values that are not 0 are
  *                  never stored as 0, but as the code 1 at least; values < 0 are stored as 0
  *   exps   u8[ceil(n/block)]
- * Each value is rounded once, ties to even, to four significant bits (fewer where a first
- * moment is below 2^-14 of its block's range).  A block that holds an infinity or a NaN (or a
- * second moment that rounds to 2^128) is stored with exps 255 and codes 0 and reads as NaN.  A
- * state whose codes are 0 is 0, whatever its exps below 255.  What changes a second moment by
- * less than half a step (beta2 0.999 and a squared gradient below 60 times the moment) is lost in
- * the rounding: take beta2 0.95 or so with 8 bits.
+ * Each value is rounded once, to four significant bits (fewer where a first moment is below 2^-14 of
+ * its block's range): by loco_adamw and loco_adamw_state_write to nearest, ties to even; by loco_adamw_ex at
+ * random.  A block that holds an infinity or a NaN (or a second moment that rounds to 2^128) is stored with
+ * exps 255 and codes 0 and reads as NaN.  A state whose codes are 0 is 0, whatever its exps below 255.
+ *
+ * Steps of a training run need random rounding.  To nearest, what changes a state by less than half a step is
+ * lost, at every step again: a second moment stays where it is for good wherever 1 - beta2 is below 1/18, and is
+ * off its average at any beta2 above 0.9; a first moment from beta1 of about 0.945 on, and at any beta1 where it
+ * is below 2^-14 of its block's range, so that a parameter without a gradient goes on moving.
  * ------------------------------------------------------------------------------ */
 
 /* One tensor (host struct, read while planning and at each step). */
@@ -616,9 +619,31 @@ int loco_adamw_plan(const loco_adamw_tensor_t* tensors, int ntensors, loco_dtype
  * the parameter's update takes m and v before they are rounded into their codes.
  *   grad_scale  device f32[1] (read), such as a clipping factor, or NULL; it must not lie in a buffer
  *               that the step writes
+ * 8-bit states are rounded to nearest: for single steps (see above).
  */
 int loco_adamw(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale,
                void* stream);
+
+/* The random bits of a step (host struct, read during the call). */
+typedef struct {
+    uint64_t seed;
+    const int64_t* counter; /* device i64[1] (read by the step), or NULL: 0.  A captured graph repeats seed and
+                               options->step: give it a counter that another kernel of the graph raises */
+} loco_adamw_rounding_t;
+
+/*
+ * loco_adamw_ex - loco_adamw with the 8-bit states rounded at random, up or down to the nearest codes in the
+ * proportion of the distances: with other bits at every step, m and v are their averages in the mean.
+ *   rounding  NULL: to nearest, as loco_adamw; of no effect on states in fp32.  counter must not lie in a buffer
+ *             that the step writes
+ * The bits are a hash of seed, options->step, *counter and the element's place among the plan's elements, in
+ * which each tensor takes a multiple of 512: the same call has the same results.  A value goes up
+ * if the part of the step that it has over the lower code, in 2^-20 of a step, and 20 bits come to 2^20 or
+ * more; what is a code's value stays.  exps of a second moment are those of the block's largest value rounded up
+ * to 4 significant bits (255 past 15/8 2^127); a value > 0 below the code 1 is still stored as 1.
+ */
+int loco_adamw_ex(const loco_adamw_plan_t* plan, const loco_adamw_t* options, const float* grad_scale,
+                  const loco_adamw_rounding_t* rounding, void* stream);
 
 /* One 8-bit state and its values (host struct, read while planning). */
 typedef struct {

@@ -4,6 +4,8 @@ in order, so it is computed in float32 and compared in bits; the others in 64 bi
 
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 
 from .layer_oracle import f64
@@ -11,6 +13,7 @@ from .layer_oracle import f64
 # -- 8-bit states -------------------------------------------------------------------------
 
 
+@functools.lru_cache
 def fp8_values():
     """The 256 values of a float8 with 4 exponent bits (bias 7) and 3 mantissa bits, no infinities."""
     out = np.zeros(256)
@@ -39,8 +42,41 @@ def _nearest(x, values):
     return np.where((d > 0) | ((d == 0) & (hi % 2 == 0)), hi, lo)
 
 
-def state_write(x, block, moment):
-    """(codes, exps) of values x, block by block from the definition."""
+def _mix(x):
+    x = ((x ^ (x >> 32)) * 0x9E3779B97F4A7C15) % 2 ** 64
+    x = ((x ^ (x >> 29)) * 0xB504F333F9DE6485) % 2 ** 64
+    return x ^ (x >> 32)
+
+
+def rounding_bits(seed, step, counter, places):
+    """(first moment's, second moment's) 20 bits for random rounding of the elements at these places among
+    the step's."""
+    places = np.asarray(places, np.uint64)
+    key = _mix((_mix((seed + step * 0x9E3779B97F4A7C15) % 2 ** 64) + counter) % 2 ** 64)
+    low = lambda x: (x & 0xFFFFFFFF).astype(np.uint32)
+    x = low(places) ^ np.uint32(key % 2 ** 32) ^ (low(places >> 32) * np.uint32(0x9E3779B9))
+    x = (x ^ (x >> 16)) * np.uint32(0x9E3779B9)
+    x = x ^ np.uint32(key >> 32)
+    x = (x ^ (x >> 15)) * np.uint32(0xB504F335)
+    x = x ^ (x >> 16)
+    back = np.zeros_like(x)
+    for i in range(20):
+        back |= (x >> i & 1) << (19 - i)
+    return x >> 12, back
+
+
+def _random(x, values, bits):
+    """The index of one of the two of the ascending values around x: the upper one if the part of their
+    distance that x has over the lower one, in 2^-20 of it, and the bits come to 2^20."""
+    hi = np.searchsorted(values, x, side="right").clip(1, len(values) - 1)
+    lo = hi - 1
+    part = np.rint((x - values[lo]) / (values[hi] - values[lo]) * 2.0 ** 20)
+    return np.where(part + bits >= 2 ** 20, hi, lo)
+
+
+def state_write(x, block, moment, bits=None):
+    """(codes, exps) of values x, block by block from the definition: rounded to nearest, or at random by 20
+    bits for each."""
     x = f64(x)
     codes, exps = np.zeros(x.size, np.uint8), np.zeros(-(-x.size // block), np.uint8)
     fp8 = fp8_values()[:127]
@@ -55,19 +91,24 @@ def state_write(x, block, moment):
                 exps[b] = 255
                 continue
             exps[b] = s + 127
-            codes[b * block:(b + 1) * block] = _nearest(np.abs(v) * 2.0 ** -s, fp8) | np.where(np.signbit(v), 128, 0)
+            y = np.abs(v) * 2.0 ** -s
+            code = _nearest(y, fp8) if bits is None else _random(y, fp8, bits[b * block:(b + 1) * block])
+            codes[b * block:(b + 1) * block] = code | np.where(np.signbit(v), 128, 0)
         else:
             # the exponent of the largest value once it has four significant bits
-            if not np.isfinite(top) or top >= 2.0 ** 128 - 2.0 ** 123:  # halfway from 15/8 2^127 to 2^128
+            # to nearest from halfway between 15/8 and 2 on, at random from 15/8
+            most = 2.0 - 2.0 ** -4 if bits is None else np.nextafter(2.0 - 2.0 ** -3, 2.0)
+            if not np.isfinite(top) or top >= most * 2.0 ** 127:
                 exps[b] = 255
                 continue
             e = 32
-            while top >= (2.0 - 2.0 ** -4) * 2.0 ** (e - 127):
+            while top >= most * 2.0 ** (e - 127):
                 e += 1
             exps[b] = e
             values = second_values(e)
             # between 0 and the code 1 (and at the bottom of the lowest exponent, which 0 takes): 1
-            code = _nearest(v, np.concatenate([[values[1] / 1.125], values[1:]]))
+            values[0] = values[1] / 1.125
+            code = _nearest(v, values) if bits is None else _random(v, values, bits[b * block:(b + 1) * block])
             codes[b * block:(b + 1) * block] = np.where(v > 0, np.maximum(code, 1), 0)
     return codes, exps
 
