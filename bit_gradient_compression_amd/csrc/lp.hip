@@ -527,9 +527,10 @@ __global__ __launch_bounds__(64) void lp_bwd_kernel(const LpBwdParams p, int64_t
     const int64_t target = p.targets ? p.targets[row] : -1;
     float dlp = p.dlogprob ? p.dlogprob[row] : 0.0f;
     if (target < 0) dlp = 0.0f;
-    else if (p.dlogprob && target >= p.vocab) dlp = __builtin_nanf("");
+    const bool past = p.dlogprob && target >= p.vocab;
+    if (past) dlp = __builtin_nanf("");
     // a row without a distribution, or without anything to differentiate, has the gradient 0
-    const bool zero = s == 0.0f || (!ENTROPY && (target < 0 || !p.dlogprob));
+    const bool zero = (s == 0.0f && !past) || (!ENTROPY && (target < 0 || !p.dlogprob));
     const float inv = 1.0f / s, c = p.scale * kLog2e;
     float k = -p.scale * dlp, kd = 0.0f;
     if constexpr (ENTROPY) {

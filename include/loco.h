@@ -488,7 +488,8 @@ int64_t loco_residual_norm_backward_workspace(int64_t rows, int64_t cols);
  *
  * A row that holds a NaN or plus infinity has no distribution: its outputs are NaN (top_ids -1), and so
  * is its gradient.  A row of minus infinities only has the log probability minus infinity, the entropy 0
- * and the gradient 0.  Minus infinity elsewhere (a masked token) has the probability 0.
+ * and the gradient 0; with a target past the vocabulary both are NaN, as in any row.  Minus infinity
+ * elsewhere (a masked token) has the probability 0.
  * ------------------------------------------------------------------------------ */
 
 /* Largest number of alternatives. */
