@@ -340,13 +340,88 @@ LOCO_API int loco_residual_norm_backward(const void* dout, const void* dh, const
 
 namespace {
 
-// Rows of `vocab` elements, `ld` apart; their elements, from the first to the last.
-int64_t span_elems(int64_t rows, int64_t vocab, int64_t ld) { return rows > 0 ? (rows - 1) * ld + vocab : 0; }
+// Sequences of rows of logits as a call gives them.
+struct Rows {
+    int64_t seqs, rows, vocab;
+    int64_t total() const { return seqs * rows; }
+    // the elements, from the first to the last, of `width` each, `ld` from row to row and `seq_ld` from sequence to sequence
+    int64_t span(int64_t ld, int64_t seq_ld, int64_t width) const {
+        return total() > 0 ? (seqs > 1 ? (seqs - 1) * seq_ld : 0) + (rows - 1) * ld + width : 0;
+    }
+    int64_t gap(int64_t ld, int64_t seq_ld) const { return seqs > 1 ? seq_ld - rows * ld : 0; }
+    bool steps_ok(int64_t ld, int64_t seq_ld, int64_t width) const {
+        if (ld < width || !sizes_ok(rows, ld)) return false;
+        return seqs <= 1 || rows == 0 || (seq_ld >= (rows - 1) * ld + width && sizes_ok(seqs, seq_ld));
+    }
+};
 
-int check_logits(int64_t rows, int64_t vocab, int64_t ld, int dtype, float scale) {
-    if (rows < 0 || vocab < 1 || ld < vocab || !sizes_ok(rows, ld) || !dtype_ok(dtype)) return LOCO_ERR_INVALID;
+int check_logits(const Rows& r, int64_t ld, int64_t seq_ld, int64_t target_ld, int dtype, float scale) {
+    if (r.seqs < 0 || r.rows < 0 || r.vocab < 1 || !sizes_ok(r.seqs, r.rows) || !r.steps_ok(ld, seq_ld, r.vocab))
+        return LOCO_ERR_INVALID;
+    if (!r.steps_ok(1, target_ld, 1) || !dtype_ok(dtype)) return LOCO_ERR_INVALID;
     if (!(scale >= 1e-6f && scale <= 1e6f)) return LOCO_ERR_INVALID;
-    return vocab > kLpMaxVocab ? LOCO_ERR_UNSUPPORTED : LOCO_OK;
+    return r.vocab > kLpMaxVocab || (r.seqs > 1 && r.total() > UINT32_MAX) ? LOCO_ERR_UNSUPPORTED : LOCO_OK;
+}
+
+LpSeqs seqs_dev(const Rows& r, int64_t ld, int64_t seq_ld, int64_t dld, int64_t dseq_ld, int64_t target_ld) {
+    return {r.seqs > 1 ? (uint32_t)r.rows : 0u, r.gap(ld, seq_ld), r.gap(dld, dseq_ld), r.gap(1, target_ld)};
+}
+
+// align: least alignment of all buffers.
+int token_logprobs(const void* logits, int dtype, const Rows& r, int64_t ld, int64_t seq_ld, const int64_t* targets,
+                   int64_t target_ld, float scale, float* logprob, float* entropy, float* stats, int top,
+                   int32_t* top_ids, float* top_logprobs, void* workspace, int64_t workspace_bytes, unsigned align,
+                   void* stream) {
+    int st = check_logits(r, ld, seq_ld, target_ld, dtype, scale);
+    if (st != LOCO_OK) return st;
+    if (top < 0) return LOCO_ERR_INVALID;
+    if (top > kLpMaxTop) return LOCO_ERR_UNSUPPORTED;
+    const int64_t rows = r.total(), need = loco_token_logprobs_workspace(rows, r.vocab, top);
+    if (workspace_bytes < need) return LOCO_ERR_INVALID;
+    if (rows == 0) return LOCO_OK;
+    if (!logits || (logprob && !targets) || (!logprob && !entropy && !stats && top == 0)) return LOCO_ERR_INVALID;
+    const unsigned size = (unsigned)dtype_size(dtype), a4 = std::max(align, 4u);
+    st = check_bufs({{logits, r.span(ld, seq_ld, r.vocab) * size, false, true, std::max(align, size)},
+                     {targets, r.span(1, target_ld, 1) * 8, false, false, std::max(align, 8u)},
+                     {logprob, rows * 4, true, false, a4},
+                     {entropy, rows * 4, true, false, a4},
+                     {stats, rows * 8, true, false, a4},
+                     {top_ids, rows * top * 4, true, true, a4},
+                     {top_logprobs, rows * top * 4, true, true, a4},
+                     {workspace, need, true, true}});
+    if (st != LOCO_OK) return st;
+    const int64_t parts = need > 0 ? rows * lp_splits(rows, r.vocab) : 0;
+    const LpParams p = {logits, rows, ld, (int)r.vocab, targets, scale, logprob, entropy, stats, top_ids, top_logprobs, top,
+                        dtype == LOCO_F32, (f32x4_t*)workspace, (uint64_t*)((char*)workspace + parts * 16),
+                        seqs_dev(r, ld, seq_ld, ld, seq_ld, target_ld), 0, 0};
+    return hip_status(launch_lp(p, (hipStream_t)stream));
+}
+
+int token_logprobs_backward(const void* logits, int dtype, const Rows& r, int64_t ld, int64_t seq_ld,
+                            const int64_t* targets, int64_t target_ld, float scale, const float* stats,
+                            const float* entropy, const float* dlogprob, const float* dentropy, void* dlogits,
+                            int64_t dld, int64_t dseq_ld, unsigned align, void* stream) {
+    int st = check_logits(r, ld, seq_ld, target_ld, dtype, scale);
+    if (st != LOCO_OK) return st;
+    if (!r.steps_ok(dld, dseq_ld, r.vocab)) return LOCO_ERR_INVALID;
+    const int64_t rows = r.total();
+    if (rows == 0) return LOCO_OK;
+    if (!logits || !stats || !dlogits || (!dlogprob && !dentropy)) return LOCO_ERR_INVALID;
+    if ((dlogprob && !targets) || (dentropy && !entropy)) return LOCO_ERR_INVALID;
+    // in place: each element is read by the lane that then writes it
+    const bool in_place = dlogits == logits && dld == ld && (r.seqs == 1 || dseq_ld == seq_ld);
+    const unsigned size = (unsigned)dtype_size(dtype), a4 = std::max(align, 4u);
+    st = check_bufs({{logits, in_place ? 0 : r.span(ld, seq_ld, r.vocab) * size, false, true, std::max(align, size)},
+                     {targets, r.span(1, target_ld, 1) * 8, false, false, std::max(align, 8u)},
+                     {stats, rows * 8, false, true, a4},
+                     {entropy, rows * 4, false, false, a4},
+                     {dlogprob, rows * 4, false, false, a4},
+                     {dentropy, rows * 4, false, false, a4},
+                     {dlogits, r.span(dld, dseq_ld, r.vocab) * size, true, true, std::max(align, size)}});
+    if (st != LOCO_OK) return st;
+    const LpBwdParams p = {logits, dlogits, rows, ld, dld, (int)r.vocab, targets, stats, entropy, dlogprob, dentropy, scale,
+                           dtype == LOCO_F32, seqs_dev(r, ld, seq_ld, dld, dseq_ld, target_ld)};
+    return hip_status(launch_lp_bwd(p, (hipStream_t)stream));
 }
 
 }  // namespace
@@ -361,51 +436,31 @@ LOCO_API int loco_token_logprobs(const void* logits, loco_dtype_t dtype, int64_t
                                  const int64_t* targets, float scale, float* logprob, float* entropy, float* stats,
                                  int top, int32_t* top_ids, float* top_logprobs, void* workspace,
                                  int64_t workspace_bytes, void* stream) {
-    int st = check_logits(rows, vocab, ld, dtype, scale);
-    if (st != LOCO_OK) return st;
-    if (top < 0) return LOCO_ERR_INVALID;
-    if (top > kLpMaxTop) return LOCO_ERR_UNSUPPORTED;
-    const int64_t need = loco_token_logprobs_workspace(rows, vocab, top);
-    if (workspace_bytes < need) return LOCO_ERR_INVALID;
-    if (rows == 0) return LOCO_OK;
-    if (!logits || (logprob && !targets) || (!logprob && !entropy && !stats && top == 0)) return LOCO_ERR_INVALID;
-    st = check_bufs({{logits, span_elems(rows, vocab, ld) * dtype_size(dtype), false, true},
-                     {targets, rows * 8, false, false},
-                     {logprob, rows * 4, true, false},
-                     {entropy, rows * 4, true, false},
-                     {stats, rows * 8, true, false},
-                     {top_ids, rows * top * 4, true, true},
-                     {top_logprobs, rows * top * 4, true, true},
-                     {workspace, need, true, true}});
-    if (st != LOCO_OK) return st;
-    const int64_t parts = need > 0 ? rows * lp_splits(rows, vocab) : 0;
-    const LpParams p = {logits, rows, ld, (int)vocab, targets, scale, logprob, entropy, stats, top_ids, top_logprobs, top,
-                        dtype == LOCO_F32, (f32x4_t*)workspace, (uint64_t*)((char*)workspace + parts * 16), 0, 0};
-    return hip_status(launch_lp(p, (hipStream_t)stream));
+    return token_logprobs(logits, dtype, {1, rows, vocab}, ld, 0, targets, 0, scale, logprob, entropy, stats, top, top_ids,
+                          top_logprobs, workspace, workspace_bytes, 16, stream);
+}
+
+LOCO_API int loco_token_logprobs_ex(const void* logits, loco_dtype_t dtype, int64_t seqs, int64_t rows, int64_t vocab,
+                                    int64_t ld, int64_t seq_ld, const int64_t* targets, int64_t target_ld, float scale,
+                                    float* logprob, float* entropy, float* stats, int top, int32_t* top_ids,
+                                    float* top_logprobs, void* workspace, int64_t workspace_bytes, void* stream) {
+    return token_logprobs(logits, dtype, {seqs, rows, vocab}, ld, seq_ld, targets, target_ld, scale, logprob, entropy,
+                          stats, top, top_ids, top_logprobs, workspace, workspace_bytes, 1, stream);
 }
 
 LOCO_API int loco_token_logprobs_backward(const void* logits, loco_dtype_t dtype, int64_t rows, int64_t vocab, int64_t ld,
                                           const int64_t* targets, float scale, const float* stats, const float* entropy,
                                           const float* dlogprob, const float* dentropy, void* dlogits, int64_t dld,
                                           void* stream) {
-    int st = check_logits(rows, vocab, ld, dtype, scale);
-    if (st != LOCO_OK) return st;
-    if (dld < vocab || !sizes_ok(rows, dld)) return LOCO_ERR_INVALID;
-    if (rows == 0) return LOCO_OK;
-    if (!logits || !stats || !dlogits || (!dlogprob && !dentropy)) return LOCO_ERR_INVALID;
-    if ((dlogprob && !targets) || (dentropy && !entropy)) return LOCO_ERR_INVALID;
-    // in place: each element is read by the lane that then writes it
-    const bool in_place = dlogits == logits && dld == ld;
-    const int64_t bytes = span_elems(rows, vocab, ld) * dtype_size(dtype);
-    st = check_bufs({{logits, in_place ? 0 : bytes, false, true},
-                     {targets, rows * 8, false, false},
-                     {stats, rows * 8, false, true},
-                     {entropy, rows * 4, false, false},
-                     {dlogprob, rows * 4, false, false},
-                     {dentropy, rows * 4, false, false},
-                     {dlogits, span_elems(rows, vocab, dld) * dtype_size(dtype), true, true}});
-    if (st != LOCO_OK) return st;
-    const LpBwdParams p = {logits, dlogits, rows, ld, dld, (int)vocab, targets, stats, entropy, dlogprob, dentropy, scale,
-                           dtype == LOCO_F32};
-    return hip_status(launch_lp_bwd(p, (hipStream_t)stream));
+    return token_logprobs_backward(logits, dtype, {1, rows, vocab}, ld, 0, targets, 0, scale, stats, entropy, dlogprob,
+                                   dentropy, dlogits, dld, 0, 16, stream);
+}
+
+LOCO_API int loco_token_logprobs_backward_ex(const void* logits, loco_dtype_t dtype, int64_t seqs, int64_t rows,
+                                             int64_t vocab, int64_t ld, int64_t seq_ld, const int64_t* targets,
+                                             int64_t target_ld, float scale, const float* stats, const float* entropy,
+                                             const float* dlogprob, const float* dentropy, void* dlogits, int64_t dld,
+                                             int64_t dseq_ld, void* stream) {
+    return token_logprobs_backward(logits, dtype, {seqs, rows, vocab}, ld, seq_ld, targets, target_ld, scale, stats,
+                                   entropy, dlogprob, dentropy, dlogits, dld, dseq_ld, 1, stream);
 }

@@ -58,18 +58,20 @@ constexpr int64_t kMaxElems = (int64_t)1 << 52;
 inline bool act_ok(int a) { return a >= LOCO_ACT_NONE && a <= LOCO_ACT_SILU; }
 inline int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// One buffer of a call.  `needed`: a null pointer is an error (of an empty buffer it is not).
+// One buffer of a call.  `needed`: a null pointer is an error (of an empty buffer it is not).  align: what its
+// address is a multiple of.
 struct Buf {
     const void* p;
     int64_t bytes;
     bool written, needed;
+    unsigned align = 16;
 };
 
 inline int check_bufs(std::initializer_list<Buf> bufs) {
     for (const Buf& b : bufs)
         if (b.needed && b.bytes > 0 && !b.p) return LOCO_ERR_INVALID;
     for (const Buf& b : bufs)
-        if (b.p && b.bytes > 0 && !aligned16(b.p)) return LOCO_ERR_ALIGN;
+        if (b.p && b.bytes > 0 && ((uintptr_t)b.p & (b.align - 1))) return LOCO_ERR_ALIGN;
     // no buffer that is written may overlap another buffer of the call
     for (const Buf& a : bufs)
         for (const Buf& b : bufs) {

@@ -115,6 +115,12 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kLpMaxTop = 32;
 constexpr int64_t kLpMaxVocab = (int64_t)1 << 24;
 
+// Sequences of rows: what a row's place in a buffer has beyond row times the step from row to row.
+struct LpSeqs {
+    uint32_t rows;  // of a sequence; 0: there is one
+    int64_t logits, dlogits, targets;  // elements between a sequence's end and the next one
+};
+
 struct LpParams {
     const void* logits;
     int64_t rows, ld;
@@ -130,6 +136,7 @@ struct LpParams {
     int f32;
     f32x4_t* sums;   // [rows][splits] of a row's pieces: maximum and sums
     uint64_t* keys;  // [rows][splits][top]: their best values
+    LpSeqs seqs;
     int splits, piece;  // set by launch_lp: pieces per row, chunks of eight per piece
 };
 // Pieces of a row that a call works on apart and joins in a second launch; 1: none.
@@ -149,6 +156,7 @@ struct LpBwdParams {
     const float* dentropy;  // may be null: 0
     float scale;
     int f32;
+    LpSeqs seqs;
 };
 hipError_t launch_lp_bwd(const LpBwdParams& p, hipStream_t stream);
 

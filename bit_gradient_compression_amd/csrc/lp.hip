@@ -82,6 +82,9 @@ __device__ __forceinline__ u32x4 load16_for(const void* p) {
     else return load16(p);
 }
 
+// The sequence of a row; rows of more than one are fewer than 2^32.
+__device__ __forceinline__ int64_t seq_of(const LpSeqs& s, int64_t row) { return s.rows ? (uint32_t)row / s.rows : 0u; }
+
 // Values of a chunk, minus infinity past the row's end.
 template <typename T>
 struct LpChunk;
@@ -242,9 +245,10 @@ __device__ __forceinline__ void write_row(const LpParams& p, int64_t row, const 
 }
 template <typename T>
 __device__ __forceinline__ float target_logit(const LpParams& p, int64_t row, int64_t& target) {
-    target = p.targets[row];
+    const int64_t seq = seq_of(p.seqs, row);
+    target = p.targets[row + seq * p.seqs.targets];
     if (target < 0 || target >= p.vocab) return 0.0f;
-    const T* x = (const T*)p.logits + row * p.ld + target;
+    const T* x = (const T*)p.logits + row * p.ld + seq * p.seqs.logits + target;
     if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)*x << 16);
     else return *x;
 }
@@ -272,7 +276,7 @@ __global__ __launch_bounds__(THREADS) void lp_kernel(const LpParams p, int64_t r
         last = min(last, first + p.piece);
     }
     const int tid = threadIdx.x;
-    const T* x = (const T*)p.logits + row * p.ld;
+    const T* x = (const T*)p.logits + row * p.ld + seq_of(p.seqs, row) * p.seqs.logits;
     const float c = p.scale * kLog2e;
     if constexpr (TOP) {
         if (tid == 0) {
@@ -520,11 +524,12 @@ __global__ __launch_bounds__(64) void lp_bwd_kernel(const LpBwdParams p, int64_t
     const uint32_t g = (uint32_t)xcd_remap<kXcds, 128>(blockIdx.x, gridDim.x), r = g / segs;
     const int64_t row = row0 + r;
     const int base = (int)(g - r * segs) * kLpBwdTile;
-    const T* x = (const T*)p.logits + row * p.ld + base;
-    T* dx = (T*)p.dlogits + row * p.dld + base;
+    const int64_t seq = seq_of(p.seqs, row);
+    const T* x = (const T*)p.logits + row * p.ld + seq * p.seqs.logits + base;
+    T* dx = (T*)p.dlogits + row * p.dld + seq * p.seqs.dlogits + base;
     const int cols = p.vocab - base;  // of this segment and what follows
     const float m = p.stats[2 * row], s = p.stats[2 * row + 1];
-    const int64_t target = p.targets ? p.targets[row] : -1;
+    const int64_t target = p.targets ? p.targets[row + seq * p.seqs.targets] : -1;
     float dlp = p.dlogprob ? p.dlogprob[row] : 0.0f;
     if (target < 0) dlp = 0.0f;
     const bool past = p.dlogprob && target >= p.vocab;

@@ -43,7 +43,8 @@ SYMBOLS = ["loco_compensate_quantize", "loco_compensate_quantize_ex", "loco_dequ
            "loco_linear_weight_grad_workspace", "loco_adamw_table_bytes", "loco_adamw_plan",
            "loco_adamw", "loco_adamw_ex", "loco_adamw_state_plan", "loco_adamw_state_read", "loco_adamw_state_write",
            "loco_residual_norm", "loco_residual_norm_backward", "loco_residual_norm_backward_workspace",
-           "loco_token_logprobs", "loco_token_logprobs_workspace", "loco_token_logprobs_backward"]
+           "loco_token_logprobs", "loco_token_logprobs_workspace", "loco_token_logprobs_backward",
+           "loco_token_logprobs_ex", "loco_token_logprobs_backward_ex"]
 
 
 class LocoError(RuntimeError):
@@ -167,7 +168,11 @@ def load(path: str | None = None):
                                                   f32, ptr, ptr, ptr, ptr, ptr, i32, ptr, i64, ptr]),
             ("loco_residual_norm_backward_workspace", i64, [i64, i64]),
             ("loco_token_logprobs", i32, [ptr, i32, i64, i64, i64, ptr, f32, ptr, ptr, ptr, i32, ptr, ptr, ptr, i64, ptr]),
+            ("loco_token_logprobs_ex", i32, [ptr, i32, i64, i64, i64, i64, i64, ptr, i64, f32, ptr, ptr, ptr, i32, ptr, ptr,
+                                             ptr, i64, ptr]),
             ("loco_token_logprobs_workspace", i64, [i64, i64, i32]),
+            ("loco_token_logprobs_backward_ex", i32, [ptr, i32, i64, i64, i64, i64, i64, ptr, i64, f32, ptr, ptr, ptr, ptr,
+                                                      ptr, i64, i64, ptr]),
             ("loco_token_logprobs_backward", i32, [ptr, i32, i64, i64, i64, ptr, f32, ptr, ptr, ptr, ptr, ptr, i64, ptr]),
             ("loco_adamw_table_bytes", i64, [i32]),
             ("loco_adamw_plan", i32, [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32, i32, ptr, i64,
@@ -726,23 +731,67 @@ def loco_residual_norm_backward_workspace(rows: int, cols: int) -> int:
 
 # -- log probabilities of tokens ----------------------------------------------------------------
 
+def _runs(shape, strides, what):
+    """[(n, step)] of leading dimensions, outermost first, those of one step merged: at most two."""
+    runs = []
+    for n, s in zip(shape, strides):
+        if n == 1:
+            continue
+        if runs and runs[-1][1] == n * s:
+            runs[-1] = (runs[-1][0] * n, s)
+        else:
+            runs.append((n, s))
+    if len(runs) > 2:
+        raise ValueError(f"{what}: rows must be one step apart, or sequences of such rows be")
+    return runs
+
+
 def _logits(t, what):
-    """(rows, vocab, elements from row to row) of a tensor whose last dimension is the vocabulary: the
-    rows, of one or more leading dimensions, lie one such step apart, each of them in one piece."""
+    """(rows, vocab, runs) of a tensor whose last dimension is the vocabulary, each row in one piece; runs as _runs
+    gives them, None where the rows follow one another."""
     rows, vocab = _rows_cols(t, what, _FLOATS)
     if rows <= 1 or vocab == 0 or t.is_contiguous():
         if vocab > 1 and t.stride(-1) != 1:
             raise ValueError(f"{what}: a row must be contiguous")
-        return rows, vocab, vocab
-    lead = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
-    ld = lead[-1][1]
-    apart = all(a[1] == b[0] * b[1] for a, b in zip(lead, lead[1:]))
-    if not apart or ld < vocab or (vocab > 1 and t.stride(-1) != 1):
+        return rows, vocab, None
+    runs = _runs(t.shape[:-1], t.stride()[:-1], what)
+    ld = runs[-1][1]
+    if ld < vocab or (vocab > 1 and t.stride(-1) != 1):
         raise ValueError(f"{what}: rows must be contiguous and one step of at least {vocab} elements apart")
-    return rows, vocab, ld
+    if len(runs) == 2 and runs[0][1] < (runs[1][0] - 1) * ld + vocab:
+        raise ValueError(f"{what}: sequences must be as far apart as their rows reach")
+    return rows, vocab, runs
+
+
+def _targets(t, rows):
+    """The runs of targets that do not follow one another; None for one."""
+    if rows <= 1:
+        return None
+    runs = _runs(t.shape, t.stride(), "targets")
+    if len(runs) == 1:  # one target of each sequence
+        runs.append((1, 1))
+    if runs[-1][1] != 1 or (len(runs) == 2 and runs[0][1] < runs[1][0]):
+        raise ValueError("targets must be contiguous, or sequences of them be")
+    return runs
+
+
+def _sequences(rows, *all_runs):
+    """(sequences, rows of each, [(step from row to row, from sequence to sequence)]) for each step from row to row of
+    buffers that follow one another (an int) or runs."""
+    inner = {r[1][0] for r in all_runs if type(r) is not int and len(r) == 2}
+    if len(inner) > 1:
+        raise ValueError(f"logits, dlogits and targets have sequences of {' and '.join(map(str, sorted(inner)))} rows")
+    n = inner.pop() if inner else rows
+    steps = []
+    for r in all_runs:
+        ld = r if type(r) is int else r[-1][1]
+        steps.append((ld, r[0][1] if type(r) is not int and len(r) == 2 else n * ld))
+    return (rows // n if n else 1), n, steps
 
 
 def _strided_ptr(t, dev):
+    if t is None:
+        return None
     d = t.get_device()
     if d != dev:
         if d < 0:
@@ -768,9 +817,10 @@ def loco_token_logprobs(logits, targets=None, *, logprob=None, entropy=None, sta
     alternatives, top_ids (int32) and top_logprobs (float32), whose last dimension says how many (up to
     LOCO_MAX_TOP), ties to the lower index.  stats (float32, two per row: the largest logit and the
     sum of exp(scale * (logit - it))) is for the backward pass.  Each output is optional.  logits may be a
-    slice of wider rows.  workspace: a tensor of token_logprobs_workspace(rows, vocab, top) bytes."""
+    slice of wider rows, or of the rows of each sequence, and targets too: logits[:, :-1] with ids[:, 1:].
+    workspace: a tensor of token_logprobs_workspace(rows, vocab, top) bytes."""
     dev = _device()
-    rows, vocab, ld = _logits(logits, "logits")
+    rows, vocab, runs = _logits(logits, "logits")
     like = logits.shape
     _row_values(targets, like, rows, "targets", _I64)
     _row_values(logprob, like, rows, "logprob")
@@ -783,10 +833,14 @@ def loco_token_logprobs(logits, targets=None, *, logprob=None, entropy=None, sta
         top = top_ids.shape[-1]
         _matrix(top_ids, like, rows, top, "top_ids", _I32)
         _matrix(top_logprobs, like, rows, top, "top_logprobs", _F32)
-    st = (_lib or load()).loco_token_logprobs(
-        _strided_ptr(logits, dev), _CODES[logits.dtype], rows, vocab, ld, _ptr(targets, dev), scale, _ptr(logprob, dev),
-        _ptr(entropy, dev), _ptr(stats, dev), top, _ptr(top_ids, dev), _ptr(top_logprobs, dev), _ptr(workspace, dev),
-        _nbytes(workspace), _stream(stream, dev))
+    truns = None if targets is None or targets.is_contiguous() else _targets(targets, rows)
+    seqs, n, ld, seq_ld, target_ld = 1, rows, vocab, 0, 0
+    if runs is not None or truns is not None:
+        seqs, n, ((ld, seq_ld), (_, target_ld)) = _sequences(rows, runs or vocab, truns or 1)
+    st = (_lib or load()).loco_token_logprobs_ex(
+        _strided_ptr(logits, dev), _CODES[logits.dtype], seqs, n, vocab, ld, seq_ld, _strided_ptr(targets, dev), target_ld,
+        scale, _ptr(logprob, dev), _ptr(entropy, dev), _ptr(stats, dev), top, _ptr(top_ids, dev), _ptr(top_logprobs, dev),
+        _ptr(workspace, dev), _nbytes(workspace), _stream(stream, dev))
     _check("loco_token_logprobs", st)
 
 
@@ -798,11 +852,12 @@ def loco_token_logprobs_backward(logits, targets, stats, *, dlogits, dlogprob=No
                                  scale: float = 1.0, stream=None) -> None:
     """dlogits = the gradient of sum(dlogprob * logprob + dentropy * entropy), with stats and entropy as
     loco_token_logprobs wrote them (entropy is needed with dentropy only).  One of dlogprob and dentropy
-    may be None.  dlogits has the type and shape of logits, and may be logits itself."""
+    may be None.  dlogits has the type and shape of logits, and may be logits itself; each may be a slice as in
+    loco_token_logprobs."""
     dev = _device()
-    rows, vocab, ld = _logits(logits, "logits")
+    rows, vocab, runs = _logits(logits, "logits")
     like = logits.shape
-    drows, dvocab, dld = _logits(dlogits, "dlogits")
+    drows, dvocab, druns = _logits(dlogits, "dlogits")
     if (drows, dvocab) != (rows, vocab) or not _same_rows(tuple(dlogits.shape[:-1]), tuple(like[:-1])):
         raise ValueError(f"dlogits has the shape {tuple(dlogits.shape)}; the call's is {tuple(like)}")
     if dlogits.dtype != logits.dtype:
@@ -811,10 +866,14 @@ def loco_token_logprobs_backward(logits, targets, stats, *, dlogits, dlogprob=No
     _matrix(stats, like, rows, 2, "stats", _F32)
     for t, what in ((dlogprob, "dlogprob"), (entropy, "entropy"), (dentropy, "dentropy")):
         _row_values(t, like, rows, what)
-    st = (_lib or load()).loco_token_logprobs_backward(
-        _strided_ptr(logits, dev), _CODES[logits.dtype], rows, vocab, ld, _ptr(targets, dev), scale, _ptr(stats, dev),
-        _ptr(entropy, dev), _ptr(dlogprob, dev), _ptr(dentropy, dev), _strided_ptr(dlogits, dev), dld,
-        _stream(stream, dev))
+    truns = None if targets is None or targets.is_contiguous() else _targets(targets, rows)
+    seqs, n, ld, seq_ld, dld, dseq_ld, target_ld = 1, rows, vocab, 0, vocab, 0, 0
+    if runs is not None or druns is not None or truns is not None:
+        seqs, n, ((ld, seq_ld), (dld, dseq_ld), (_, target_ld)) = _sequences(rows, runs or vocab, druns or vocab, truns or 1)
+    st = (_lib or load()).loco_token_logprobs_backward_ex(
+        _strided_ptr(logits, dev), _CODES[logits.dtype], seqs, n, vocab, ld, seq_ld, _strided_ptr(targets, dev), target_ld,
+        scale, _ptr(stats, dev), _ptr(entropy, dev), _ptr(dlogprob, dev), _ptr(dentropy, dev), _strided_ptr(dlogits, dev),
+        dld, dseq_ld, _stream(stream, dev))
     _check("loco_token_logprobs_backward", st)
 
 

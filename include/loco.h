@@ -55,7 +55,7 @@ typedef enum { LOCO_F32 = 0, LOCO_BF16 = 1, LOCO_I8 = 2 } loco_dtype_t;
 #define LOCO_OK 0
 #define LOCO_ERR_INVALID (-1)     /* bad size, bits, block, k, chunk, beta, scale, dtype,
                                      peer count < 1, null pointer, or overlapping buffers */
-#define LOCO_ERR_ALIGN (-2)       /* a device pointer is not 16-byte aligned */
+#define LOCO_ERR_ALIGN (-2)       /* a device pointer is not aligned, to 16 bytes unless its call says otherwise */
 #define LOCO_ERR_UNSUPPORTED (-3) /* valid but not built: bits not in {2,4,8}, block not
                                      in {64,128,256,512}, chunk not in
                                      {256,512,1024,2048,4096}, more than LOCO_MAX_PEERS
@@ -533,6 +533,28 @@ int loco_token_logprobs_backward(const void* logits, loco_dtype_t dtype, int64_t
                                  int64_t ld, const int64_t* targets, float scale, const float* stats,
                                  const float* entropy, const float* dlogprob, const float* dentropy,
                                  void* dlogits, int64_t dld, void* stream);
+
+/*
+ * loco_token_logprobs_ex, loco_token_logprobs_backward_ex - the same of seqs sequences of `rows` rows each, where the
+ * last rows of a sequence, or other elements, lie between it and the next: logits[:, :-1] with targets ids[:, 1:].
+ *   seq_ld, dseq_ld  elements from one sequence's first row of logits, of dlogits, to the next one's: at least
+ *                    (rows - 1) * ld + vocab
+ *   target_ld        the same of targets: at least rows.  All other buffers hold seqs * rows rows without gaps
+ *   dlogits          may be logits itself with dld = ld and dseq_ld = seq_ld
+ * With one sequence these steps are ignored; more may have 2^32 - 1 rows in all (LOCO_ERR_UNSUPPORTED beyond).  The
+ * workspace is that of seqs * rows rows, and the only buffer to be 16-byte aligned: the others need their elements'
+ * alignment (8 bytes for targets, 4 for stats), so that each may start anywhere in a tensor.
+ */
+int loco_token_logprobs_ex(const void* logits, loco_dtype_t dtype, int64_t seqs, int64_t rows, int64_t vocab,
+                           int64_t ld, int64_t seq_ld, const int64_t* targets, int64_t target_ld,
+                           float scale, float* logprob, float* entropy, float* stats, int top,
+                           int32_t* top_ids, float* top_logprobs, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+int loco_token_logprobs_backward_ex(const void* logits, loco_dtype_t dtype, int64_t seqs, int64_t rows,
+                                    int64_t vocab, int64_t ld, int64_t seq_ld, const int64_t* targets,
+                                    int64_t target_ld, float scale, const float* stats,
+                                    const float* entropy, const float* dlogprob, const float* dentropy,
+                                    void* dlogits, int64_t dld, int64_t dseq_ld, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * AdamW over many tensors at once, with states in fp32 or in 8 bits: the step of the parameters
