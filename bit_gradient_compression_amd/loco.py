@@ -884,6 +884,12 @@ def _keep(t):
     return None if t is None else t.detach()
 
 
+def _alike(t, like, what):
+    """t, of as many elements as the shape `like`, must be flat or have that shape: another one counts them in another order."""
+    if t is not None and not _same_rows(tuple(t.shape), tuple(like)):
+        raise ValueError(f"{what} has the shape {tuple(t.shape)}, not {tuple(like)}")
+
+
 def _state(state, n, nb, what):
     """(codes or values, exps or None), checked, and the bits of the state."""
     if isinstance(state, torch.Tensor):
@@ -938,7 +944,7 @@ class AdamwTensors:
     step.  tensors: an iterable of (param, grad, m, v[, param_bf16[, weight_decay]]): param
     float32 or bfloat16, grad float32 or bfloat16, m and v float32, or in 8 bits (m: (codes
     float8_e4m3fn, exps uint8), v: (codes uint8, exps uint8), one exps byte per block); every
-    param, every grad and every state of one kind.  param_bf16 (or None) receives the bfloat16 copy
+    param, every grad and every state of one kind; grad and param_bf16 flat or of the param's shape.  param_bf16 (or None) receives the bfloat16 copy
     of a float32 param.  weight_decay is that of the tensors that do not give one.  The memory of
     the tensors is kept alive and must not be resized; later calls use it as it is now, on the
     device that is current now.  The description is on the device when the constructor returns; it
@@ -967,6 +973,8 @@ class AdamwTensors:
             if copy is not None and param.dtype != torch.float32:
                 raise TypeError(f"tensor {i}: param_bf16 goes with a float32 param")
             _sized(copy, n, f"tensor {i}: param_bf16", _BF)
+            _alike(grad, param.shape, f"tensor {i}: grad")
+            _alike(copy, param.shape, f"tensor {i}: param_bf16")
             parts = (param, grad, m, v, me, ve, copy)
             rows.append((*(_ptr(x, dev) for x in parts), n, weight_decay if decay is None else decay))
             keep.append(tuple(_keep(x) for x in parts))
