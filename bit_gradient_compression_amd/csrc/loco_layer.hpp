@@ -281,17 +281,26 @@ __device__ __forceinline__ void decode_codes(u32x2 w, uint32_t e, float (&v)[8])
     for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))) * step;
 }
 
-// ---- wave sums ----------------------------------------------------------------------
+// ---- sums of lanes --------------------------------------------------------------------
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over aligned groups of LANES (16, 32 or 64) lanes; every lane gets its group's.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
     v += __uint_as_float(dpp<0xB1>(__float_as_uint(v)));
     v += __uint_as_float(dpp<0x4E>(__float_as_uint(v)));
     v += __uint_as_float(dpp<0x141>(__float_as_uint(v)));
     v += __uint_as_float(dpp<0x140>(__float_as_uint(v)));
-    auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    if constexpr (LANES >= 32) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    if constexpr (LANES >= 64) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    return v;
 }
+
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
 }  // namespace loco

@@ -18,24 +18,6 @@ namespace loco {
 
 namespace {
 
-// Sum over aligned groups of LANES (16, 32 or 64) lanes; every lane gets its group's.
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v) {
-    v += __uint_as_float(dpp<0xB1>(__float_as_uint(v)));
-    v += __uint_as_float(dpp<0x4E>(__float_as_uint(v)));
-    v += __uint_as_float(dpp<0x141>(__float_as_uint(v)));
-    v += __uint_as_float(dpp<0x140>(__float_as_uint(v)));
-    if constexpr (LANES >= 32) {
-        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    }
-    if constexpr (LANES >= 64) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    }
-    return v;
-}
-
 // Sum over the LPT lanes of a row; every lane gets it.  `slot` alternates between calls so that one
 // barrier per call is enough.
 template <int LPT>
@@ -374,8 +356,6 @@ __device__ __forceinline__ Rsrc span_of(const void* p, int64_t at, uint32_t coun
     return buffer_rsrc((const T*)p + at, count * (uint32_t)sizeof(T));
 }
 
-constexpr int kStream = 2;  // a buffer access's nt bit
-
 // W consecutive elements, the first of them element i of a span, as they lie in memory.
 template <typename T, int W>
 struct Piece;
@@ -384,7 +364,7 @@ struct Piece<uint16_t, 8> {
     u32x4 w;
     template <bool ONCE = false>
     __device__ __forceinline__ void load(Rsrc r, uint32_t i) {
-        w = __builtin_amdgcn_raw_buffer_load_b128(r, i * 2, 0, ONCE ? kStream : 0);
+        w = __builtin_amdgcn_raw_buffer_load_b128(r, i * 2, 0, ONCE ? kLoadNt : 0);
     }
     __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(w, v); }
     // Makes the compiler unpack the values again, instead of keeping them from one phase of a row to the
@@ -399,8 +379,8 @@ struct Piece<float, 8> {
     u32x4 a, b;
     template <bool ONCE = false>
     __device__ __forceinline__ void load(Rsrc r, uint32_t i) {
-        a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, ONCE ? kStream : 0);
-        b = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4 + 16, 0, ONCE ? kStream : 0);
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4, 0, ONCE ? kLoadNt : 0);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, i * 4 + 16, 0, ONCE ? kLoadNt : 0);
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
