@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import warnings
 
@@ -948,7 +949,7 @@ class AdamwTensors:
     of a float32 param.  weight_decay is that of the tensors that do not give one.  The memory of
     the tensors is kept alive and must not be resized; later calls use it as it is now, on the
     device that is current now.  The description is on the device when the constructor returns; it
-    cannot be made while a graph is captured."""
+    cannot be made while a graph is captured, and has to live as long as a graph that steps it."""
 
     def __init__(self, tensors, *, block: int = 256, weight_decay: float = 0.0, stream=None, _wait: bool = True):
         self.device, self.block = _device(), block
@@ -1002,8 +1003,9 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
     captured graph repeats them.
 
     seed: an int, or an int64 tensor of one element.  With it, 8-bit states are rounded at random, by bits
-    that seed, step and the element's place decide, and follow their averages over a run.  A captured graph,
-    which repeats step, needs a tensor that the graph raises at each replay.  Without it they are rounded to
+    that seed, step and the element's place among the tensors decide, and follow their averages over a run.  It may
+    stay the same from step to step; ranks that hold copies of the tensors take the same one, other lists of tensors
+    another.  A captured graph, which repeats step, needs a tensor that the graph raises at each replay.  Without it they are rounded to
     nearest, for a single step: over many, a state that changes by less than half a step at once stays where
     it is.  Then beta2 has no default, and the first such step of a description warns."""
     if not isinstance(tensors, AdamwTensors):
@@ -1029,7 +1031,7 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
         _sized(seed, 1, "seed", _I64)
         rounding = ctypes.byref(AdamwRounding(0, _ptr(seed, dev)))
     else:
-        rounding = ctypes.byref(AdamwRounding(int(seed) & 0xFFFFFFFFFFFFFFFF, None))
+        rounding = ctypes.byref(AdamwRounding(operator.index(seed) & 0xFFFFFFFFFFFFFFFF, None))
     opt = AdamwOptions(lr, beta1, 0.999 if beta2 is None else beta2, eps, step)
     st = (_lib or load()).loco_adamw_ex(ctypes.byref(tensors.plan), ctypes.byref(opt), _ptr(grad_scale, dev), rounding,
                                         tensors._table.stream(stream, dev))

@@ -159,7 +159,7 @@ if not torch.cuda.is_available():
             loco.adamw(plan, step=1, lr=1e-3, seed=torch.zeros(1, dtype=torch.int64))
             assert (loco._lib.rounding.seed, loco._lib.rounding.counter) == (0, 4096)
         for bad, err in ((torch.zeros(2, dtype=torch.int64), ValueError), (torch.zeros(1, dtype=torch.int32), TypeError),
-                         (torch.zeros(1), TypeError)):
+                         (torch.zeros(1), TypeError), (1.5, TypeError), ("7", TypeError)):
             with pytest.raises(err):
                 loco.adamw(plan, step=1, lr=1e-3, seed=bad)
 
