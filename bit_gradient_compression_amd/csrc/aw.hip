@@ -19,8 +19,8 @@
 // any b1 and b2.  The random bits are a hash of the call's key and the element's position.
 //
 // Bound by HBM: every byte is moved once, 28 per element with fp32 weights and states, bf16 gradients and a bf16
-// copy, 16 with 8-bit states.  One LLaMA-7B layer (202 million elements) takes 904 - 974 us
-// (6.3 - 5.8 TB/s, from one card to the next) and 523 us (6.2 TB/s, at 89 instructions per element), 547 with random
+// copy, 16 with 8-bit states.  One LLaMA-7B layer (202 million elements) takes 906 - 1025 us
+// (6.3 - 5.5 TB/s, from one card to the next) and 523 us (6.2 TB/s, at 89 instructions per element), 547 with random
 // rounding.  200 tensors of 100 to 40000 elements take 9 us in either.
 
 #include "loco_device.hpp"
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(256) void aw_fill_kernel(const AwFillParams p) {
 
 // ---- the step ---------------------------------------------------------------------------
 
-// One-wave workgroups in runs of 128 on one XCD.  One LLaMA-7B layer (202 million elements), us with fp32 /
+// One-wave workgroups in runs of 128 on one XCD.  One LLaMA-7B layer, on one card, us with fp32 /
 // 8-bit states, the latter read back: 967 / 739, against 1019 / 750 in workgroups of four waves in dispatch
 // order, 992 / 763 in ones of one wave, 988 / 762 in runs of 64; two or four sub-tiles per wave are as fast here
 // and slower for small tensors (19.6 and 24.5 against 17.3 for 200 of them).

@@ -14,9 +14,12 @@
 // lanes' values, some k of them at or above it, are collected and ranked by value and index.
 //
 // Forward, a large call is bound by HBM and nearly as much by its 11 instructions per value: 8192 x 32000 in
-// bf16 84 us, 6.2 TB/s, with the vector units busy for 75 of them.  A few rows are bound by latency: a row of
-// 32000 with 8 alternatives takes 6.8 us, 3.5 more than nothing at all, 48 of 131071 with 20 take 12.8 and 3.9
-// for the join.  The gradient reads and writes each value once: 167 us for 8192 x 32000, 6.3 TB/s.
+// bf16 86 us, 6.1 TB/s, with the vector units busy for most of them; in fp32 176 us, 6.0 TB/s.  A few rows are
+// bound by latency: a row of 32000 with 8 alternatives takes 6.8 us, 3.5 more than nothing at all, 48 of 131071 with
+// 20 take 12.8 and 3.9 for the join; half of their LDS cycles are conflicts of the groups' layout.  The gradient
+// reads and writes each value once: 168 us for 8192 x 32000, 6.2 TB/s; in fp32 398 us, 5.3 TB/s.
+//
+// How a row is cut depends on the number of rows (below), and so do the order of its sums and their last bit.
 
 #include "loco_layer.hpp"
 #include "loco_step_internal.hpp"
@@ -498,7 +501,7 @@ const void* pick_lp_join(bool top) {
 // ---- backward -------------------------------------------------------------------------
 
 // One wave takes 1024 elements of a row; runs of 128 of them are on one XCD.  The stores stream past the
-// caches.  8192 x 32000 in bf16 / 333 x 50001 in fp32 (133 MB, whose half the caches hold), us: 169 / 25;
+// caches.  8192 x 32000 in bf16 / 333 x 50001 in fp32 (133 MB, whose half the caches hold), us in one run: 169 / 25;
 // four waves of 2048 elements each in dispatch order 192 / 25, with streaming stores 184 / 27, with streaming
 // loads too 180 / 32; this with streaming loads too 165 / 29, with 1536 elements 175 / 26.
 constexpr int kLpBwdChunks = 2;  // per lane

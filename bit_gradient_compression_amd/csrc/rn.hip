@@ -6,10 +6,15 @@
 //   dy  = rp (t - yh mean(t yh)),  t = s g dh' wp         (or dy = s g dh')
 //   dw = sum over rows of dout xh,  dwp = sum of s g dh' yh,  dg = s dh' u, summed for a gate of columns
 //
-// Both are bound by HBM: each element is read once and written once.  A row stays in registers from
-// its loads to its stores, through both of its sums; all sums are fp32.  16384 x 4096 in bf16 with a gate of
-// columns: forward 97 us (5.5 TB/s), 106 with the checkpoint (5.7 TB/s, vector units busy for 76 of them);
-// backward 151 us (5.4 TB/s, vector units busy for 68) and 5 for the join.
+// Both are bound by HBM: each element is read once and written once, but for fp32 rows past 8192 columns
+// backward, which read h, dout and y again for the phase that needs them.  A row stays in registers from
+// its loads to its stores, through both of its sums; all sums are fp32.
+//
+// Times here are of calls one after another whose matrices change from call to call, unless they say "the same
+// buffers": then the caches hold some of them.  16384 x 4096 in bf16 with a gate of columns: forward 97 us
+// (5.5 TB/s), 108 with the checkpoint (5.6 TB/s); backward 152 us (5.4 TB/s), 5 of them for the join.  Past 8192
+// columns they are further from the copy's 6.4 TB/s: 4096 x 11008 takes 81 us forward (4.4 TB/s: a third of
+// the lanes' chunks is empty) and 154 backward (3.5 TB/s: a row waits for its own loads).
 
 #include "loco_layer.hpp"
 #include "loco_step_internal.hpp"
@@ -45,9 +50,9 @@ __device__ __forceinline__ void fill(float (&v)[8], float x) {
 // Where a lane's chunk lies in a row: `valid` elements, 0 to 8, from column c on.  WHOLE: all of a chunk or
 // nothing.  Else a chunk of which less than all exists is read as the row's last eight elements (`at`), of which
 // `shift` are dropped when they are there: element by element, or in parts that are put together where they are
-// loaded, one matrix waited for the one before it (16384 x 4095 in bf16 with a checkpoint 236 and 176 us, so
-// 149; 8192 x 4095 in fp32 109, 114 and 107; only a last chunk alone in its wave is slower, 4097 in fp32 116, 117
-// and 136).
+// loaded, one matrix waited for the one before it (16384 x 4095 in bf16 with a checkpoint, the same buffers, 236
+// and 176 us, so 149; 8192 x 4095 in fp32 109, 114 and 107; only a last chunk alone in its wave is slower, 4097
+// in fp32 116, 117 and 136).
 struct Place {
     int c, at, valid, shift;
 };
@@ -816,7 +821,7 @@ __global__ __launch_bounds__(1024) void rn_bwd_join_kernel(const RnBwdParams p, 
 struct RnBwdShape {
     int lpt, waves, groups;  // groups: the workgroups that are at work at once
 };
-// Two rows a workgroup from 2049 to 4096 columns.  16384 x 4096 in bf16 with a gate of columns, without one, with
+// Two rows a workgroup from 2049 to 4096 columns.  Without streaming, 16384 x 4096 in bf16 with a gate of columns, without one, with
 // one of elements, the norm alone, and 1024 rows, us: in one row of eight waves, 512 at once, 163, 161, 218, 81
 // and 22.9; in two, 256 at once, 155, 154, 205, 78 and 20.3.
 RnBwdShape rn_bwd_shape(int64_t cols) {
@@ -866,8 +871,9 @@ hipError_t launch_rn(const RnParams& p, hipStream_t stream) {
     const int rpw = s.lpt <= 64 ? 256 / s.lpt : 1, threads = s.lpt <= 64 ? 256 : s.lpt;
     const void* k = p.cols % 8 == 0 ? (p.f32 ? pick_rn<float, true>(s) : pick_rn<uint16_t, true>(s))
                                     : (p.f32 ? pick_rn<float, false>(s) : pick_rn<uint16_t, false>(s));
-    // What is written.  us without / with, both norms and a gate of columns in bf16: 16384 x 4096 96 / 94, with the
-    // checkpoint 117 / 114, 8192 x 8192 110 / 106.  Smaller outputs the caches hold for what reads them next.
+    // What is written.  us without / with, both norms and a gate of columns in bf16: 16384 x 4096 98 / 97, with the
+    // checkpoint 109 / 108, 8192 x 8192 101 / 96; the same buffers 110 / 88, 115 / 97 and 101 / 80.  Smaller
+    // outputs the caches hold for what reads them next.
     const bool once = p.rows * p.cols * ((p.h ? 1 : 0) + (p.out ? 1 : 0)) * (p.f32 ? 4 : 2) >= kStreamBytes;
     for (int64_t row0 = 0; row0 < p.rows; row0 += kMaxGrid * rpw) {
         const int64_t rows = p.rows - row0 < kMaxGrid * rpw ? p.rows - row0 : kMaxGrid * rpw;
@@ -889,9 +895,10 @@ hipError_t launch_rn_bwd(const RnBwdParams& p, hipStream_t stream) {
     const RnBwdShape s = rn_bwd_shape(p.cols);
     const int64_t groups = rn_bwd_groups(p.rows, p.cols);
     const bool post = p.post_rstd || p.sums[1];  // without rows the sum is there without rstd
-    // What is read, in bf16.  Rows of 4096, again and again, us without / with: 4096 rows with a gate of columns
-    // 40 / 49, without one 37 / 43; 6144 62 / 64, 57 / 57; 8192 86 / 79, 85 / 71; 16384 154 / 143, 152 / 129.  In
-    // fp32, which reads each row when it is its turn, 8192 rows 165 / 174.
+    // What is read, in bf16.  Rows of 4096, us without / with, with a gate of columns, without one: 8192 rows 86 / 82
+    // and 84 / 80, 16384 155 / 152 and 155 / 147.  The same buffers: 4096 rows 40 / 49 and 37 / 43, 6144 62 / 64
+    // and 57 / 57, 8192 86 / 80 and 85 / 71, 16384 155 / 140 and 155 / 128.  In fp32, which reads each row when it is
+    // its turn, 8192 rows 165 / 174.
     const int matrices = (p.dout ? 2 : 0) + (p.dh ? 1 : 0) + (post || p.gate_kind != kGateNone ? 1 : 0) +
                          (p.gate_kind == kGateElement ? 1 : 0);
     const bool once = !p.f32 && p.rows * p.cols * matrices * 2 >= kStreamBytes;

@@ -490,6 +490,9 @@ int64_t loco_residual_norm_backward_workspace(int64_t rows, int64_t cols);
  * is its gradient.  A row of minus infinities only has the log probability minus infinity, the entropy 0
  * and the gradient 0; with a target past the vocabulary both are NaN, as in any row.  Minus infinity
  * elsewhere (a masked token) has the probability 0.
+ *
+ * The same call has the same bits.  The order of a row's sums depends on the number of rows of the call, so between
+ * calls of other numbers of rows the last bits of its log probabilities, entropy and stats may differ.
  * ------------------------------------------------------------------------------ */
 
 /* Largest number of alternatives. */
