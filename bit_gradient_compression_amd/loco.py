@@ -886,7 +886,8 @@ def _keep(t):
 
 
 def _alike(t, like, what):
-    """t, of as many elements as the shape `like`, must be flat or have that shape: another one counts them in another order."""
+    """t, of as many elements as the shape `like`, must be flat or have that shape: another shape counts
+    them in another order."""
     if t is not None and not _same_rows(tuple(t.shape), tuple(like)):
         raise ValueError(f"{what} has the shape {tuple(t.shape)}, not {tuple(like)}")
 
@@ -945,9 +946,9 @@ class AdamwTensors:
     step.  tensors: an iterable of (param, grad, m, v[, param_bf16[, weight_decay]]): param
     float32 or bfloat16, grad float32 or bfloat16, m and v float32, or in 8 bits (m: (codes
     float8_e4m3fn, exps uint8), v: (codes uint8, exps uint8), one exps byte per block); every
-    param, every grad and every state of one kind; grad and param_bf16 flat or of the param's shape.  param_bf16 (or None) receives the bfloat16 copy
-    of a float32 param.  weight_decay is that of the tensors that do not give one.  The memory of
-    the tensors is kept alive and must not be resized; later calls use it as it is now, on the
+    param, every grad and every state of one kind; grad and param_bf16 flat or of the param's
+    shape.  param_bf16 (or None) receives the bfloat16 copy of a float32 param.  weight_decay is that
+    of the tensors that do not give one.  The memory of the tensors is kept alive and must not be resized; later calls use it as it is now, on the
     device that is current now.  The description is on the device when the constructor returns; it
     cannot be made while a graph is captured, and has to live as long as a graph that steps it."""
 
@@ -1003,11 +1004,12 @@ def loco_adamw(tensors, *, step: int, lr: float, beta1: float = 0.9, beta2: floa
     captured graph repeats them.
 
     seed: an int, or an int64 tensor of one element.  With it, 8-bit states are rounded at random, by bits
-    that seed, step and the element's place among the tensors decide, and follow their averages over a run.  It may
-    stay the same from step to step; ranks that hold copies of the tensors take the same one, other lists of tensors
-    another.  A captured graph, which repeats step, needs a tensor that the graph raises at each replay.  Without it they are rounded to
-    nearest, for a single step: over many, a state that changes by less than half a step at once stays where
-    it is.  Then beta2 has no default, and the first such step of a description warns."""
+    that seed, step and the element's place among the tensors decide, and follow their averages over a
+    run.  It may stay the same from step to step; ranks that hold copies of the tensors take the same
+    one, other lists of tensors another.  A captured graph, which repeats step, needs a tensor that the
+    graph raises at each replay.  Without a seed 8-bit states are rounded to nearest, for a single step:
+    over many, a state that changes by less than half a step of its code at once stays where it is.
+    Then beta2 has no default, and the first such step of a description warns."""
     if not isinstance(tensors, AdamwTensors):
         tensors = AdamwTensors(tensors, block=256 if block is None else block, weight_decay=weight_decay or 0.0,
                                stream=stream, _wait=False)
